@@ -33,7 +33,9 @@ DEVERR_PRECONDITION = 0x20
 EXPORTS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_decode_step", "kda_decode_multi",
            "kda_chunk_fwd_checkpoints", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_get_device_error",
            "kda_status_string", "kda_trace_enable", "kda_trace_collect", "kda_chunk_fwd_noalloc",
-           "kda_noalloc_scratch_bytes", "kda_chunk_fwd_segment_map", "kda_state_compose")
+           "kda_noalloc_scratch_bytes", "kda_chunk_fwd_segment_map", "kda_state_compose", "kda_rmsnorm_quant",
+           "kda_matmul_fp8", "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
+           "kda_linear_decode_step")
 
 
 class KdaError(RuntimeError):
@@ -84,6 +86,17 @@ def load_library(path: Optional[str] = None):
         lib.kda_chunk_fwd_segment_map.restype = I
         lib.kda_state_compose.argtypes = [P, P, P, P, I, I, I, I, P]
         lib.kda_state_compose.restype = I
+        F = ctypes.c_float
+        lib.kda_rmsnorm_quant.argtypes = [P, P, P, P, P, P, I64, I, F, I, P]
+        lib.kda_rmsnorm_quant.restype = I
+        lib.kda_matmul_fp8.argtypes = [P, P, P, P, P, I64, I, I, I, P]
+        lib.kda_matmul_fp8.restype = I
+        lib.kda_linear_chunk_fwd_workspace_size.argtypes = [I, I64, I, I, I, I]
+        lib.kda_linear_chunk_fwd_workspace_size.restype = SZ
+        lib.kda_linear_chunk_fwd.argtypes = [P, P, P, P, I, P, P, P, P, I, I64, I, I, I, I64, I64, I64, F, I, I, P, SZ, P]
+        lib.kda_linear_chunk_fwd.restype = I
+        lib.kda_linear_decode_step.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I64, I64, I64, F, I, I, P]
+        lib.kda_linear_decode_step.restype = I
         lib.kda_noalloc_scratch_bytes.argtypes = []
         lib.kda_noalloc_scratch_bytes.restype = SZ
         lib.kda_trace_enable.argtypes = [I]
@@ -481,4 +494,173 @@ def kda_state_compose(P, b, S0=None, out=None):
     st = lib.kda_state_compose(_ptr(P), _ptr(b), _ptr(S0), _ptr(out), n, H, dk, dv, _stream(dev))
     if st != 0:
         raise KdaError("kda_state_compose", st)
+    return out
+
+
+# ------------------------------------------------------------- operators around a recurrent layer
+_BLOCK = 128  # values that share a scale
+
+
+def kda_rmsnorm_quant(x, weight=None, residual=None, *, eps: float = 1e-6, y=None, y_scale=None, residual_out=None):
+    """RMS norm of x (+ residual) with e4m3 output and one scale for each 128 values.  x, residual:
+    [rows, D], bf16 or fp32; weight: fp32 [D] or None.  residual_out may be the residual (in place).
+    Returns (y [rows, D] float8_e4m3fn, y_scale [rows, ceil(D / 128)] fp32, x + residual or None)."""
+    lib = load_library()
+    dev = x.device
+    rows, D = x.shape
+    code = _dtype_code(x)
+    _check(x, "x", device=dev)
+    _check(residual, "residual", x.dtype, (rows, D), dev)
+    _check(weight, "weight", torch.float32, (D,), dev)
+    if y is None:
+        y = torch.empty(rows, D, device=dev, dtype=torch.float8_e4m3fn)
+    else:
+        _check(y, "y", torch.float8_e4m3fn, (rows, D), dev)
+    blocks = (D + _BLOCK - 1) // _BLOCK
+    if y_scale is None:
+        y_scale = torch.empty(rows, blocks, device=dev, dtype=torch.float32)
+    else:
+        _check(y_scale, "y_scale", torch.float32, (rows, blocks), dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    elif residual_out is None:
+        residual_out = torch.empty_like(x)
+    else:
+        _check(residual_out, "residual_out", x.dtype, (rows, D), dev)
+    st = lib.kda_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(y_scale), rows,
+                               D, float(eps), code, _stream(dev))
+    if st != 0:
+        raise KdaError("kda_rmsnorm_quant", st)
+    return y, y_scale, residual_out
+
+
+def kda_matmul_fp8(a, a_scale, b, b_scale, out=None, *, out_dtype: Optional[torch.dtype] = None):
+    """a @ b.T of e4m3 rows with block scales.  a: [M, K] float8_e4m3fn with a_scale [M, ceil(K / 128)];
+    b: [N, K] float8_e4m3fn (a weight) with b_scale [ceil(N / 128), ceil(K / 128)], scales fp32.
+    Returns out [M, N] (out_dtype: bf16 unless given; bf16 or fp32)."""
+    lib = load_library()
+    dev = a.device
+    M, K = a.shape
+    N = b.shape[0]
+    kb, nb = (K + _BLOCK - 1) // _BLOCK, (N + _BLOCK - 1) // _BLOCK
+    _check(a, "a", torch.float8_e4m3fn, (M, K), dev)
+    _check(a_scale, "a_scale", torch.float32, (M, kb), dev)
+    _check(b, "b", torch.float8_e4m3fn, (N, K), dev)
+    _check(b_scale, "b_scale", torch.float32, (nb, kb), dev)
+    if out is None:
+        out = torch.empty(M, N, device=dev, dtype=out_dtype or torch.bfloat16)
+    else:
+        _check(out, "out", out_dtype, (M, N), dev)
+    st = lib.kda_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(out), M, N, K, _dtype_code(out),
+                            _stream(dev))
+    if st != 0:
+        raise KdaError("kda_matmul_fp8", st)
+    return out
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """Checks [tokens, H, d] whose heads are dense and whose tokens may lie further apart; returns the
+    distance of two tokens in elements."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, H, d = shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else H * d
+
+
+def _head_decay(g: torch.Tensor, rows: int, H: int, device) -> int:
+    """1 if g is [rows, H] (a decay per token), 0 if it is [H]."""
+    per_token = g.dim() == 2
+    _check(g, "g", torch.float32, (rows, H) if per_token else (H,), device)
+    return int(per_token)
+
+
+def kda_linear_chunk_fwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
+                                        dtype: torch.dtype = torch.bfloat16) -> int:
+    code = KDA_DTYPE_BF16 if dtype == torch.bfloat16 else KDA_DTYPE_FP32
+    return int(load_library().kda_linear_chunk_fwd_workspace_size(B, T, H, dk, dv, code))
+
+
+def kda_linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None, *, B: Optional[int] = None,
+                         scale: float = 1.0, workspace=None, output_final_state: bool = True,
+                         out_dtype: Optional[torch.dtype] = None):
+    """Linear attention with one decay per head, whole sequences.  q, k: [T_tot, H, dk]; v:
+    [T_tot, H, dv] (tokens may be strided, e.g. parts of one projection's rows); g: log decay, fp32,
+    [T_tot, H] or one constant per head [H]; h0: [B, H, dk, dv] fp32 or None; cu_seqlens: int32 [B+1]
+    on the device or None (then B sequences of T_tot/B tokens).
+    Returns (out [T_tot, H, dv], hT [B, H, dk, dv] or None)."""
+    lib = load_library()
+    dev = q.device
+    T_tot, H, dk = q.shape
+    dv = v.shape[2]
+    dt = q.dtype
+    code = _dtype_code(q)
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, device=dev)
+        nB = cu_seqlens.numel() - 1
+        if B is not None and B != nB:
+            raise ValueError("B does not match cu_seqlens")
+        B, T_arg = nB, T_tot
+    else:
+        B = 1 if B is None else B
+        if T_tot % B:
+            raise ValueError("without cu_seqlens, T_tot must be a multiple of B")
+        T_arg = T_tot // B
+    qs = _token_rows(q, "q", dt, (T_tot, H, dk), dev)
+    ks = _token_rows(k, "k", dt, (T_tot, H, dk), dev)
+    vs = _token_rows(v, "v", dt, (T_tot, H, dv), dev)
+    per_token = _head_decay(g, T_tot, H, dev)
+    _check(h0, "h0", torch.float32, (B, H, dk, dv), dev)
+    if out is None:
+        out = torch.empty(T_tot, H, dv, device=dev, dtype=out_dtype or dt)
+    _check(out, "out", out_dtype, (T_tot, H, dv), dev)
+    if hT is None and output_final_state:
+        hT = torch.empty(B, H, dk, dv, device=dev, dtype=torch.float32)
+    _check(hT, "hT", torch.float32, (B, H, dk, dv), dev)
+    need = int(lib.kda_linear_chunk_fwd_workspace_size(B, T_arg, H, dk, dv, code))
+    if need == 0:
+        raise KdaError("kda_linear_chunk_fwd_workspace_size", 2)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+    _check(workspace, "workspace", torch.uint8, None, dev)
+    st = lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(h0), _ptr(cu_seqlens), _ptr(out),
+                                  _ptr(hT), B, T_arg, H, dk, dv, qs, ks, vs, float(scale), code, _dtype_code(out),
+                                  _ptr(workspace), workspace.numel(), _stream(dev))
+    if st != 0:
+        raise KdaError("kda_linear_chunk_fwd", st)
+    return out, hT
+
+
+def kda_linear_decode_step(q, k, v, g, state_pool, slot_idx, out=None, *, scale: float = 1.0,
+                           out_dtype: Optional[torch.dtype] = None):
+    """One token of linear attention per request.  q, k: [N, H, dk]; v: [N, H, dv] (rows may be
+    strided); g: log decay, fp32, [N, H] or one constant per head [H]; state_pool:
+    [num_slots, H, dk, dv] fp32 (updated in place); slot_idx: int32 [N].  Returns out [N, H, dv]."""
+    lib = load_library()
+    dev = q.device
+    N, H, dk = q.shape
+    dv = v.shape[2]
+    dt = q.dtype
+    code = _dtype_code(q)
+    num_slots = state_pool.shape[0]
+    qs = _token_rows(q, "q", dt, (N, H, dk), dev)
+    ks = _token_rows(k, "k", dt, (N, H, dk), dev)
+    vs = _token_rows(v, "v", dt, (N, H, dv), dev)
+    per_token = _head_decay(g, N, H, dev)
+    _check(state_pool, "state_pool", torch.float32, (num_slots, H, dk, dv), dev)
+    _check(slot_idx, "slot_idx", torch.int32, (N,), dev)
+    if out is None:
+        out = torch.empty(N, H, dv, device=dev, dtype=out_dtype or dt)
+    _check(out, "out", out_dtype, (N, H, dv), dev)
+    st = lib.kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(state_pool), _ptr(slot_idx),
+                                    _ptr(out), N, H, dk, dv, num_slots, qs, ks, vs, float(scale), code,
+                                    _dtype_code(out), _stream(dev))
+    if st != 0:
+        raise KdaError("kda_linear_decode_step", st)
     return out

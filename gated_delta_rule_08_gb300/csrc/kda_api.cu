@@ -99,6 +99,13 @@ size_t blob_bytes(kda_dtype dtype, int dk, int dv) {
 
 }  // namespace
 
+bool device_ready(unsigned int** err, bool* supported) {
+  int major = 0, minor = 0;
+  if (device_state(err, &major, &minor) != KDA_OK) return false;
+  *supported = major == 10 && minor == 3;  // built for sm_103a only
+  return true;
+}
+
 bool test_wait_timeout() {
   const char* e = getenv("KDA_TEST_WAIT_TIMEOUT");
   return e != nullptr && *e != '\0' && strcmp(e, "0") != 0;

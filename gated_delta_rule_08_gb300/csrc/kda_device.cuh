@@ -50,6 +50,14 @@ __device__ __forceinline__ int sequence_of_rank(int r, const int32_t* plan, cons
   return cu == nullptr ? r : plan[B + 2 + r];
 }
 
+// Whether cu[0..B] rises from 0 to T_tot without a step back.  All threads of the CTA take part, so
+// that every CTA finds the same answer from one round of loads and no kernel has to run before it.
+__device__ __forceinline__ bool offsets_ok(const int32_t* __restrict__ cu, int B, int64_t T_tot) {
+  bool bad = cu[0] != 0 || cu[B] != T_tot;
+  for (int i = threadIdx.x; i < B; i += blockDim.x) bad |= cu[i + 1] < cu[i];
+  return !__syncthreads_or(bad);
+}
+
 // Resolve a global chunk index into (sequence b, token start t0, valid rows n).
 // Without cu_seqlens: B sequences of T tokens each.  Returns false for a chunk
 // index beyond the last chunk (grid over-provisioning) or an invalid plan.

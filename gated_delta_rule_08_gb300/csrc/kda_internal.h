@@ -169,6 +169,83 @@ cudaError_t plan_launch(const int32_t* cu_seqlens, int B, int64_t T_tot, int32_t
 // decode (kda_decode.cu)
 cudaError_t decode_launch(const DecodeArgs& a, cudaStream_t stream);
 
+// ---- the operators around a recurrent layer (kda_layer_api.cu dispatches to them)
+
+// Error-word address of the current device and whether it is the compute capability this library is
+// built for; false if a CUDA query failed.
+bool device_ready(unsigned int** err, bool* supported);
+
+// Linear attention with one decay per head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+struct LinearArgs {
+  const void* q;              // token rows at q_stride / k_stride / v_stride elements, heads dense inside a row
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const float* g;             // [T_tot, H], or [H] for a constant decay
+  bool g_per_token;
+  const float* h0;            // may be null
+  const int32_t* cu_seqlens;  // may be null (equal lengths)
+  void* out;                  // [T_tot, H, dv] dense
+  float* hT;                  // may be null; may alias h0
+  int B;
+  int64_t T;                  // per-sequence length if cu_seqlens == null, else T_tot
+  int64_t T_tot;
+  int H, dk, dv;
+  float scale;
+  bool bf16, out_bf16;
+  void* workspace;
+  unsigned int* err;
+  bool give_up;
+};
+cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t stream);
+
+struct LinearStepArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const float* g;             // [N, H], or [H]
+  bool g_per_token;
+  float* state_pool;
+  const int32_t* slot_idx;
+  void* out;                  // [N, H, dv] dense
+  int N, H, dk, dv, num_slots;
+  float scale;
+  bool bf16, out_bf16;
+  unsigned int* err;
+};
+cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t stream);
+
+// z = x (+ residual); y = z / sqrt(mean z^2 + eps) w; per 128 values: scale = max|y| / 448, q = e4m3(y / scale)
+struct NormQuantArgs {
+  const void* x;
+  const void* residual;      // may be null
+  const float* weight;       // may be null (1)
+  void* residual_out;        // may be null
+  uint8_t* y;                // [rows, D] e4m3
+  float* y_scale;            // [rows, ceil(D / 128)]
+  int64_t rows;
+  int D;
+  float eps;
+  bool bf16;
+};
+cudaError_t rmsnorm_quant_launch(const NormQuantArgs& a, cudaStream_t stream);
+
+// out[m][n] = sum over 128-value blocks kb of a_scale[m][kb] b_scale[n / 128][kb] sum_k a[m][k] b[n][k]
+struct MatmulArgs {
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* b;
+  const float* b_scale;
+  void* out;
+  int64_t M;
+  int N, K;
+  bool out_bf16;
+  unsigned int* err;
+  bool give_up;
+};
+cudaError_t matmul_fp8_launch(const MatmulArgs& a, cudaStream_t stream);
+
 // Kernel tracing (kda_trace_enable): brackets internal launches with CUDA events.
 bool trace_enabled();
 void trace_begin(const char* name, cudaStream_t s);

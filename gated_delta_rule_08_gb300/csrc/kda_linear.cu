@@ -1,0 +1,217 @@
+// Linear attention with one decay per head: the recurrent forms.
+//
+// Per (sequence or request, head), state S in R^{dk x dv} (rows = key channels):
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// the KDA recurrence (section 2.2 Eq. 1) without the delta rule's erase and with a scalar decay.
+//
+// linear_recurrent_kernel: whole sequences in fp32, token by token.  Value columns are independent of
+// one another, so a CTA takes 16 of them for the whole sequence and keeps its dk x 16 slice of the
+// state in registers; a thread owns dk / 8 rows of one column.
+//
+// linear_step_kernel: one token per request on a pool of states, in place (section 13.9's pooled
+// layout).  It streams each state in and out once.
+#include "kda_device.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace {
+
+// ------------------------------------------------------------------------------ sequences
+constexpr int kCols = 16;  // value columns of a CTA
+constexpr int kTile = 16;  // tokens staged at a time
+constexpr int kRecThreads = 128;
+
+template <int DK, typename Tin, typename Tout>
+__global__ void __launch_bounds__(kRecThreads)
+linear_recurrent_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* __restrict__ g,
+                        int g_per_token, const float* h0, const int32_t* __restrict__ cu, Tout* __restrict__ out,
+                        float* hT, int B, int64_t T, int64_t T_tot, int H, int dv, float scale,
+                        unsigned int* __restrict__ err) {
+  constexpr int NI = DK / 32;  // groups of four rows of a thread
+  constexpr int kPer = kTile * DK / kRecThreads;
+  __shared__ __align__(16) float sk[kTile][DK], sq[kTile][DK];
+  __shared__ float sv[kTile][kCols], so[kTile][kCols], se[kTile];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slices = dv / kCols;
+  const int slice = blockIdx.x % slices, bh = blockIdx.x / slices, h = bh % H, b = bh / H;
+  int64_t t0 = (int64_t)b * T, n = T;
+  if (cu != nullptr) {
+    if (!offsets_ok(cu, B, T_tot)) {
+      if (tid == 0) atomicOr(err, KDA_DEVERR_BAD_SEQLENS);
+      return;
+    }
+    t0 = cu[b];
+    n = cu[b + 1] - cu[b];
+  }
+  const int rg = lane & 7, col = warp * 4 + (lane >> 3);
+  const int64_t soff = ((int64_t)b * H + h) * DK * dv + slice * kCols + col;
+  float s[NI][4];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = h0 ? h0[soff + (int64_t)(32 * i + 4 * rg + j) * dv] : 0.f;
+
+  for (int64_t c = 0; c < n; c += kTile) {
+    const int m = (int)(n - c < kTile ? n - c : kTile);
+    float rk[kPer], rq[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kRecThreads, r = e / DK, d = e % DK;
+      const bool in = r < m;
+      rk[i] = in ? to_f32(k[(t0 + c + r) * k_stride + h * DK + d]) : 0.f;
+      rq[i] = in ? to_f32(q[(t0 + c + r) * q_stride + h * DK + d]) : 0.f;
+    }
+    float rv[kTile * kCols / kRecThreads];
+#pragma unroll
+    for (int i = 0; i < kTile * kCols / kRecThreads; ++i) {
+      const int e = tid + i * kRecThreads, r = e / kCols, d = e % kCols;
+      rv[i] = r < m ? to_f32(v[(t0 + c + r) * v_stride + (int64_t)h * dv + slice * kCols + d]) : 0.f;
+    }
+    float re = 1.f;
+    if (tid < m) re = expf(g_per_token ? g[(t0 + c + tid) * H + h] : g[h]);
+    __syncthreads();  // the previous tile has been read and its outputs stored
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = tid + i * kRecThreads;
+      (&sk[0][0])[e] = rk[i];
+      (&sq[0][0])[e] = rq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kTile * kCols / kRecThreads; ++i) (&sv[0][0])[tid + i * kRecThreads] = rv[i];
+    if (tid < kTile) se[tid] = re;
+    __syncthreads();
+#pragma unroll 4
+    for (int t = 0; t < m; ++t) {
+      const float e = se[t], x = sv[t][col];
+      float acc = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&sk[t][32 * i + 4 * rg]);
+        const float4 q4 = *reinterpret_cast<const float4*>(&sq[t][32 * i + 4 * rg]);
+        s[i][0] = fmaf(k4.x, x, e * s[i][0]);
+        s[i][1] = fmaf(k4.y, x, e * s[i][1]);
+        s[i][2] = fmaf(k4.z, x, e * s[i][2]);
+        s[i][3] = fmaf(k4.w, x, e * s[i][3]);
+        acc = fmaf(q4.x, s[i][0], fmaf(q4.y, s[i][1], fmaf(q4.z, s[i][2], fmaf(q4.w, s[i][3], acc))));
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (rg == 0) so[t][col] = acc;
+    }
+    __syncthreads();
+    for (int e = tid; e < m * kCols; e += kRecThreads)
+      out[((t0 + c + e / kCols) * H + h) * dv + slice * kCols + e % kCols] = from_f32<Tout>(scale * (&so[0][0])[e]);
+  }
+  if (hT) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) hT[soff + (int64_t)(32 * i + 4 * rg + j) * dv] = s[i][j];
+  }
+}
+
+template <typename Tin, typename Tout>
+cudaError_t recurrent_typed(const LinearArgs& a, cudaStream_t st) {
+  const int64_t grid = (int64_t)a.B * a.H * (a.dv / kCols);
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  auto* kernel = a.dk == 64 ? linear_recurrent_kernel<64, Tin, Tout> : linear_recurrent_kernel<128, Tin, Tout>;
+  TraceScope ts("kda_linear_recurrent", st);
+  kernel<<<(unsigned)grid, kRecThreads, 0, st>>>(
+      static_cast<const Tin*>(a.q), static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v), a.q_stride, a.k_stride,
+      a.v_stride, a.g, a.g_per_token, a.h0, a.cu_seqlens, static_cast<Tout*>(a.out), a.hT, a.B, a.T, a.T_tot, a.H,
+      a.dv, a.scale, a.err);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------ one token
+constexpr int kStepThreads = 256;
+
+// CTA = (request, head, one of SPLIT groups of value columns).  A thread owns four columns of
+// DK / NG consecutive rows, so a warp's state accesses are whole 128-bit pieces of a row; the slice
+// stays in registers between load and store.
+template <int DK, int DV, int SPLIT, typename Tin, typename Tout>
+__global__ void __launch_bounds__(kStepThreads)
+linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, const float* __restrict__ g, int g_per_token,
+                   float* __restrict__ pool, const int32_t* __restrict__ slot_idx, Tout* __restrict__ out, int H,
+                   int num_slots, float scale, unsigned int* __restrict__ err) {
+  constexpr int DVS = DV / SPLIT;           // columns of this CTA
+  constexpr int TPR = DVS / 4;              // threads per row
+  constexpr int NG = kStepThreads / TPR;    // row groups
+  constexpr int RPG = DK / NG;              // rows per thread
+  static_assert(DK % NG == 0, "rows must split evenly");
+  __shared__ __align__(16) float sk[DK], sq[DK];
+  __shared__ __align__(16) float4 part[NG][TPR];
+
+  const int part_id = blockIdx.x % SPLIT, nh = blockIdx.x / SPLIT;
+  const int n = nh / H, h = nh - n * H;
+  const int tid = threadIdx.x, cg = tid % TPR, rg = tid / TPR;
+  const int slot = slot_idx[n];
+  if (slot < 0 || slot >= num_slots) {
+    if (tid == 0 && h == 0 && part_id == 0) atomicOr(err, KDA_DEVERR_BAD_SLOT);
+    return;
+  }
+  float* S = pool + ((int64_t)slot * H + h) * (DK * DV) + part_id * DVS + 4 * cg;
+  float4 s[RPG];
+#pragma unroll
+  for (int i = 0; i < RPG; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(S + (rg * RPG + i) * DV));
+
+  const float e = expf(g[g_per_token ? (int64_t)nh : h]);
+  for (int i = tid; i < DK; i += kStepThreads) {
+    sk[i] = to_f32(k[n * k_stride + h * DK + i]);
+    sq[i] = to_f32(q[n * q_stride + h * DK + i]);
+  }
+  float4 x;
+  {
+    const Tin* vp = v + n * v_stride + h * DV + part_id * DVS + 4 * cg;
+    x = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < RPG; ++i) {
+    const float kk = sk[rg * RPG + i], qq = sq[rg * RPG + i];
+    s[i] = f4_fma(kk, x, make_float4(e * s[i].x, e * s[i].y, e * s[i].z, e * s[i].w));
+    __stcs(reinterpret_cast<float4*>(S + (rg * RPG + i) * DV), s[i]);
+    acc = f4_fma(qq, s[i], acc);
+  }
+  part[rg][cg] = acc;
+  __syncthreads();
+  if (tid < DVS) {
+    float o = 0.f;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) o += reinterpret_cast<const float*>(part[i])[tid];
+    out[(int64_t)nh * DV + part_id * DVS + tid] = from_f32<Tout>(scale * o);
+  }
+}
+
+template <int DK, int DV, typename Tin, typename Tout>
+cudaError_t step_sized(const LinearStepArgs& a, cudaStream_t st) {
+  TraceScope ts("kda_linear_step", st);
+  linear_step_kernel<DK, DV, 1, Tin, Tout><<<(unsigned)(a.N * a.H), kStepThreads, 0, st>>>(
+      static_cast<const Tin*>(a.q), static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v), a.q_stride, a.k_stride,
+      a.v_stride, a.g, a.g_per_token, a.state_pool, a.slot_idx, static_cast<Tout*>(a.out), a.H, a.num_slots, a.scale,
+      a.err);
+  return cudaGetLastError();
+}
+template <typename Tin, typename Tout>
+cudaError_t step_typed(const LinearStepArgs& a, cudaStream_t st) {
+  if (a.dk == 64) return a.dv == 64 ? step_sized<64, 64, Tin, Tout>(a, st) : step_sized<64, 128, Tin, Tout>(a, st);
+  return a.dv == 64 ? step_sized<128, 64, Tin, Tout>(a, st) : step_sized<128, 128, Tin, Tout>(a, st);
+}
+
+}  // namespace
+
+cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t st) {
+  if (a.bf16)
+    return a.out_bf16 ? recurrent_typed<__nv_bfloat16, __nv_bfloat16>(a, st) : recurrent_typed<__nv_bfloat16, float>(a, st);
+  return a.out_bf16 ? recurrent_typed<float, __nv_bfloat16>(a, st) : recurrent_typed<float, float>(a, st);
+}
+
+cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t st) {
+  if (a.bf16) return a.out_bf16 ? step_typed<__nv_bfloat16, __nv_bfloat16>(a, st) : step_typed<__nv_bfloat16, float>(a, st);
+  return a.out_bf16 ? step_typed<float, __nv_bfloat16>(a, st) : step_typed<float, float>(a, st);
+}
+
+}  // namespace kda

@@ -21,7 +21,7 @@
  *     (an out-of-range slot index, inconsistent cu_seqlens, a device wait that ran out)
  *     are recorded in a per-device error word read by kda_get_device_error(); the
  *     affected rows are skipped, never trapped on.
- *   - dk, dv must each be 64 or 128 and C must be 64 (KDA_ERR_UNSUPPORTED otherwise).
+ *   - dk, dv must each be 64 or 128 and, where there is a C, C must be 64 (KDA_ERR_UNSUPPORTED otherwise).
  *   - `dtype` is the element type of q, k, v and the gate logits; `out_dtype` that of out
  *     (either may be bf16 or fp32).  bf16 prefill inputs with dk = dv = 128 run on the tcgen05
  *     tensor-core path.  fp32 inputs, and bf16 inputs with dk or dv = 64, run on a path with
@@ -241,6 +241,74 @@ kda_status kda_chunk_fwd_segment_map(const void* k, const void* v, const float* 
  * memory (KDA_ERR_INVALID_ARG otherwise). */
 kda_status kda_state_compose(const float* P, const float* b, const float* S0, float* S_out, int n, int H,
                              int dk, int dv, void* stream);
+
+/* ---- Operators around a recurrent layer (serving): the 8-bit projections and the plainer linear
+ * attention that models mix with KDA.  A layer runs kda_rmsnorm_quant, kda_matmul_fp8 (q, k, v),
+ * kda_linear_chunk_fwd or kda_linear_decode_step, kda_rmsnorm_quant and kda_matmul_fp8 (output). */
+
+/* RMS norm with the residual's addition and an 8-bit output with scales, for a row of D values
+ *   z = x + residual,  y_ = z / sqrt(mean(z^2) + eps) * weight
+ *   per block of 128 values (the last of a row may be shorter):
+ *     y_scale = max(max|y_|, 1e-30) / 448,   y = y_ / y_scale rounded to e4m3
+ * so that y * y_scale approximates y_.  Sum, norm and scales are fp32; the norm is taken on the
+ * unrounded sum z.  A NaN or infinity in a row reaches the row's scales.
+ *   x            : [rows, D] (dtype)
+ *   residual     : [rows, D] (dtype) or NULL (z = x)
+ *   weight       : [D] fp32 or NULL (1)
+ *   residual_out : [rows, D] (dtype) or NULL; z rounded to dtype.  May be residual or x (in place);
+ *                  needs a residual
+ *   y            : [rows, D] e4m3 (one byte per value), the layout kda_matmul_fp8 reads
+ *   y_scale      : [rows, ceil(D / 128)] fp32
+ *   D            : a multiple of 16, at most 32768 (KDA_ERR_UNSUPPORTED otherwise)
+ * All pointers 16-byte aligned (y_scale: 4). */
+kda_status kda_rmsnorm_quant(const void* x, const void* residual, const float* weight, void* residual_out,
+                             void* y, float* y_scale, int64_t rows, int D, float eps, kda_dtype dtype,
+                             void* stream);
+
+/* Matrix product of e4m3 rows with a scale for each block of 128 values:
+ *   out[m][n] = sum_kb a_scale[m][kb] * b_scale[n / 128][kb] * sum_{k in block kb} a[m][k] * b[n][k]
+ *   a       : [M, K] e4m3,  a_scale : [M, ceil(K / 128)] fp32          (activations)
+ *   b       : [N, K] e4m3,  b_scale : [ceil(N / 128), ceil(K / 128)] fp32  (a weight, 128 x 128 blocks)
+ *   out     : [M, N] (out_dtype), rounded once from fp32 sums
+ *   K       : a multiple of 16; K, M, N at most 2^22
+ * a, b and out 16-byte aligned, the scales 4-byte aligned.  M = 0 does nothing. */
+kda_status kda_matmul_fp8(const void* a, const float* a_scale, const void* b, const float* b_scale, void* out,
+                          int64_t M, int N, int K, kda_dtype out_dtype, void* stream);
+
+/* Linear attention with one decay per head over a packed batch of B variable-length sequences:
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * (section 2.2 Eq. 1 without the erase and with a scalar decay).
+ *   q, k      : [T_tot, H, dk] (dtype);  v : [T_tot, H, dv] (dtype).  A token's heads are dense; the
+ *               tokens lie q_stride / k_stride / v_stride elements apart (at least a dense row, a
+ *               multiple of 16 bytes), so that they can be parts of one projection's rows
+ *   g         : log decay, fp32: [T_tot, H] if g_per_token, else [H] (one constant per head).  g <= 0;
+ *               -infinity empties the state
+ *   h0        : [B, H, dk, dv] fp32 or NULL (zero);  hT : the same or NULL (not written); may alias h0
+ *   cu_seqlens: as for kda_chunk_fwd.  Offsets that do not rise from 0 to T_tot set
+ *               KDA_DEVERR_BAD_SEQLENS, and nothing is written
+ *   B         : at most 16384
+ *   out       : [T_tot, H, dv] (out_dtype), dense; must not overlap an input
+ *   T         : as for kda_chunk_fwd; T_tot below 2^31
+ *   workspace : at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte aligned
+ * q, k, v and the states have to be finite (a chunk's values meet in tensor-core products, where an
+ * infinity times a masked zero is NaN). */
+size_t kda_linear_chunk_fwd_workspace_size(int B, int64_t T, int H, int dk, int dv, kda_dtype dtype);
+kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_token,
+                                const float* h0, const int32_t* cu_seqlens, void* out, float* hT, int B,
+                                int64_t T, int H, int dk, int dv, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, float scale, kda_dtype dtype, kda_dtype out_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of linear attention for N requests on a pool of fp32 states, updated in place.
+ *   q, k, v   : [N, H, dk] / [N, H, dv] (dtype) with row strides as in kda_linear_chunk_fwd
+ *   g         : [N, H] if g_per_token, else [H], fp32
+ *   state_pool, slot_idx : as for kda_decode_step (distinct slots; a bad index sets
+ *               KDA_DEVERR_BAD_SLOT and leaves that request's rows and every slot untouched)
+ *   out       : [N, H, dv] (out_dtype), dense */
+kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const float* g, int g_per_token,
+                                  float* state_pool, const int32_t* slot_idx, void* out, int N, int H, int dk,
+                                  int dv, int num_slots, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  float scale, kda_dtype dtype, kda_dtype out_dtype, void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's error word into
  * *flags (KDA_DEVERR_* bits).  Returns KDA_OK, or KDA_ERR_CUDA if the sync failed. */
