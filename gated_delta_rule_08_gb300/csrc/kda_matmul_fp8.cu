@@ -1,67 +1,546 @@
-// Matrix product of e4m3 rows with a scale for each block of 128 values.
+// Matrix product of e4m3 rows with a scale for each block of 128 values, on the tcgen05 tensor cores.
 //
-//   out[m][n] = sum_kb a_scale[m][kb] b_scale[n / 128][kb] sum_{k in block kb} a[m][k] b[n][k]
-#include <cuda_fp8.h>
-
+//   out[m][n] = sum_kb a_scale[m][kb] b_scale[n / 128][kb] P_kb[m][n],  P_kb = sum_{k in block kb} a[m][k] b[n][k]
+//
+// The scales are free fp32 numbers, so each block's product P_kb (four MMAs of K = 32 into a fresh
+// TMEM accumulator) is read back and added in fp32 registers with its scale: the tensor cores sum 128
+// terms, registers the blocks.  TMEM holds several accumulators, so that the MMAs of a block run while
+// earlier ones are read.  A block of 128 e4m3 values is one 128-byte row: exactly one swizzle atom, one
+// stage of the ring that the TMA copies fill.  Rows and columns past the edges read as zeros.
+//
+// Two orientations:
+//  matmul_fp8_tall: 128 activation rows x 256 weight rows per tile, one CTA per SM walking over tiles;
+//    a thread owns one activation row and one 128-column block, whose scale is one number.
+//  matmul_fp8_flat: 128 weight rows x BN activation rows per tile, for few rows: the weight is then the
+//    operand with 128 rows and nothing is padded but the activations (to BN).  Bound by the weight's
+//    bytes, so the K blocks of a tile are split over the CTAs of a cluster, which add their partial
+//    sums through distributed shared memory in a fixed order.
 #include "kda_device.cuh"
 #include "kda_internal.h"
+#include "kda_tc_common.cuh"
+#include "kda_tma.h"
 
 namespace kda {
 namespace {
 
-constexpr int kTile = 64, kKs = 16;
+using namespace tcx;
+
+constexpr int kK = 128;  // values of a scale block = bytes of a stage's row
+
+// kind::f8f6f4: D fp32 (bit 4), A and B e4m3 (0), both K-major
+constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// One block of 128: P = A B^T, K = 32 bytes per MMA.
+__device__ __forceinline__ void mma_block(uint32_t d, const uint8_t* a, const uint8_t* b, uint32_t idesc) {
+  const uint64_t da = smem_desc_sw128(smem_u32(a), 16, 1024), db = smem_desc_sw128(smem_u32(b), 16, 1024);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma_f8(d, desc_add(da, 32 * i), desc_add(db, 32 * i), idesc, i > 0);
+}
+
+// Waits for this thread's TMEM loads; the values pass through, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_landed(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_landed(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+// acc (two fp32 lanes) += s * d
+__device__ __forceinline__ void fma2(uint64_t& acc, float s0, float s1, float d0, float d1) {
+  asm("{\n .reg .b64 rs, rd;\n mov.b64 rs, {%1, %2};\n mov.b64 rd, {%3, %4};\n fma.rn.f32x2 %0, rs, rd, %0;\n}"
+      : "+l"(acc)
+      : "f"(s0), "f"(s1), "f"(d0), "f"(d1));
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+// At the end of a CTA (all threads, after a barrier, so that the flag is final): if a wait ran out, the
+// copies and MMAs that may still be in flight are waited for, with a limit, before shared memory and TMEM
+// are given back.  Without an abort every MMA, and with it every copy, was waited for by its readers.
+template <int STAGES>
+__device__ __forceinline__ void drain_after_abort(volatile int* abort_flag, bool copier, bool multiplier, uint64_t* full,
+                                                  int64_t issued, uint64_t* bar_fin, unsigned int* err) {
+  if (!*abort_flag) return;
+  if (copier) {
+    for (int64_t l = issued > STAGES ? issued - STAGES : 0; l < issued; ++l)
+      mbar_wait(&full[l % STAGES], (uint32_t)((l / STAGES) & 1));
+    atomicOr(err, KDA_DEVERR_WAIT_TIMEOUT);
+  }
+  if (multiplier) {
+    mma_commit(bar_fin);
+    mbar_wait(bar_fin, 0);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------------------ many rows
+constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
+constexpr int kPromote = 256;  // warps 0-7: read accumulators, scale, store; warp 8 copies, warp 9 multiplies
+constexpr int kTallThreads = kPromote + 64;
+constexpr uint32_t kTallA = kTallM * kK, kTallStage = (kTallM + kTallN) * kK;
+constexpr uint32_t kTallBar = kTallStages * kTallStage;
+constexpr uint32_t kTallSmem = kTallBar + 256 + 1024;
+
+template <typename Tout, bool GIVEUP>
+__global__ void __launch_bounds__(kTallThreads, 1)
+matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
+                Tout* __restrict__ out, int M, int N, int nkb, int tiles_m, int tiles, unsigned int* __restrict__ err) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kTallBar);  // [stages] tiles landed
+  uint64_t* empty = full + kTallStages;                         // [stages] tiles read by their MMAs
+  uint64_t* acc_full = empty + kTallStages;                     // [2] accumulator complete
+  uint64_t* acc_empty = acc_full + 2;                           // [2] accumulator read
+  uint64_t* bar_fin = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_fin + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < kTallStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kPromote);
+    }
+    mbar_init(bar_fin, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int64_t issued = 0;  // stages whose copies warp 8 has started
+
+  if (warp == 8) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int m0 = tile % tiles_m * kTallM, n0 = tile / tiles_m * kTallN;
+        for (int kb = 0; kb < nkb && ok; ++kb, ++issued) {
+          const int s = (int)(issued % kTallStages);
+          if (issued >= kTallStages)
+            ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((issued / kTallStages - 1) & 1), abort_flag);
+          if (!ok) break;
+          uint8_t* st = sm + s * kTallStage;
+          mbar_arrive_expect_tx(&full[s], kTallStage);
+          tma_load_2d(st, &maps.a, kb * kK, m0, &full[s]);
+          tma_load_2d(st + kTallA, &maps.b, kb * kK, n0, &full[s]);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      int64_t it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
+          const int s = (int)(it % kTallStages), buf = (int)(it & 1);
+          ok = wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
+          if (ok && it >= 2) ok = wait_or_abort_t<GIVEUP>(&acc_empty[buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint8_t* st = sm + s * kTallStage;
+          mma_block(tmem + 256 * buf, st, st + kTallA, idesc_e4m3(kTallM, kTallN));
+          mma_commit(&empty[s]);
+          mma_commit(&acc_full[buf]);
+        }
+      }
+    }
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem_lane(tmem, warp) + 128 * half;
+    int64_t it = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + 128 * half;
+      // rows and blocks past the edges take the last one's scale; their products are zero
+      const float* pa = a_scale + (int64_t)(m < M ? m : M - 1) * nkb;
+      const float* pb = b_scale + (int64_t)(n0 < N ? n0 / 128 : 0) * nkb;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      float sa = __ldg(pa), sb = __ldg(pb);
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int buf = (int)(it & 1);
+        const float s = sa * sb;
+        if (kb + 1 < nkb) {
+          sa = __ldg(pa + kb + 1);
+          sb = __ldg(pb + kb + 1);
+        }
+        ok = wait_or_abort_t<GIVEUP>(&acc_full[buf], (uint32_t)((it / 2) & 1), abort_flag);
+        // the loads below are collective: a warp leaves together
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          tmem_ld32(tl + 256 * buf + 32 * c, v);
+          tmem_landed(v);
+          if (c == 3) {
+            tc_fence_before();
+            mbar_arrive(&acc_empty[buf]);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], s, s, v[2 * i], v[2 * i + 1]);
+        }
+      }
+      if (ok && m < M) {
+        Tout* dst = out + (int64_t)m * N + n0;
+        if (N % 8 == 0) {  // 16-byte aligned pieces of eight
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (n0 + 8 * i < N) {
+              const float2 x0 = split2(acc[4 * i]), x1 = split2(acc[4 * i + 1]), x2 = split2(acc[4 * i + 2]),
+                           x3 = split2(acc[4 * i + 3]);
+              if constexpr (sizeof(Tout) == 4) {
+                reinterpret_cast<float4*>(dst + 8 * i)[0] = make_float4(x0.x, x0.y, x1.x, x1.y);
+                reinterpret_cast<float4*>(dst + 8 * i)[1] = make_float4(x2.x, x2.y, x3.x, x3.y);
+              } else {
+                const __nv_bfloat162 p[4] = {__floats2bfloat162_rn(x0.x, x0.y), __floats2bfloat162_rn(x1.x, x1.y),
+                                             __floats2bfloat162_rn(x2.x, x2.y), __floats2bfloat162_rn(x3.x, x3.y)};
+                *reinterpret_cast<uint4*>(dst + 8 * i) = *reinterpret_cast<const uint4*>(p);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const float2 x = split2(acc[i]);
+            if (n0 + 2 * i < N) dst[2 * i] = from_f32<Tout>(x.x);
+            if (n0 + 2 * i + 1 < N) dst[2 * i + 1] = from_f32<Tout>(x.y);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  drain_after_abort<kTallStages>(abort_flag, tid == 8 * 32, tid == 9 * 32, full, issued, bar_fin, err);
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------ few rows
+constexpr int kFlatRows = 128;     // weight rows of a tile
+constexpr int kFlatThreads = 192;  // warps 0-3: read accumulators, scale, add up; warp 4 copies, warp 5 multiplies
+
+template <int BN>
+struct Flat {
+  static constexpr int kBufs = BN <= 64 ? 4 : 2;  // accumulators; two CTAs share an SM's 512 columns
+  static constexpr uint32_t kCols = kBufs * BN < 32 ? 32 : kBufs * BN;
+  static constexpr uint32_t kW = kFlatRows * kK, kStage = kW + BN * kK;
+  static constexpr int kStages = 98304 / kStage;  // 96 KB: two CTAs per SM
+  static constexpr uint32_t kPart = BN * kFlatRows * 4;  // partial sums, over the stages once they are read
+  static constexpr uint32_t kScale = (kStages * kStage > kPart ? kStages * kStage : kPart);
+  static constexpr uint32_t kBar = kScale + 4 * 2 * BN * 4;  // factors: [warp][2][BN]
+  static constexpr uint32_t kSmem = kBar + 256 + 1024;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at the same shared-memory offset of CTA `rank` of the cluster
+__device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <int BN, typename Tout, bool GIVEUP>
+__global__ void __launch_bounds__(kFlatThreads)
+matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
+                Tout* __restrict__ out, int M, int N, int nkb, int split, unsigned int* __restrict__ err) {
+  using F = Flat<BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kBar);
+  uint64_t* empty = full + F::kStages;
+  uint64_t* acc_full = empty + F::kStages;
+  uint64_t* acc_empty = acc_full + F::kBufs;
+  uint64_t* bar_fin = acc_empty + F::kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_fin + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* part = reinterpret_cast<float*>(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int n0 = blockIdx.x / split * kFlatRows, m0 = blockIdx.y * BN;
+  // this CTA's blocks: [kb0, kb0 + cnt), as even as they get
+  const int kb0 = (int)((int64_t)nkb * rank / split), cnt = (int)((int64_t)nkb * (rank + 1) / split) - kb0;
+
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, F::kCols);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < F::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < F::kBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 128);
+    }
+    mbar_init(bar_fin, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int issued = 0;  // stages whose copies warp 4 has started
+
+  if (warp == 4) {
+    if (lane == 0) {
+      bool ok = true;
+      for (; issued < cnt; ++issued) {
+        const int it = issued, s = it % F::kStages;
+        if (it >= F::kStages) ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((it / F::kStages - 1) & 1), abort_flag);
+        if (!ok) break;
+        uint8_t* st = sm + s * F::kStage;
+        mbar_arrive_expect_tx(&full[s], F::kStage);
+        tma_load_2d(st, &maps.b, (kb0 + it) * kK, n0, &full[s]);
+        tma_load_2d(st + F::kW, &maps.a, (kb0 + it) * kK, m0, &full[s]);
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int it = 0; it < cnt && ok; ++it) {
+        const int s = it % F::kStages, buf = it % F::kBufs;
+        ok = wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
+        if (ok && it >= F::kBufs)
+          ok = wait_or_abort_t<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* st = sm + s * F::kStage;
+        mma_block(tmem + BN * buf, st, st + F::kW, idesc_e4m3(kFlatRows, BN));
+        mma_commit(&empty[s]);
+        mma_commit(&acc_full[buf]);
+      }
+    }
+  } else {
+    constexpr int kPer = (BN + 31) / 32;  // factors a lane fetches
+    const uint32_t tl = tmem_lane(tmem, warp);
+    float* fac = reinterpret_cast<float*>(sm + F::kScale) + warp * 2 * BN;
+    const float* pb = b_scale + (int64_t)(n0 / 128) * nkb + kb0;
+    uint64_t acc[BN / 2];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
+    float f[kPer];
+    auto fetch = [&](int it) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int j = lane + 32 * i, m = m0 + j;
+        f[i] = j < BN && m < M ? __ldg(a_scale + (int64_t)m * nkb + kb0 + it) * __ldg(pb + it) : 0.f;
+      }
+    };
+    if (cnt > 0) fetch(0);
+    bool ok = true;
+    for (int it = 0; it < cnt; ++it) {
+      const int buf = it % F::kBufs;
+      float* fw = fac + (it & 1) * BN;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (lane + 32 * i < BN) fw[lane + 32 * i] = f[i];
+      __syncwarp();
+      if (it + 1 < cnt) fetch(it + 1);
+      ok = wait_or_abort_t<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c) {
+        float v[16];
+        tmem_ld16(tl + BN * buf + 16 * c, v);
+        tmem_landed(v);
+        if (c == BN / 16 - 1) {
+          tc_fence_before();
+          mbar_arrive(&acc_empty[buf]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 s = *reinterpret_cast<const float4*>(fw + 16 * c + 4 * i);
+          fma2(acc[8 * c + 2 * i], s.x, s.y, v[4 * i], v[4 * i + 1]);
+          fma2(acc[8 * c + 2 * i + 1], s.z, s.w, v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    }
+    // Every copy has landed and every MMA has read its stage once the last accumulator is complete (the
+    // MMAs complete in order), so the partial sums may lie over the stages.  After a wait that ran out the
+    // copies may still be on their way: nothing is written there.  All four warps decide together.
+    if (group_and(1, 128, ok && !*abort_flag)) {
+      const int n = (warp & 3) * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < BN / 2; ++i) {
+        const float2 x = split2(acc[i]);
+        part[(2 * i) * kFlatRows + n] = x.x;
+        part[(2 * i + 1) * kFlatRows + n] = x.y;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  drain_after_abort<F::kStages>(abort_flag, tid == 4 * 32, tid == 5 * 32, full, issued, bar_fin, err);
+  if (split > 1) cluster_sync();
+  tc_fence_after();
+  // the activation rows are dealt to the CTAs of the cluster; each sums the partial sums in rank order
+  const int rows = M - m0 < BN ? M - m0 : BN;
+  if (!*abort_flag) {
+    for (int j = rank; j < rows; j += split) {
+      for (int n = tid; n < kFlatRows; n += kFlatThreads) {
+        if (n0 + n >= N) continue;
+        const float* p = part + j * kFlatRows + n;
+        float x = 0.f;
+        if (split == 1) x = *p;
+        else
+          for (int r = 0; r < split; ++r) x += load_peer(p, r);
+        out[(int64_t)(m0 + j) * N + n0 + n] = from_f32<Tout>(x);
+      }
+    }
+  }
+  if (split > 1) cluster_sync();  // the peers' partial sums stay until they are read
+  if (warp == 0) tmem_dealloc(tmem, F::kCols);
+}
+
+// ------------------------------------------------------------------------------ host side
+struct DeviceState {
+  DeviceOnce once;
+  int sms[kMaxDevices] = {};
+};
+DeviceState g_state;
+
+template <typename Kernel>
+cudaError_t allow_smem(Kernel* k, uint32_t bytes) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+template <int BN>
+cudaError_t allow_flat() {
+  cudaError_t e = allow_smem(matmul_fp8_flat<BN, __nv_bfloat16, false>, Flat<BN>::kSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, float, false>, Flat<BN>::kSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, __nv_bfloat16, true>, Flat<BN>::kSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, float, true>, Flat<BN>::kSmem);
+  return e;
+}
+cudaError_t prepare_device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const cudaError_t e = g_state.once.run(dev, [dev] {
+    cudaError_t e = allow_smem(matmul_fp8_tall<__nv_bfloat16, false>, kTallSmem);
+    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<float, false>, kTallSmem);
+    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<__nv_bfloat16, true>, kTallSmem);
+    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<float, true>, kTallSmem);
+    if (e == cudaSuccess) e = allow_flat<16>();
+    if (e == cudaSuccess) e = allow_flat<32>();
+    if (e == cudaSuccess) e = allow_flat<64>();
+    if (e == cudaSuccess) e = allow_flat<128>();
+    if (e != cudaSuccess) return e;
+    return cudaDeviceGetAttribute(&g_state.sms[dev], cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (e == cudaSuccess) *sms = g_state.sms[dev];
+  return e;
+}
+
+template <int BN, typename Tout>
+cudaError_t launch_flat(const MatmulArgs& a, int sms, cudaStream_t st) {
+  using F = Flat<BN>;
+  const int nkb = (a.K + kK - 1) / kK, tiles = (a.N + kFlatRows - 1) / kFlatRows;
+  const int64_t rows = (a.M + BN - 1) / BN;
+  Maps maps;
+  if (!tensor_map_2d(&maps.a, a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.K, BN, kK) ||
+      !tensor_map_2d(&maps.b, a.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.N, a.K, a.K, kFlatRows, kK))
+    return cudaErrorInvalidValue;
+  // as many CTAs as fit two to an SM, with two blocks each at least
+  int64_t split = 2 * (int64_t)sms / (tiles * rows);
+  if (split > nkb / 2) split = nkb / 2;
+  if (split > 8) split = 8;
+  if (split < 1) split = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)rows);
+  cfg.blockDim = dim3(kFlatThreads);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  TraceScope ts("kda_matmul_fp8_flat", st);
+  auto* kernel = a.give_up ? matmul_fp8_flat<BN, Tout, true> : matmul_fp8_flat<BN, Tout, false>;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, nkb,
+                            (int)split, a.err);
+}
 
 template <typename Tout>
-__global__ void __launch_bounds__(256)
-matmul_fp8_kernel(const __nv_fp8_e4m3* __restrict__ a, const float* __restrict__ a_scale,
-                  const __nv_fp8_e4m3* __restrict__ b, const float* __restrict__ b_scale, Tout* __restrict__ out,
-                  int64_t M, int N, int K) {
-  __shared__ float sa[kKs][kTile + 1], sb[kKs][kTile + 1];
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const int64_t m0 = (int64_t)blockIdx.y * kTile;
-  const int n0 = blockIdx.x * kTile, kb = (K + 127) / 128;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += kKs) {  // K is a multiple of 16
-    for (int i = tid; i < kTile * kKs; i += 256) {
-      const int r = i / kKs, c = i % kKs, blk = (k0 + c) / 128;
-      const int64_t m = m0 + r;
-      const int n = n0 + r;
-      sa[c][r] = m < M ? float(a[m * K + k0 + c]) * a_scale[m * kb + blk] : 0.f;
-      sb[c][r] = n < N ? float(b[(int64_t)n * K + k0 + c]) * b_scale[(int64_t)(n / 128) * kb + blk] : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kKs; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[c][ty + 16 * i], sb[c][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+cudaError_t launch(const MatmulArgs& a, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = prepare_device(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles_m = (a.M + kTallM - 1) / kTallM, tiles = tiles_m * ((a.N + kTallN - 1) / kTallN);
+  if (tiles * 2 < sms) {
+    if (a.M <= 16) return launch_flat<16, Tout>(a, sms, st);
+    if (a.M <= 32) return launch_flat<32, Tout>(a, sms, st);
+    if (a.M <= 64) return launch_flat<64, Tout>(a, sms, st);
+    return launch_flat<128, Tout>(a, sms, st);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i;
-      const int n = n0 + tx + 16 * j;
-      if (m < M && n < N) out[m * N + n] = from_f32<Tout>(acc[i][j]);
-    }
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  Maps maps;
+  if (!tensor_map_2d(&maps.a, a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.K, kTallM, kK) ||
+      !tensor_map_2d(&maps.b, a.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.N, a.K, a.K, kTallN, kK))
+    return cudaErrorInvalidValue;
+  TraceScope ts("kda_matmul_fp8_tall", st);
+  auto* kernel = a.give_up ? matmul_fp8_tall<Tout, true> : matmul_fp8_tall<Tout, false>;
+  kernel<<<(unsigned)(tiles < sms ? tiles : sms), kTallThreads, kTallSmem, st>>>(
+      maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, (a.K + kK - 1) / kK, (int)tiles_m,
+      (int)tiles, a.err);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t matmul_fp8_launch(const MatmulArgs& a, cudaStream_t st) {
-  const int64_t gy = (a.M + kTile - 1) / kTile;
-  if (gy > 65535) return cudaErrorInvalidValue;
-  const dim3 grid((a.N + kTile - 1) / kTile, (unsigned)gy);
-  TraceScope ts("kda_matmul_fp8", st);
-  const auto* pa = reinterpret_cast<const __nv_fp8_e4m3*>(a.a);
-  const auto* pb = reinterpret_cast<const __nv_fp8_e4m3*>(a.b);
-  if (a.out_bf16)
-    matmul_fp8_kernel<<<grid, 256, 0, st>>>(pa, a.a_scale, pb, a.b_scale, static_cast<__nv_bfloat16*>(a.out), a.M, a.N, a.K);
-  else
-    matmul_fp8_kernel<<<grid, 256, 0, st>>>(pa, a.a_scale, pb, a.b_scale, static_cast<float*>(a.out), a.M, a.N, a.K);
-  return cudaGetLastError();
+  return a.out_bf16 ? launch<__nv_bfloat16>(a, st) : launch<float>(a, st);
 }
 
 }  // namespace kda
