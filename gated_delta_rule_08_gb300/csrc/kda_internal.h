@@ -197,7 +197,9 @@ struct LinearArgs {
   unsigned int* err;
   bool give_up;
 };
-cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t stream);
+cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t stream);  // fp32 inputs (kda_linear.cu)
+cudaError_t linear_tc_launch(const LinearArgs& a, cudaStream_t stream);         // bf16 inputs (kda_linear_tc.cu)
+size_t linear_tc_workspace(int B, int64_t T, int H, int dk, int dv);
 
 struct LinearStepArgs {
   const void* q;

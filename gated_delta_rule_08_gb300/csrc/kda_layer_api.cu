@@ -33,7 +33,7 @@ kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA
 
 KDA_API size_t kda_linear_chunk_fwd_workspace_size(int B, int64_t T, int H, int dk, int dv, kda_dtype dtype) {
   if (B <= 0 || T < 0 || H <= 0 || !dims_ok(dk, dv) || !dtype_ok(dtype)) return 0;
-  return 256;
+  return 256 + (dtype == KDA_DTYPE_BF16 ? linear_tc_workspace(B, T, H, dk, dv) : 0);
 }
 
 KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, const float* g, int g_per_token,
@@ -66,7 +66,8 @@ KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void
   a.B = B; a.T = T; a.T_tot = T_tot; a.H = H; a.dk = dk; a.dv = dv; a.scale = scale;
   a.bf16 = dtype == KDA_DTYPE_BF16; a.out_bf16 = out_dtype == KDA_DTYPE_BF16;
   a.workspace = workspace; a.err = err; a.give_up = test_wait_timeout();
-  return done(linear_recurrent_launch(a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(a.bf16 ? linear_tc_launch(a, s) : linear_recurrent_launch(a, s));
 }
 
 KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const float* g, int g_per_token,

@@ -4,7 +4,7 @@
 //   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
 // the KDA recurrence (section 2.2 Eq. 1) without the delta rule's erase and with a scalar decay.
 //
-// linear_recurrent_kernel: whole sequences in fp32, token by token.  Value columns are independent of
+// linear_recurrent_kernel: whole sequences of fp32 inputs, token by token (bf16: kda_linear_tc.cu).  Value columns are independent of
 // one another, so a CTA takes 16 of them for the whole sequence and keeps its dk x 16 slice of the
 // state in registers; a thread owns dk / 8 rows of one column.
 //
@@ -21,9 +21,9 @@ constexpr int kCols = 16;  // value columns of a CTA
 constexpr int kTile = 16;  // tokens staged at a time
 constexpr int kRecThreads = 128;
 
-template <int DK, typename Tin, typename Tout>
+template <int DK, typename Tout>
 __global__ void __launch_bounds__(kRecThreads)
-linear_recurrent_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
+linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* __restrict__ g,
                         int g_per_token, const float* h0, const int32_t* __restrict__ cu, Tout* __restrict__ out,
                         float* hT, int B, int64_t T, int64_t T_tot, int H, int dv, float scale,
@@ -59,14 +59,14 @@ linear_recurrent_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, co
     for (int i = 0; i < kPer; ++i) {
       const int e = tid + i * kRecThreads, r = e / DK, d = e % DK;
       const bool in = r < m;
-      rk[i] = in ? to_f32(k[(t0 + c + r) * k_stride + h * DK + d]) : 0.f;
-      rq[i] = in ? to_f32(q[(t0 + c + r) * q_stride + h * DK + d]) : 0.f;
+      rk[i] = in ? k[(t0 + c + r) * k_stride + h * DK + d] : 0.f;
+      rq[i] = in ? q[(t0 + c + r) * q_stride + h * DK + d] : 0.f;
     }
     float rv[kTile * kCols / kRecThreads];
 #pragma unroll
     for (int i = 0; i < kTile * kCols / kRecThreads; ++i) {
       const int e = tid + i * kRecThreads, r = e / kCols, d = e % kCols;
-      rv[i] = r < m ? to_f32(v[(t0 + c + r) * v_stride + (int64_t)h * dv + slice * kCols + d]) : 0.f;
+      rv[i] = r < m ? v[(t0 + c + r) * v_stride + (int64_t)h * dv + slice * kCols + d] : 0.f;
     }
     float re = 1.f;
     if (tid < m) re = expf(g_per_token ? g[(t0 + c + tid) * H + h] : g[h]);
@@ -111,15 +111,15 @@ linear_recurrent_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, co
   }
 }
 
-template <typename Tin, typename Tout>
+template <typename Tout>
 cudaError_t recurrent_typed(const LinearArgs& a, cudaStream_t st) {
   const int64_t grid = (int64_t)a.B * a.H * (a.dv / kCols);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  auto* kernel = a.dk == 64 ? linear_recurrent_kernel<64, Tin, Tout> : linear_recurrent_kernel<128, Tin, Tout>;
+  auto* kernel = a.dk == 64 ? linear_recurrent_kernel<64, Tout> : linear_recurrent_kernel<128, Tout>;
   TraceScope ts("kda_linear_recurrent", st);
   kernel<<<(unsigned)grid, kRecThreads, 0, st>>>(
-      static_cast<const Tin*>(a.q), static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v), a.q_stride, a.k_stride,
-      a.v_stride, a.g, a.g_per_token, a.h0, a.cu_seqlens, static_cast<Tout*>(a.out), a.hT, a.B, a.T, a.T_tot, a.H,
+      static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), a.q_stride,
+      a.k_stride, a.v_stride, a.g, a.g_per_token, a.h0, a.cu_seqlens, static_cast<Tout*>(a.out), a.hT, a.B, a.T, a.T_tot, a.H,
       a.dv, a.scale, a.err);
   return cudaGetLastError();
 }
@@ -204,9 +204,7 @@ cudaError_t step_typed(const LinearStepArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t st) {
-  if (a.bf16)
-    return a.out_bf16 ? recurrent_typed<__nv_bfloat16, __nv_bfloat16>(a, st) : recurrent_typed<__nv_bfloat16, float>(a, st);
-  return a.out_bf16 ? recurrent_typed<float, __nv_bfloat16>(a, st) : recurrent_typed<float, float>(a, st);
+  return a.out_bf16 ? recurrent_typed<__nv_bfloat16>(a, st) : recurrent_typed<float>(a, st);
 }
 
 cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t st) {

@@ -1,0 +1,639 @@
+// Linear attention with one decay per head over whole sequences, on the tcgen05 tensor cores (bf16 inputs).
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t
+//
+// In chunks of 64 tokens, with S the state before the chunk and G_i the running sum of its log decays:
+//   o_i = scale ( e^{G_i} S^T q_i + sum_{j <= i} A_ij v_j ),   A_ij = e^{G_i - G_j} q_i . k_j
+//   S'  = e^{G_64} S + U,   U = sum_j w_j k_j v_j^T,           w_j = e^{G_64 - G_j}
+// A and U need nothing of the state, so the tensor cores work on them ahead of the serial part, which is
+// one fused multiply-add per state element.
+//
+// A CTA walks over the chunks of one (sequence, head) or of a segment of it.  Everything is laid out with
+// the value channel as the tensor core's row (M = 128; with dv = 64 the upper rows are not used):
+//   D_A [128 x 64]  = [Q ; K] K^T     rows 0-63 are q_i . k_j (the stack fills the 128 rows an MMA has)
+//   D_U [dv x dk]   = V^T K~          K~ = w_j k_j as the exact sum of three bf16 parts, so U has fp32 accuracy
+//   D_2 [dv x 64]   = V^T A^T         A masked, scaled and rounded to bf16 in shared memory
+//   D_1 [dv x 64]   = S^T Q^T         S^T rounded to bf16 in TMEM
+// with S^T itself (fp32) in the registers of warps 0-7.  So out is off by the roundings of A and S to
+// bf16 (half a step each, of its terms), like its own rounding; the states are not rounded below fp32.
+//
+// Decays: sums are kept in log2.  A token whose decay is below 2^-150 (g = -inf among them) empties the
+// state: sums start again at 0 after it, and pairs with such a token between them are masked, so that no
+// infinity meets another and a long sum loses no precision.
+//
+// Warps: 0-7 state and output (two per TMEM lane quadrant), 8-9 A, 10-13 K~, 14 copies and decays,
+// 15 (one lane) all MMAs.
+//
+// Few long sequences would leave most of the device idle, so they are cut into segments: MODE 1 runs
+// compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
+// folds them in order, and MODE 0 runs every segment from its state.
+#include "kda_internal.h"
+#include "kda_tc_common.cuh"
+#include "kda_tma.h"
+
+namespace kda {
+namespace {
+
+using namespace tcx;
+
+constexpr int kC = 64;                      // tokens of a chunk
+constexpr int kThreads = 512;
+constexpr int kStateThreads = 256, kMaskThreads = 64, kKeyThreads = 128;
+constexpr int kCopyWarp = 14, kMmaWarp = 15;
+constexpr int kStages = 3;
+// a stage: [Q | K] of the first 64 channels, [Q | K] of the second, V of the first 64 channels, of the second
+constexpr uint32_t kBlk = 8192;             // 64 tokens x 64 channels
+constexpr uint32_t kQ = 0, kKey = kBlk, kPair = 2 * kBlk, kV = 4 * kBlk, kStageBytes = 6 * kBlk;
+constexpr uint32_t kKt = kStages * kStageBytes;         // K~: three parts of two blocks
+constexpr uint32_t kA = kKt + 6 * kBlk;                 // A [64 i][64 j]
+constexpr int kRing = 8;                                // decays: read until the state has been updated
+constexpr uint32_t kDecay = kA + kBlk;
+struct Decay {
+  float G[kC];    // log2 of the decay from the chunk's start, or from the last emptying token, to token i
+  float E[kC];    // e^{G_i} on the state before the chunk; 0 once it has been emptied
+  float W[kC];    // w_j; 0 for tokens past the sequence
+  int first[kC];  // the first token that reaches token i
+  float all;      // decay of the state over the whole chunk
+  int pad[3];
+};
+constexpr uint32_t kBar = kDecay + kRing * sizeof(Decay);
+constexpr uint32_t kSmem = kBar + 256 + 1024;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// TMEM columns
+constexpr uint32_t kTmA = 0, kTm1 = 64, kTm2 = 128, kTmS = 192, kTmU = 256;  // D_U twice
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kEmpty = -150.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+struct Params {
+  const float* g;
+  int g_per_token;
+  const float* h0;
+  const int32_t* cu;
+  void* out;
+  float* hT;
+  int B;
+  int64_t T, T_tot;
+  int H, dv;
+  float scale;
+  unsigned int* err;
+  int nseg;
+  int seg_len;       // chunks of a segment
+  float* seg_state;  // [B H][nseg][dk dv]: MODE 1 writes U_seg, the merge turns it into the state before the segment
+  float* seg_decay;  // [B H][nseg]
+};
+
+// Sequence of a CTA, in shared memory, by all threads: the longest first, so that no long one starts
+// last; their number is small where lengths differ much, and beyond 64 the order is left as it is.
+__device__ __forceinline__ int sequence_by_rank(const int32_t* __restrict__ cu, int B, int r, int* slot) {
+  if (cu == nullptr || B > 64) return r;
+  if (threadIdx.x < B) {
+    const int i = threadIdx.x, n = cu[i + 1] - cu[i];
+    int rank = 0;
+    for (int j = 0; j < B; ++j) {
+      const int m = cu[j + 1] - cu[j];
+      rank += m > n || (m == n && j < i);
+    }
+    if (rank == r) *slot = i;
+  }
+  __syncthreads();
+  return *slot;
+}
+
+// Decays of one chunk (one warp, tokens 2 lane and 2 lane + 1).  Returns log2 of the chunk's decay and
+// whether a token emptied the state.
+__device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n, int lane, bool& emptied) {
+  const int i0 = 2 * lane, i1 = i0 + 1;
+  const bool e0 = g0 <= kEmpty, e1 = g1 <= kEmpty;
+  const float a0 = e0 ? 0.f : g0, a1 = e1 ? 0.f : g1;
+  // running sum since the last emptying token, and that token's index
+  int last = e1 ? i1 : (e0 ? i0 : -1);
+  float sum = e1 ? 0.f : a0 + a1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float s = __shfl_up_sync(0xffffffffu, sum, o);
+    const int l = __shfl_up_sync(0xffffffffu, last, o);
+    if (lane >= o && last < 0) {
+      sum += s;
+      last = l;
+    }
+  }
+  float before = __shfl_up_sync(0xffffffffu, sum, 1);
+  int lastb = __shfl_up_sync(0xffffffffu, last, 1);
+  if (lane == 0) {
+    before = 0.f;
+    lastb = -1;
+  }
+  const float G0 = e0 ? 0.f : before + a0, G1 = e1 ? 0.f : G0 + a1;
+  const int l0 = e0 ? i0 : lastb, l1 = e1 ? i1 : l0;
+  // sum of the decays after a token: from the other end, so that the weights near 1 are the exact ones
+  float tail = a0 + a1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float s = __shfl_down_sync(0xffffffffu, tail, o);
+    if (lane + o < 32) tail += s;
+  }
+  const float total = __shfl_sync(0xffffffffu, tail, 0);
+  float after = __shfl_down_sync(0xffffffffu, tail, 1);
+  if (lane == 31) after = 0.f;
+  const int final_last = __shfl_sync(0xffffffffu, l1, 31);
+  d->G[i0] = G0;
+  d->G[i1] = G1;
+  d->E[i0] = l0 < 0 ? exp2f(G0) : 0.f;
+  d->E[i1] = l1 < 0 ? exp2f(G1) : 0.f;
+  d->W[i0] = i0 < n && i0 >= final_last ? exp2f(a1 + after) : 0.f;
+  d->W[i1] = i1 < n && i1 >= final_last ? exp2f(after) : 0.f;
+  d->first[i0] = l0 < 0 ? 0 : l0;
+  d->first[i1] = l1 < 0 ? 0 : l1;
+  emptied = final_last >= 0;
+  if (lane == 0) d->all = emptied ? 0.f : exp2f(total);
+  return total;
+}
+
+// MODE 0: states and outputs.  MODE 1: a segment's contribution to the state after it, and its decay.
+template <int DK, int MODE, typename Tout, bool GIVEUP>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
+  constexpr int KB = DK / 64;   // 64-channel blocks of q and k
+  constexpr int KC = DK / 2;    // state columns of a thread
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBar);  // [stages] tiles landed and decays written
+  uint64_t* empty = full + kStages;                         // [stages] all MMAs of the chunk done, decays seen by the state warps
+  uint64_t* a_done = empty + kStages;                       // D_A complete
+  uint64_t* a_ready = a_done + 1;                           // A written, D_A read
+  uint64_t* kt_ready = a_done + 2;                          // K~ written (and V's rows past the sequence cleared)
+  uint64_t* u_full = a_done + 3;                            // [2] D_U complete
+  uint64_t* u_empty = a_done + 5;                           // [2] D_U read
+  uint64_t* s_ready = a_done + 7;                           // S^T in TMEM
+  uint64_t* o_full = a_done + 8;                            // D_1 and D_2 complete
+  uint64_t* bar_fin = a_done + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 10);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* seq_slot = reinterpret_cast<int*>(tmem_slot + 2);
+  Decay* decay = reinterpret_cast<Decay*>(sm + kDecay);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = p.H, dv = p.dv;
+  if (p.cu != nullptr && !offsets_ok(p.cu, p.B, p.T_tot)) {
+    if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
+    return;
+  }
+  const int seg = blockIdx.x % p.nseg, chain = blockIdx.x / p.nseg;
+  const int h = chain % H, b = sequence_by_rank(p.cu, p.B, chain / H, seq_slot);
+  const int64_t t_begin = p.cu ? (int64_t)p.cu[b] : (int64_t)b * p.T;
+  const int64_t len = p.cu ? (int64_t)p.cu[b + 1] - p.cu[b] : p.T;
+  const int nchunks = (int)((len + kC - 1) / kC);
+  const int last_seg = nchunks > 0 ? (nchunks - 1) / p.seg_len : 0;
+  if (MODE == 0 ? seg > last_seg : seg >= last_seg) return;
+  const int c0 = seg * p.seg_len, nc = (nchunks < c0 + p.seg_len ? nchunks : c0 + p.seg_len) - c0;
+  const int64_t t0 = t_begin + (int64_t)c0 * kC;  // the segment's first token
+  const int64_t rows = len - (int64_t)c0 * kC;    // tokens from there to the sequence's end
+  const int64_t state_at = ((int64_t)b * H + h) * DK * dv;
+  const int64_t seg_at = (((int64_t)b * H + h) * p.nseg + seg);
+
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 2);
+      mbar_init(&empty[i], 1 + kStateThreads / 32);
+    }
+    mbar_init(a_done, 1);
+    mbar_init(a_ready, kMaskThreads);
+    mbar_init(kt_ready, kKeyThreads);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], kStateThreads);
+    }
+    mbar_init(s_ready, kStateThreads);
+    mbar_init(o_full, 1);
+    mbar_init(bar_fin, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int issued = 0;  // stages whose copies have been started (warp 14)
+
+  if (warp == kCopyWarp) {
+    // ======================== copies and decays
+    const int vb = dv / 64;
+    const uint32_t bytes = (uint32_t)((MODE == 0 ? 2 * KB : KB) + vb) * kBlk;
+    double total = 0.0;  // log2 of the segment's decay
+    bool any = false;
+    auto load_g = [&](int c, int i) -> float {
+      const int64_t r = (int64_t)c * kC + i;
+      if (r >= rows) return 0.f;
+      return kLog2e * (p.g_per_token ? __ldg(p.g + (t0 + r) * H + h) : __ldg(p.g + h));
+    };
+    float g0 = nc > 0 ? load_g(0, 2 * lane) : 0.f, g1 = nc > 0 ? load_g(0, 2 * lane + 1) : 0.f;
+    bool ok = true;
+    for (; issued < nc; ++issued) {
+      const int c = issued, s = c % kStages;
+      if (c >= kStages) ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((c / kStages - 1) & 1), abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        uint8_t* st = sm + s * kStageBytes;
+        const int y = (int)(t0 + (int64_t)c * kC);
+        mbar_arrive_expect_tx(&full[s], bytes);
+        for (int i = 0; i < KB; ++i) {
+          if (MODE == 0) tma_load_2d(st + kQ + i * kPair, &maps.q, h * DK + 64 * i, y, &full[s]);
+          tma_load_2d(st + kKey + i * kPair, &maps.k, h * DK + 64 * i, y, &full[s]);
+        }
+        for (int i = 0; i < vb; ++i) tma_load_2d(st + kV + i * kBlk, &maps.v, h * dv + 64 * i, y, &full[s]);
+      }
+      const int64_t left = rows - (int64_t)c * kC;
+      bool emptied;
+      total += chunk_decay(&decay[c % kRing], g0, g1, (int)(left < kC ? left : kC), lane, emptied);
+      any |= emptied;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      if (c + 1 < nc) {
+        g0 = load_g(c + 1, 2 * lane);
+        g1 = load_g(c + 1, 2 * lane + 1);
+      }
+    }
+    if (MODE == 1 && lane == 0) p.seg_decay[seg_at] = any ? 0.f : (float)exp2(total);
+  } else if (warp == kMmaWarp) {
+    // ======================== all MMAs
+    if (lane == 0) {
+      constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, true, true),
+                         id_1 = idesc_bf16_f32(128, kC, false, false), id_2 = idesc_bf16_f32(128, kC, true, false);
+      const uint64_t d_kt = smem_desc_sw128(smem_u32(sm + kKt), kBlk, 1024);
+      const uint64_t d_a = smem_desc_sw128(smem_u32(sm + kA), 16, 1024);
+      bool ok = true;
+      auto scores = [&](int c) {  // D_A of chunk c
+        const int s = c % kStages;
+        if (!wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag)) return false;
+        tc_fence_after();
+        const uint8_t* st = sm + s * kStageBytes;
+        const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i) {
+          const uint32_t off = (i / 4) * kPair + (i % 4) * 32;
+          mma_bf16_ss(tmem + kTmA, desc_add(dq, off), desc_add(dk, off), id_a, i > 0);
+        }
+        mma_commit(a_done);
+        return true;
+      };
+      if (MODE == 0 && nc > 0) ok = scores(0);
+      for (int c = 0; c < nc && ok; ++c) {
+        const int s = c % kStages;
+        const uint8_t* st = sm + s * kStageBytes;
+        const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
+        ok = wait_or_abort_t<GIVEUP>(kt_ready, (uint32_t)(c & 1), abort_flag);
+        if (ok && c >= 2) ok = wait_or_abort_t<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int j = 0; j < kC / 16; ++j)
+            mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, j * 2048), desc_add(d_kt, i * 2 * kBlk + j * 2048), id_u,
+                        i + j > 0);
+        mma_commit(&u_full[c & 1]);
+        if constexpr (MODE == 0) {
+          ok = wait_or_abort_t<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
+          // D_1 and D_2 of the chunk before have been read once S^T is there
+          ok = ok && wait_or_abort_t<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < kC / 16; ++j)
+            mma_bf16_ss(tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, j * 32), id_2, j > 0);
+#pragma unroll
+          for (int i = 0; i < DK / 16; ++i)
+            mma_f16_ts(tmem + kTm1, tmem + kTmS + 8 * i, desc_add(d_q, (i / 4) * kPair + (i % 4) * 32), id_1, i > 0);
+          mma_commit(o_full);
+          mma_commit(&empty[s]);
+          if (c + 1 < nc) ok = scores(c + 1);
+        } else {
+          mma_commit(&empty[s]);
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ======================== state and output
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // value channel
+    const uint32_t tl = tmem_lane(tmem, warp);
+    const bool live = row < dv;
+    float S[KC];
+    {
+      const float* init = MODE == 1 ? nullptr : p.nseg > 1 ? p.seg_state + seg_at * DK * dv : p.h0 ? p.h0 + state_at : nullptr;
+#pragma unroll
+      for (int i = 0; i < KC; ++i) S[i] = init && live ? init[(int64_t)(KC * half + i) * dv + row] : 0.f;
+    }
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
+      const Decay* d = &decay[c % kRing];
+      if constexpr (MODE == 0) {
+#pragma unroll
+        for (int i = 0; i < KC / 32; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = pack_bf2(S[32 * i + 2 * j], S[32 * i + 2 * j + 1]);
+          tmem_st16u(tl + kTmS + (KC / 2) * half + 16 * i, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(s_ready);
+      }
+      ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&empty[c % kStages]);  // so that the stage's phase cannot pass by unseen
+      ok = wait_or_abort_t<GIVEUP>(&u_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float all = d->all;
+#pragma unroll
+      for (int i = 0; i < KC / 16; ++i) {
+        float u[16];
+        tmem_ld16(tl + kTmU + 128 * (c & 1) + KC * half + 16 * i, u);
+        tmem_landed(u);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) S[16 * i + j] = fmaf(all, S[16 * i + j], u[j]);
+      }
+      tc_fence_before();
+      mbar_arrive(&u_empty[c & 1]);
+      if constexpr (MODE == 0) {
+        ok = wait_or_abort_t<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int64_t left = rows - (int64_t)c * kC;
+        Tout* dst = static_cast<Tout*>(p.out) + ((t0 + (int64_t)c * kC) * H + h) * dv + row;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tok = 32 * half + 16 * i;
+          float x[16], y[16];
+          tmem_ld16(tl + kTm1 + tok, x);
+          tmem_ld16(tl + kTm2 + tok, y);
+          tmem_landed(x);
+          tmem_landed(y);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float o = p.scale * fmaf(d->E[tok + j], x[j], y[j]);
+            if (live && tok + j < left) dst[(int64_t)(tok + j) * H * dv] = from_f32<Tout>(o);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    if (ok && live) {
+      float* dst = MODE == 1 ? p.seg_state + seg_at * DK * dv : p.hT && seg == last_seg ? p.hT + state_at : nullptr;
+      if (dst) {
+#pragma unroll
+        for (int i = 0; i < KC; ++i) dst[(int64_t)(KC * half + i) * dv + row] = S[i];
+      }
+    }
+  } else if (warp < 10) {
+    // ======================== A: masked, decayed, to bf16
+    if constexpr (MODE == 0) {
+      const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
+      const uint32_t tl = tmem_lane(tmem, warp & 1);
+      const int jend = (warp & 1) ? kC : kC / 2;  // tokens 0-31 see none past 31
+      bool ok = true;
+      for (int c = 0; c < nc; ++c) {
+        const Decay* d = &decay[c % kRing];
+        ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+        ok = ok && wait_or_abort_t<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
+        // the products that read A of the chunk before
+        if (ok && c > 0) ok = wait_or_abort_t<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float Gi = d->G[i];
+        const uint32_t first = (uint32_t)d->first[i], span = (uint32_t)i - first;
+#pragma unroll
+        for (int j0 = 0; j0 < kC; j0 += 16) {
+          float x[16];
+          if (j0 < jend) {
+            tmem_ld16(tl + kTmA + j0, x);
+            tmem_landed(x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float e = ex2(Gi - d->G[j0 + j]);
+              x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * e : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float* y = x + 8 * e;
+            *reinterpret_cast<uint4*>(sm + kA + row_chunk(i, j0 / 8 + e)) =
+                make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(a_ready);
+      }
+    }
+  } else {
+    // ======================== K~ = w k as three bf16 parts (8 bits each: their sum is exact)
+    const int t = tid - 10 * 32, r = t & 63, blk = t >> 6;
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
+      uint8_t* st = sm + (c % kStages) * kStageBytes;
+      ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+      if (ok && c > 0) ok = wait_or_abort_t<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+      if (!ok) break;
+      const float w = decay[c % kRing].W[r];
+      if (blk < KB) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 kk = *reinterpret_cast<const uint4*>(st + kKey + blk * kPair + row_chunk(r, j));
+          const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
+          uint32_t p0[4], p1[4], p2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
+            const float a = w == 0.f ? 0.f : w * __uint_as_float(in[e] << 16);
+            const float z = w == 0.f ? 0.f : w * __uint_as_float(in[e] & 0xffff0000u);
+            const uint32_t ah = __float_as_uint(a) & 0xffff0000u, zh = __float_as_uint(z) & 0xffff0000u;
+            const float ar = a - __uint_as_float(ah), zr = z - __uint_as_float(zh);
+            const uint32_t am = __float_as_uint(ar) & 0xffff0000u, zm = __float_as_uint(zr) & 0xffff0000u;
+            const float al = ar - __uint_as_float(am), zl = zr - __uint_as_float(zm);
+            p0[e] = (ah >> 16) | zh;
+            p1[e] = (am >> 16) | zm;
+            p2[e] = (__float_as_uint(al) >> 16) | (__float_as_uint(zl) & 0xffff0000u);
+          }
+          uint8_t* dst = sm + kKt + blk * kBlk + row_chunk(r, j);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
+          *reinterpret_cast<uint4*>(dst + 2 * kBlk) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4*>(dst + 4 * kBlk) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+        }
+      }
+      // values past the sequence's end meet weights of 0, but may hold anything: clear them
+      if (r >= rows - (int64_t)c * kC && 64 * blk < dv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(st + kV + blk * kBlk + r * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(kt_ready);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  drain_after_abort<kStages>(abort_flag, tid == kCopyWarp * 32, tid == kMmaWarp * 32, full, issued, bar_fin, p.err);
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Folds the segments of a (sequence, head) in order: seg_state[i] becomes the state before segment i.
+// One thread per four state values; fp32 throughout.
+constexpr int kMergeThreads = 128;
+__global__ void __launch_bounds__(kMergeThreads)
+linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu, float* __restrict__ seg_state,
+                    const float* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
+                    int elems, int parts) {
+  if (cu != nullptr && !offsets_ok(cu, B, T_tot)) return;
+  const int bh = blockIdx.x / parts, b = bh / H;
+  const int at = (blockIdx.x % parts * kMergeThreads + threadIdx.x) * 4;
+  const int64_t len = cu ? (int64_t)cu[b + 1] - cu[b] : T;
+  const int nchunks = (int)((len + kC - 1) / kC), last = nchunks > 0 ? (nchunks - 1) / seg_len : 0;
+  float4 S = h0 ? *reinterpret_cast<const float4*>(h0 + (int64_t)bh * elems + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float* p = seg_state + (int64_t)bh * nseg * elems + at;
+  const float* e = seg_decay + (int64_t)bh * nseg;
+  for (int i = 0; i < last; ++i, p += elems) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    *reinterpret_cast<float4*>(p) = S;
+    S = f4_fma(e[i], S, u);
+  }
+  *reinterpret_cast<float4*>(p) = S;
+}
+
+// Segments: only where at least half of the device would be idle, of 8 chunks at least, and so long that
+// all chunks together give each SM one.
+constexpr int kMinSplitChunks = 32, kMinSegChunks = 8;
+void segments(int B, int64_t T, int64_t T_tot, bool has_cu, int H, int sms, int* nseg, int* seg_len) {
+  const int64_t longest = (T + kC - 1) / kC;  // of a sequence, at most
+  *nseg = 1;
+  *seg_len = longest > 0 ? (int)longest : 1;
+  if ((int64_t)B * H * 2 > sms || longest < kMinSplitChunks) return;
+  const int64_t chunks = has_cu ? (T_tot + kC - 1) / kC : (int64_t)B * longest;
+  int64_t n = (chunks * H + sms - 1) / sms;
+  if (n < kMinSegChunks) n = kMinSegChunks;
+  if (n >= longest) return;
+  *nseg = (int)((longest + n - 1) / n);
+  *seg_len = (int)n;
+}
+
+struct DeviceState {
+  DeviceOnce once;
+  int sms[kMaxDevices] = {};
+};
+DeviceState g_state;
+
+template <int DK, bool GIVEUP>
+cudaError_t allow() {
+  cudaError_t e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, float, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 1, float, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  return e;
+}
+cudaError_t device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const cudaError_t e = g_state.once.run(dev, [dev] {
+    return cudaDeviceGetAttribute(&g_state.sms[dev], cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (e == cudaSuccess) *sms = g_state.sms[dev];
+  return e;
+}
+cudaError_t allow_all() {
+  static DeviceOnce once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  return once.run(dev, [] {
+    cudaError_t e = allow<64, false>();
+    if (e == cudaSuccess) e = allow<128, false>();
+    if (e == cudaSuccess) e = allow<64, true>();
+    if (e == cudaSuccess) e = allow<128, true>();
+    return e;
+  });
+}
+
+template <int DK, bool GIVEUP>
+cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)a.B * a.H * p.nseg);
+  if (p.nseg > 1) {
+    {
+      TraceScope ts("kda_linear_segments", st);
+      linear_chunk_kernel<DK, 1, float, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
+    }
+    const int elems = DK * a.dv, parts = elems / (4 * kMergeThreads);
+    TraceScope ts("kda_linear_merge", st);
+    linear_merge_kernel<<<(unsigned)(a.B * a.H * parts), kMergeThreads, 0, st>>>(
+        a.h0, a.cu_seqlens, p.seg_state, p.seg_decay, a.B, a.T, a.T_tot, a.H, p.nseg, p.seg_len, elems, parts);
+  }
+  {
+    TraceScope ts("kda_linear_chunk", st);
+    if (a.out_bf16) linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
+    else linear_chunk_kernel<DK, 0, float, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t linear_tc_workspace(int B, int64_t T, int H, int dk, int dv) {
+  int sms = 0;
+  if (device_sms(&sms) != cudaSuccess) return 0;
+  size_t most = 0;  // with and without offsets (T is then one sequence's length)
+  for (int has_cu = 0; has_cu < 2; ++has_cu) {
+    int nseg, seg_len;
+    segments(B, T, has_cu ? T : (int64_t)B * T, has_cu != 0, H, sms, &nseg, &seg_len);
+    const size_t n = nseg > 1 ? (size_t)B * H * nseg * ((size_t)dk * dv + 1) * sizeof(float) : 0;
+    if (n > most) most = n;
+  }
+  return align_up(most, 256);
+}
+
+cudaError_t linear_tc_launch(const LinearArgs& a, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = allow_all();
+  if (e != cudaSuccess) return e;
+  Params p{};
+  p.g = a.g; p.g_per_token = a.g_per_token; p.h0 = a.h0; p.cu = a.cu_seqlens; p.out = a.out; p.hT = a.hT;
+  p.B = a.B; p.T = a.T; p.T_tot = a.T_tot; p.H = a.H; p.dv = a.dv; p.scale = a.scale; p.err = a.err;
+  segments(a.B, a.T, a.T_tot, a.cu_seqlens != nullptr, a.H, sms, &p.nseg, &p.seg_len);
+  p.seg_state = static_cast<float*>(a.workspace);
+  p.seg_decay = p.seg_state + (size_t)a.B * a.H * p.nseg * a.dk * a.dv;
+  Maps maps{};
+  if (a.T_tot > 0 &&
+      (!tensor_map_2d(&maps.q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dk, a.q_stride * 2, kC, 64) ||
+       !tensor_map_2d(&maps.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dk, a.k_stride * 2, kC, 64) ||
+       !tensor_map_2d(&maps.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dv, a.v_stride * 2, kC, 64)))
+    return cudaErrorInvalidValue;
+  if (a.dk == 64) return a.give_up ? launch<64, true>(a, maps, p, st) : launch<64, false>(a, maps, p, st);
+  return a.give_up ? launch<128, true>(a, maps, p, st) : launch<128, false>(a, maps, p, st);
+}
+
+}  // namespace kda

@@ -135,5 +135,41 @@ __device__ __forceinline__ bool wait_or_abort_t(uint64_t* bar, uint32_t parity, 
   }
 }
 
+// Waits for this thread's TMEM loads; the values pass through, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_landed(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_landed(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+// At the end of a CTA (all threads, after a barrier, so that the flag is final): if a wait ran out, the
+// copies and MMAs that may still be in flight are waited for, with a limit, before shared memory and TMEM
+// are given back.  Without an abort every MMA, and with it every copy, was waited for by its readers.
+template <int STAGES>
+__device__ __forceinline__ void drain_after_abort(volatile int* abort_flag, bool copier, bool multiplier, uint64_t* full,
+                                                  int64_t issued, uint64_t* bar_fin, unsigned int* err) {
+  if (!*abort_flag) return;
+  if (copier) {
+    for (int64_t l = issued > STAGES ? issued - STAGES : 0; l < issued; ++l)
+      mbar_wait(&full[l % STAGES], (uint32_t)((l / STAGES) & 1));
+    atomicOr(err, KDA_DEVERR_WAIT_TIMEOUT);
+  }
+  if (multiplier) {
+    mma_commit(bar_fin);
+    mbar_wait(bar_fin, 0);
+  }
+  __syncthreads();
+}
+
 }  // namespace tcx
 }  // namespace kda
