@@ -38,7 +38,7 @@ using namespace tcx;
 
 constexpr int kC = 64;                      // tokens of a chunk
 constexpr int kThreads = 512;
-constexpr int kStateThreads = 256, kMaskThreads = 64, kKeyThreads = 128;
+constexpr int kStateWarps = 8, kMaskWarps = 2, kKeyWarps = 4;
 constexpr int kCopyWarp = 14, kMmaWarp = 15;
 constexpr int kStages = 3;
 // a stage: [Q | K] of the first 64 channels, [Q | K] of the second, V of the first 64 channels, of the second
@@ -213,16 +213,16 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   if (tid == 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 2);
-      mbar_init(&empty[i], 1 + kStateThreads / 32);
+      mbar_init(&empty[i], 1 + kStateWarps);
     }
     mbar_init(a_done, 1);
-    mbar_init(a_ready, kMaskThreads);
-    mbar_init(kt_ready, kKeyThreads);
+    mbar_init(a_ready, kMaskWarps);
+    mbar_init(kt_ready, kKeyWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], kStateThreads);
+      mbar_init(&u_empty[i], kStateWarps);
     }
-    mbar_init(s_ready, kStateThreads);
+    mbar_init(s_ready, kStateWarps);
     mbar_init(o_full, 1);
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -249,8 +249,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
     bool ok = true;
     for (; issued < nc; ++issued) {
       const int c = issued, s = c % kStages;
-      if (c >= kStages) ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((c / kStages - 1) & 1), abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      if (c >= kStages) ok = warp_wait<GIVEUP>(&empty[s], (uint32_t)((c / kStages - 1) & 1), abort_flag);
       if (!ok) break;
       if (lane == 0) {
         uint8_t* st = sm + s * kStageBytes;
@@ -266,8 +265,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       bool emptied;
       total += chunk_decay(&decay[c % kRing], g0, g1, (int)(left < kC ? left : kC), lane, emptied);
       any |= emptied;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
+      warp_arrive(&full[s]);
       if (c + 1 < nc) {
         g0 = load_g(c + 1, 2 * lane);
         g1 = load_g(c + 1, 2 * lane + 1);
@@ -356,14 +354,12 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(s_ready);
+        warp_arrive(s_ready);
       }
-      ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
       if (!ok) break;
-      if (lane == 0) mbar_arrive(&empty[c % kStages]);  // so that the stage's phase cannot pass by unseen
-      ok = wait_or_abort_t<GIVEUP>(&u_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      warp_arrive(&empty[c % kStages]);  // so that the stage's phase cannot pass by unseen
+      ok = warp_wait<GIVEUP>(&u_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
       if (!ok) break;
       tc_fence_after();
       const float all = d->all;
@@ -376,15 +372,15 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         for (int j = 0; j < 16; ++j) S[16 * i + j] = fmaf(all, S[16 * i + j], u[j]);
       }
       tc_fence_before();
-      mbar_arrive(&u_empty[c & 1]);
+      warp_arrive(&u_empty[c & 1]);
       if constexpr (MODE == 0) {
-        ok = wait_or_abort_t<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        ok = warp_wait<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
+          if (!ok) break;
         tc_fence_after();
         const int64_t left = rows - (int64_t)c * kC;
-        Tout* dst = static_cast<Tout*>(p.out) + ((t0 + (int64_t)c * kC) * H + h) * dv + row;
-#pragma unroll
+        const int64_t out_step = (int64_t)H * dv;
+        Tout* dst = static_cast<Tout*>(p.out) + ((t0 + (int64_t)c * kC + 32 * half) * H + h) * dv + row;
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int tok = 32 * half + 16 * i;
           float x[16], y[16];
@@ -395,7 +391,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float o = p.scale * fmaf(d->E[tok + j], x[j], y[j]);
-            if (live && tok + j < left) dst[(int64_t)(tok + j) * H * dv] = from_f32<Tout>(o);
+            if (live && tok + j < left) *dst = from_f32<Tout>(o);
+            dst += out_step;
           }
         }
         tc_fence_before();
@@ -417,16 +414,15 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       bool ok = true;
       for (int c = 0; c < nc; ++c) {
         const Decay* d = &decay[c % kRing];
-        ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-        ok = ok && wait_or_abort_t<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
+        ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+        ok = ok && warp_wait<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
         // the products that read A of the chunk before
-        if (ok && c > 0) ok = wait_or_abort_t<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (ok && c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+          if (!ok) break;
         tc_fence_after();
         const float Gi = d->G[i];
         const uint32_t first = (uint32_t)d->first[i], span = (uint32_t)i - first;
-#pragma unroll
+#pragma unroll 1
         for (int j0 = 0; j0 < kC; j0 += 16) {
           float x[16];
           if (j0 < jend) {
@@ -450,7 +446,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(a_ready);
+        warp_arrive(a_ready);
       }
     }
   } else {
@@ -459,12 +455,12 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
       uint8_t* st = sm + (c % kStages) * kStageBytes;
-      ok = wait_or_abort_t<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-      if (ok && c > 0) ok = wait_or_abort_t<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+      ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+      if (ok && c > 0) ok = warp_wait<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
       if (!ok) break;
       const float w = decay[c % kRing].W[r];
       if (blk < KB) {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 8; ++j) {
           const uint4 kk = *reinterpret_cast<const uint4*>(st + kKey + blk * kPair + row_chunk(r, j));
           const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
@@ -495,7 +491,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           *reinterpret_cast<uint4*>(st + kV + blk * kBlk + r * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
-      mbar_arrive(kt_ready);
+      warp_arrive(kt_ready);
     }
   }
   tc_fence_before();

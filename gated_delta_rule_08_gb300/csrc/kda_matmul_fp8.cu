@@ -10,7 +10,7 @@
 //
 // Two orientations:
 //  matmul_fp8_tall: 128 activation rows x 256 weight rows per tile, one CTA per SM walking over tiles;
-//    a thread owns one activation row and one 128-column block, whose scale is one number.
+//    a thread owns part of one activation row, whose scale for a block of K is one number.
 //  matmul_fp8_flat: 128 weight rows x BN activation rows per tile, for few rows: the weight is then the
 //    operand with 128 rows and nothing is padded but the activations (to BN).  Bound by the weight's
 //    bytes, so the K blocks of a tile are split over the CTAs of a cluster, which add their partial
@@ -63,10 +63,18 @@ struct Maps {
 
 // ------------------------------------------------------------------------------ many rows
 constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
-constexpr int kPromote = 256;  // warps 0-7: read accumulators, scale, store; warp 8 copies, warp 9 multiplies
-constexpr int kTallThreads = kPromote + 64;
+// Warps 0-7 read accumulators, scale, add and store: a thread owns 128 columns of a row.  Warp 8 copies.  Warps 9
+// and 10 issue the MMAs, of even and odd blocks: a thread's wait on a barrier queues behind the MMAs that it has
+// issued, so one thread alone leaves the tensor pipe idle for half of the time (1060 clocks a block instead of 512).
+// Warp 11 only completes their group of four, which hands its registers to the first eight.
+constexpr int kPromoteWarps = 8, kTallCopyWarp = 8, kTallMmaWarp = 9, kTallThreads = 384;
+constexpr int kPromoteRegs = 216, kOtherRegs = 72;
+static_assert(kPromoteWarps * 32 * kPromoteRegs + 4 * 32 * kOtherRegs <= kTallThreads * 168, "registers of the launch");
 constexpr uint32_t kTallA = kTallM * kK, kTallStage = (kTallM + kTallN) * kK;
-constexpr uint32_t kTallBar = kTallStages * kTallStage;
+// Each promoting warp's 32 rows x 128 bytes of output, so that rows are stored as whole lines: a thread's own row,
+// 16 bytes at a time, took 8400 clocks a tile.
+constexpr uint32_t kTallOut = kTallStages * kTallStage, kTallOutWarp = 32 * 128;
+constexpr uint32_t kTallBar = kTallOut + kPromoteWarps * kTallOutWarp;
 constexpr uint32_t kTallSmem = kTallBar + 256 + 1024;
 
 template <typename Tout, bool GIVEUP>
@@ -95,9 +103,9 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kPromote);
+      mbar_init(&acc_empty[i], kPromoteWarps);
     }
-    mbar_init(bar_fin, 1);
+    mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -105,10 +113,11 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int64_t issued = 0;  // stages whose copies warp 8 has started
+  int64_t issued = 0;  // stages whose copies have been started
 
-  if (warp == 8) {
-    if (lane == 0) {
+  if (warp >= kPromoteWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kTallCopyWarp && lane == 0) {
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         const int m0 = tile % tiles_m * kTallM, n0 = tile / tiles_m * kTallN;
@@ -123,14 +132,14 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
           tma_load_2d(st + kTallA, &maps.b, kb * kK, n0, &full[s]);
         }
       }
-    }
-  } else if (warp == 9) {
-    if (lane == 0) {
+    } else if ((warp == kTallMmaWarp || warp == kTallMmaWarp + 1) && lane == 0) {
+      const int buf = warp - kTallMmaWarp;
       int64_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
-          const int s = (int)(it % kTallStages), buf = (int)(it & 1);
+          if ((it & 1) != buf) continue;
+          const int s = (int)(it % kTallStages);
           ok = wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
           if (ok && it >= 2) ok = wait_or_abort_t<GIVEUP>(&acc_empty[buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
           if (!ok) break;
@@ -143,19 +152,21 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       }
     }
   } else {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tl = tmem_lane(tmem, warp) + 128 * half;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
+    const int col = 128 * (warp >> 2), row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem_lane(tmem, warp) + col;
     int64_t it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + 128 * half;
-      // rows and blocks past the edges take the last one's scale; their products are zero
+      const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + col;
+      // rows and blocks past the edges take another's scale; their products are zero
       const float* pa = a_scale + (int64_t)(m < M ? m : M - 1) * nkb;
       const float* pb = b_scale + (int64_t)(n0 < N ? n0 / 128 : 0) * nkb;
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
       float sa = __ldg(pa), sb = __ldg(pb);
+#pragma unroll 1
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int buf = (int)(it & 1);
         const float s = sa * sb;
@@ -164,55 +175,78 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
           sb = __ldg(pb + kb + 1);
         }
         ok = wait_or_abort_t<GIVEUP>(&acc_full[buf], (uint32_t)((it / 2) & 1), abort_flag);
-        // the loads below are collective: a warp leaves together
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, ok);  // the loads below are collective: a warp leaves together
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          tmem_ld32(tl + 256 * buf + 32 * c, v);
+        for (int c = 0; c < 2; ++c) {
+          float v[32], w[32];
+          tmem_ld32(tl + 256 * buf + 64 * c, v);
+          tmem_ld32(tl + 256 * buf + 64 * c + 32, w);
           tmem_landed(v);
-          if (c == 3) {
+          tmem_landed(w);
+          if (c == 1) {
             tc_fence_before();
-            mbar_arrive(&acc_empty[buf]);
+            warp_arrive(&acc_empty[buf]);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], s, s, v[2 * i], v[2 * i + 1]);
-        }
-      }
-      if (ok && m < M) {
-        Tout* dst = out + (int64_t)m * N + n0;
-        if (N % 8 == 0) {  // 16-byte aligned pieces of eight
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (n0 + 8 * i < N) {
-              const float2 x0 = split2(acc[4 * i]), x1 = split2(acc[4 * i + 1]), x2 = split2(acc[4 * i + 2]),
-                           x3 = split2(acc[4 * i + 3]);
-              if constexpr (sizeof(Tout) == 4) {
-                reinterpret_cast<float4*>(dst + 8 * i)[0] = make_float4(x0.x, x0.y, x1.x, x1.y);
-                reinterpret_cast<float4*>(dst + 8 * i)[1] = make_float4(x2.x, x2.y, x3.x, x3.y);
-              } else {
-                const __nv_bfloat162 p[4] = {__floats2bfloat162_rn(x0.x, x0.y), __floats2bfloat162_rn(x1.x, x1.y),
-                                             __floats2bfloat162_rn(x2.x, x2.y), __floats2bfloat162_rn(x3.x, x3.y)};
-                *reinterpret_cast<uint4*>(dst + 8 * i) = *reinterpret_cast<const uint4*>(p);
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float2 x = split2(acc[i]);
-            if (n0 + 2 * i < N) dst[2 * i] = from_f32<Tout>(x.x);
-            if (n0 + 2 * i + 1 < N) dst[2 * i + 1] = from_f32<Tout>(x.y);
+            fma2(acc[32 * c + i], s, s, v[2 * i], v[2 * i + 1]);
+            fma2(acc[32 * c + 16 + i], s, s, w[2 * i], w[2 * i + 1]);
           }
         }
+      }
+      if (!ok) break;
+      // by 128 bytes of columns: to shared memory with the row's 16-byte pieces permuted, then out by rows
+      constexpr int kCols = 128 / sizeof(Tout), kPiece = 16 / sizeof(Tout);
+      uint8_t* stage = sm + kTallOut + warp * kTallOutWarp;
+      const int m_warp = m - lane;
+#pragma unroll
+      for (int c = 0; c < 128 / kCols; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 w;
+          if constexpr (sizeof(Tout) == 4) {
+            const float2 x = split2(acc[(c * kCols + 4 * i) / 2]), y = split2(acc[(c * kCols + 4 * i) / 2 + 1]);
+            w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+          } else {
+            uint32_t q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = split2(acc[(c * kCols + 8 * i) / 2 + e]);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+              q[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            w = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+          *reinterpret_cast<uint4*>(stage + row_chunk(lane, i)) = w;
+        }
+        __syncwarp();
+        const int nc = n0 + c * kCols;
+        if (N % kPiece == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), n = nc + (lane & 7) * kPiece;
+            if (m_warp + r < M && n < N)
+              *reinterpret_cast<uint4*>(out + (int64_t)(m_warp + r) * N + n) =
+                  *reinterpret_cast<const uint4*>(stage + row_chunk(r, lane & 7));
+          }
+        } else {  // rows off the 16-byte boundaries: value by value
+          for (int r = 0; r < 32 && m_warp + r < M; ++r)
+#pragma unroll
+            for (int e = lane; e < kCols; e += 32)
+              if (nc + e < N)
+                out[(int64_t)(m_warp + r) * N + nc + e] =
+                    *reinterpret_cast<const Tout*>(stage + row_chunk(r, e / kPiece) + e % kPiece * sizeof(Tout));
+        }
+        __syncwarp();
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  drain_after_abort<kTallStages>(abort_flag, tid == 8 * 32, tid == 9 * 32, full, issued, bar_fin, err);
+  drain_after_abort<kTallStages>(abort_flag, tid == kTallCopyWarp * 32,
+                                 tid == kTallMmaWarp * 32 || tid == (kTallMmaWarp + 1) * 32, full, issued, bar_fin, err);
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -282,7 +316,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
     }
     for (int i = 0; i < F::kBufs; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], 4);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -360,7 +394,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         tmem_landed(v);
         if (c == BN / 16 - 1) {
           tc_fence_before();
-          mbar_arrive(&acc_empty[buf]);
+          warp_arrive(&acc_empty[buf]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -135,6 +135,21 @@ __device__ __forceinline__ bool wait_or_abort_t(uint64_t* bar, uint32_t parity, 
   }
 }
 
+// The wait of a whole warp: one lane polls, so that 31 others do not load shared memory and the issue
+// slots that the working warps need.  Every lane returns the same answer.
+template <bool kGiveUp>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// One arrival for a whole warp, after all its lanes' work (each has executed the fence that work needs).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Waits for this thread's TMEM loads; the values pass through, so that nothing reads them earlier.
 __device__ __forceinline__ void tmem_landed(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
