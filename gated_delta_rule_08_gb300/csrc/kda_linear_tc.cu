@@ -282,7 +282,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       bool ok = true;
       auto scores = [&](int c) {  // D_A of chunk c
         const int s = c % kStages;
-        if (!wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag)) return false;
+        if (!spin_or_abort<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag)) return false;
         tc_fence_after();
         const uint8_t* st = sm + s * kStageBytes;
         const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
@@ -299,8 +299,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int s = c % kStages;
         const uint8_t* st = sm + s * kStageBytes;
         const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
-        ok = wait_or_abort_t<GIVEUP>(kt_ready, (uint32_t)(c & 1), abort_flag);
-        if (ok && c >= 2) ok = wait_or_abort_t<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+        ok = spin_or_abort<GIVEUP>(kt_ready, (uint32_t)(c & 1), abort_flag);
+        if (ok && c >= 2) ok = spin_or_abort<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -311,9 +311,9 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
                         i + j > 0);
         mma_commit(&u_full[c & 1]);
         if constexpr (MODE == 0) {
-          ok = wait_or_abort_t<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
+          ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
           // D_1 and D_2 of the chunk before have been read once S^T is there
-          ok = ok && wait_or_abort_t<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
+          ok = ok && spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll

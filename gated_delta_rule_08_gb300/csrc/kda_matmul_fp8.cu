@@ -63,19 +63,26 @@ struct Maps {
 
 // ------------------------------------------------------------------------------ many rows
 constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
-// Warps 0-7 read accumulators, scale, add and store: a thread owns 128 columns of a row.  Warp 8 copies.  Warps 9
-// and 10 issue the MMAs, of even and odd blocks: a thread's wait on a barrier queues behind the MMAs that it has
-// issued, so one thread alone leaves the tensor pipe idle for half of the time (1060 clocks a block instead of 512).
-// Warp 11 only completes their group of four, which hands its registers to the first eight.
-constexpr int kPromoteWarps = 8, kTallCopyWarp = 8, kTallMmaWarp = 9, kTallThreads = 384;
-constexpr int kPromoteRegs = 216, kOtherRegs = 72;
-static_assert(kPromoteWarps * 32 * kPromoteRegs + 4 * 32 * kOtherRegs <= kTallThreads * 168, "registers of the launch");
+// The tile's two halves of 128 columns are worked on apart, each with two accumulators: while one set of four
+// warps adds a block's half, the other half's MMAs and the next block's run, and the two sets stay out of step, so
+// that one's TMEM loads lie beside the other's arithmetic.
+// Warps 0-3 and 4-7 read accumulators, scale, add and store: a thread owns 128 columns of a row.  Warp 8 copies,
+// warp 9 fetches the scales.  Warps 12-15 issue the MMAs, one warp to an accumulator: a commit takes 70 clocks of the
+// thread that issues it and a wait behind it 150, so one thread alone would leave the tensor pipe idle in between.
+// Warps 10 and 11 only complete their group of four; the groups hand their registers to the first eight warps.
+constexpr int kPromoteWarps = 8, kTallCopyWarp = 8, kTallScaleWarp = 9, kTallMmaWarp = 12, kTallThreads = 512;
+constexpr int kPromoteRegs = 208, kOtherRegs = 48;
+static_assert(kPromoteWarps * 32 * kPromoteRegs + 8 * 32 * kOtherRegs <= kTallThreads * 128, "registers of the launch");
 constexpr uint32_t kTallA = kTallM * kK, kTallStage = (kTallM + kTallN) * kK;
-// Each promoting warp's 32 rows x 128 bytes of output, so that rows are stored as whole lines: a thread's own row,
+// Each promoting warp's 16 rows x 128 bytes of output, so that rows are stored as whole lines: a thread's own row,
 // 16 bytes at a time, took 8400 clocks a tile.
-constexpr uint32_t kTallOut = kTallStages * kTallStage, kTallOutWarp = 32 * 128;
-constexpr uint32_t kTallBar = kTallOut + kPromoteWarps * kTallOutWarp;
+constexpr uint32_t kTallOut = kTallStages * kTallStage, kTallOutWarp = 16 * 128;
+// The activations' scales of a tile's rows, for groups of eight blocks: [2][8][132], and the weights' [2][8][2].
+constexpr int kGroup = 8, kScaleLd = kTallM + 4;
+constexpr uint32_t kTallSa = kTallOut + kPromoteWarps * kTallOutWarp, kTallSb = kTallSa + 2 * kGroup * kScaleLd * 4;
+constexpr uint32_t kTallBar = kTallSb + 2 * kGroup * 2 * 4;
 constexpr uint32_t kTallSmem = kTallBar + 256 + 1024;
+static_assert(kTallSmem <= 232448, "shared memory of a CTA");
 
 template <typename Tout, bool GIVEUP>
 __global__ void __launch_bounds__(kTallThreads, 1)
@@ -84,12 +91,15 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kTallBar);  // [stages] tiles landed
-  uint64_t* empty = full + kTallStages;                         // [stages] tiles read by their MMAs
-  uint64_t* acc_full = empty + kTallStages;                     // [2] accumulator complete
-  uint64_t* acc_empty = acc_full + 2;                           // [2] accumulator read
-  uint64_t* bar_fin = acc_empty + 2;
+  uint64_t* mma_done = full + kTallStages;                      // [half][stages] accumulator complete, stage read
+  uint64_t* acc_empty = mma_done + 2 * kTallStages;             // [half][2] accumulator read
+  uint64_t* sc_full = acc_empty + 4;                            // [2] group of scales there
+  uint64_t* sc_empty = sc_full + 2;                             // [2] group of scales read
+  uint64_t* bar_fin = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_sa = reinterpret_cast<float*>(sm + kTallSa);
+  float* s_sb = reinterpret_cast<float*>(sm + kTallSb);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == 0) {
@@ -99,13 +109,15 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   if (tid == 32) {
     for (int i = 0; i < kTallStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&mma_done[i], 1);
+      mbar_init(&mma_done[kTallStages + i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&acc_empty[i], kPromoteWarps / 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kPromoteWarps);
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], kPromoteWarps);
     }
-    mbar_init(bar_fin, 2);
+    mbar_init(bar_fin, 4);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -123,8 +135,11 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         const int m0 = tile % tiles_m * kTallM, n0 = tile / tiles_m * kTallN;
         for (int kb = 0; kb < nkb && ok; ++kb, ++issued) {
           const int s = (int)(issued % kTallStages);
-          if (issued >= kTallStages)
-            ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((issued / kTallStages - 1) & 1), abort_flag);
+          if (issued >= kTallStages) {
+            const uint32_t ph = (uint32_t)((issued / kTallStages - 1) & 1);
+            ok = spin_or_abort<GIVEUP>(&mma_done[s], ph, abort_flag) &&
+                 spin_or_abort<GIVEUP>(&mma_done[kTallStages + s], ph, abort_flag);
+          }
           if (!ok) break;
           uint8_t* st = sm + s * kTallStage;
           mbar_arrive_expect_tx(&full[s], kTallStage);
@@ -132,69 +147,111 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
           tma_load_2d(st + kTallA, &maps.b, kb * kK, n0, &full[s]);
         }
       }
-    } else if ((warp == kTallMmaWarp || warp == kTallMmaWarp + 1) && lane == 0) {
-      const int buf = warp - kTallMmaWarp;
+    } else if (warp >= kTallMmaWarp && lane == 0) {
+      const int half = (warp - kTallMmaWarp) >> 1, buf = warp & 1;
       int64_t it = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
           if ((it & 1) != buf) continue;
           const int s = (int)(it % kTallStages);
-          ok = wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
-          if (ok && it >= 2) ok = wait_or_abort_t<GIVEUP>(&acc_empty[buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
+          ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
+          if (ok && it >= 2)
+            ok = spin_or_abort<GIVEUP>(&acc_empty[2 * half + buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint8_t* st = sm + s * kTallStage;
-          mma_block(tmem + 256 * buf, st, st + kTallA, idesc_e4m3(kTallM, kTallN));
-          mma_commit(&empty[s]);
-          mma_commit(&acc_full[buf]);
+          mma_block(tmem + 256 * buf + 128 * half, st, st + kTallA + half * 128 * kK, idesc_e4m3(kTallM, kTallN / 2));
+          mma_commit(&mma_done[half * kTallStages + s]);
+        }
+      }
+    } else if (warp == kTallScaleWarp) {
+      int64_t grp = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        // rows and blocks past the edges take another's scale; their products are zero
+        const int m0 = tile % tiles_m * kTallM, nb0 = tile / tiles_m * (kTallN / 128), nb = (N + 127) / 128;
+        for (int k0 = 0; k0 < nkb; k0 += kGroup, ++grp) {
+          const int slot = (int)(grp & 1), kb = k0 + (lane & 7);
+          if (grp >= 2) ok = warp_wait<GIVEUP>(&sc_empty[slot], (uint32_t)((grp / 2 - 1) & 1), abort_flag);
+          if (!ok) break;
+          float* d = s_sa + slot * kGroup * kScaleLd + (lane & 7) * kScaleLd;
+          if (kb < nkb) {
+#pragma unroll 8
+            for (int r = lane >> 3; r < kTallM; r += 4) {
+              const int m = m0 + r;
+              d[r] = __ldg(a_scale + (int64_t)(m < M ? m : M - 1) * nkb + kb);
+            }
+            if (lane < 16) {
+              const int j = nb0 + (lane >> 3);
+              s_sb[(slot * kGroup + (lane & 7)) * 2 + (lane >> 3)] = __ldg(b_scale + (int64_t)(j < nb ? j : nb - 1) * nkb + kb);
+            }
+          }
+          warp_arrive(&sc_full[slot]);
         }
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
-    const int col = 128 * (warp >> 2), row = (warp & 3) * 32 + lane;
-    const uint32_t tl = tmem_lane(tmem, warp) + col;
-    int64_t it = 0;
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem_lane(tmem, warp) + 128 * half;
+    uint64_t* my_done = mma_done + kTallStages * half;
+    uint64_t* my_empty = acc_empty + 2 * half;
+    int64_t it = 0, grp = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + col;
-      // rows and blocks past the edges take another's scale; their products are zero
-      const float* pa = a_scale + (int64_t)(m < M ? m : M - 1) * nkb;
-      const float* pb = b_scale + (int64_t)(n0 < N ? n0 / 128 : 0) * nkb;
+      const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + 128 * half;
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float sa = __ldg(pa), sb = __ldg(pb);
+      // In steps of 32 columns: the next step's load is under way while this one is added, across blocks too
+      // (a barrier that is already complete still takes some 250 clocks to be seen).
+      float v[32], w[32];
+      auto add = [&](const float (&x)[32], int c, float s) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], s, s, x[2 * i], x[2 * i + 1]);
+      };
+      auto wait_block = [&](int64_t i) {  // the loads are collective: a warp leaves together
+        return __all_sync(0xffffffffu, spin_or_abort<GIVEUP>(&my_done[i % kTallStages], (uint32_t)((i / kTallStages) & 1), abort_flag));
+      };
+      ok = wait_block(it);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tl + 256 * (uint32_t)(it & 1), v);
 #pragma unroll 1
       for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int buf = (int)(it & 1);
-        const float s = sa * sb;
-        if (kb + 1 < nkb) {
-          sa = __ldg(pa + kb + 1);
-          sb = __ldg(pb + kb + 1);
+        const uint32_t ta = tl + 256 * (uint32_t)(it & 1);
+        const bool more = kb + 1 < nkb;
+        const int slot = (int)(grp & 1), kg = kb % kGroup;
+        if (kg == 0) {
+          ok = __all_sync(0xffffffffu, spin_or_abort<GIVEUP>(&sc_full[slot], (uint32_t)((grp / 2) & 1), abort_flag));
+          if (!ok) break;
         }
-        ok = wait_or_abort_t<GIVEUP>(&acc_full[buf], (uint32_t)((it / 2) & 1), abort_flag);
-        ok = __all_sync(0xffffffffu, ok);  // the loads below are collective: a warp leaves together
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float v[32], w[32];
-          tmem_ld32(tl + 256 * buf + 64 * c, v);
-          tmem_ld32(tl + 256 * buf + 64 * c + 32, w);
-          tmem_landed(v);
-          tmem_landed(w);
-          if (c == 1) {
-            tc_fence_before();
-            warp_arrive(&acc_empty[buf]);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            fma2(acc[32 * c + i], s, s, v[2 * i], v[2 * i + 1]);
-            fma2(acc[32 * c + 16 + i], s, s, w[2 * i], w[2 * i + 1]);
-          }
+        const float s = s_sa[(slot * kGroup + kg) * kScaleLd + row] * s_sb[(slot * kGroup + kg) * 2 + half];
+        tmem_landed(v);
+        tmem_ld32(ta + 32, w);
+        add(v, 0, s);
+        tmem_landed(w);
+        tmem_ld32(ta + 64, v);
+        add(w, 1, s);
+        tmem_landed(v);
+        tmem_ld32(ta + 96, w);
+        const bool seen = !GIVEUP && more && mbar_test_wait(&my_done[(it + 1) % kTallStages], (uint32_t)(((it + 1) / kTallStages) & 1));
+        add(v, 2, s);
+        tmem_landed(w);
+        tc_fence_before();
+        warp_arrive(&my_empty[it & 1]);
+        if (kg == kGroup - 1 || !more) {
+          warp_arrive(&sc_empty[slot]);
+          ++grp;
         }
+        if (more) {
+          if (!__all_sync(0xffffffffu, seen)) ok = wait_block(it + 1);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld32(tl + 256 * (uint32_t)((it + 1) & 1), v);
+        }
+        add(w, 3, s);
       }
       if (!ok) break;
       // by 128 bytes of columns: to shared memory with the row's 16-byte pieces permuted, then out by rows
@@ -203,50 +260,54 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       const int m_warp = m - lane;
 #pragma unroll
       for (int c = 0; c < 128 / kCols; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 w;
-          if constexpr (sizeof(Tout) == 4) {
-            const float2 x = split2(acc[(c * kCols + 4 * i) / 2]), y = split2(acc[(c * kCols + 4 * i) / 2 + 1]);
-            w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
-          } else {
-            uint32_t q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 x = split2(acc[(c * kCols + 8 * i) / 2 + e]);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-              q[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            w = make_uint4(q[0], q[1], q[2], q[3]);
-          }
-          *reinterpret_cast<uint4*>(stage + row_chunk(lane, i)) = w;
-        }
-        __syncwarp();
         const int nc = n0 + c * kCols;
-        if (N % kPiece == 0) {
+        for (int h = 0; h < 2; ++h) {  // rows 0-15, then 16-31 of the warp
+          if ((lane >> 4) == h) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3), n = nc + (lane & 7) * kPiece;
-            if (m_warp + r < M && n < N)
-              *reinterpret_cast<uint4*>(out + (int64_t)(m_warp + r) * N + n) =
-                  *reinterpret_cast<const uint4*>(stage + row_chunk(r, lane & 7));
+            for (int i = 0; i < 8; ++i) {
+              uint4 w4;
+              if constexpr (sizeof(Tout) == 4) {
+                const float2 x = split2(acc[(c * kCols + 4 * i) / 2]), y = split2(acc[(c * kCols + 4 * i) / 2 + 1]);
+                w4 = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+              } else {
+                uint32_t q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 x = split2(acc[(c * kCols + 8 * i) / 2 + e]);
+                  const __nv_bfloat162 hh = __floats2bfloat162_rn(x.x, x.y);
+                  q[e] = *reinterpret_cast<const uint32_t*>(&hh);
+                }
+                w4 = make_uint4(q[0], q[1], q[2], q[3]);
+              }
+              *reinterpret_cast<uint4*>(stage + row_chunk(lane & 15, i)) = w4;
+            }
           }
-        } else {  // rows off the 16-byte boundaries: value by value
-          for (int r = 0; r < 32 && m_warp + r < M; ++r)
+          __syncwarp();
+          const int m_half = m_warp + 16 * h;
+          if (N % kPiece == 0) {
 #pragma unroll
-            for (int e = lane; e < kCols; e += 32)
-              if (nc + e < N)
-                out[(int64_t)(m_warp + r) * N + nc + e] =
-                    *reinterpret_cast<const Tout*>(stage + row_chunk(r, e / kPiece) + e % kPiece * sizeof(Tout));
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * i + (lane >> 3), n = nc + (lane & 7) * kPiece;
+              if (m_half + r < M && n < N)
+                *reinterpret_cast<uint4*>(out + (int64_t)(m_half + r) * N + n) =
+                    *reinterpret_cast<const uint4*>(stage + row_chunk(r, lane & 7));
+            }
+          } else {  // rows off the 16-byte boundaries: value by value
+            for (int r = 0; r < 16 && m_half + r < M; ++r)
+#pragma unroll
+              for (int e = lane; e < kCols; e += 32)
+                if (nc + e < N)
+                  out[(int64_t)(m_half + r) * N + nc + e] =
+                      *reinterpret_cast<const Tout*>(stage + row_chunk(r, e / kPiece) + e % kPiece * sizeof(Tout));
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  drain_after_abort<kTallStages>(abort_flag, tid == kTallCopyWarp * 32,
-                                 tid == kTallMmaWarp * 32 || tid == (kTallMmaWarp + 1) * 32, full, issued, bar_fin, err);
+  drain_after_abort<kTallStages>(abort_flag, tid == kTallCopyWarp * 32, warp >= kTallMmaWarp && lane == 0, full, issued, bar_fin, err);
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -333,7 +394,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       bool ok = true;
       for (; issued < cnt; ++issued) {
         const int it = issued, s = it % F::kStages;
-        if (it >= F::kStages) ok = wait_or_abort_t<GIVEUP>(&empty[s], (uint32_t)((it / F::kStages - 1) & 1), abort_flag);
+        if (it >= F::kStages) ok = spin_or_abort<GIVEUP>(&empty[s], (uint32_t)((it / F::kStages - 1) & 1), abort_flag);
         if (!ok) break;
         uint8_t* st = sm + s * F::kStage;
         mbar_arrive_expect_tx(&full[s], F::kStage);
@@ -346,9 +407,9 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       bool ok = true;
       for (int it = 0; it < cnt && ok; ++it) {
         const int s = it % F::kStages, buf = it % F::kBufs;
-        ok = wait_or_abort_t<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
+        ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
         if (ok && it >= F::kBufs)
-          ok = wait_or_abort_t<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
+          ok = spin_or_abort<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint8_t* st = sm + s * F::kStage;
@@ -383,7 +444,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         if (lane + 32 * i < BN) fw[lane + 32 * i] = f[i];
       __syncwarp();
       if (it + 1 < cnt) fetch(it + 1);
-      ok = wait_or_abort_t<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
+      ok = spin_or_abort<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();

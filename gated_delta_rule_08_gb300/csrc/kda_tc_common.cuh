@@ -135,12 +135,32 @@ __device__ __forceinline__ bool wait_or_abort_t(uint64_t* bar, uint32_t parity, 
   }
 }
 
-// The wait of a whole warp: one lane polls, so that 31 others do not load shared memory and the issue
-// slots that the working warps need.  Every lane returns the same answer.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// wait_or_abort_t for hand-overs that take less than a microsecond: polls first (a poll takes 15 clocks),
+// because a thread that try_wait has suspended comes back some hundreds of clocks late.
+template <bool kGiveUp>
+__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if constexpr (!kGiveUp) {
+    for (int i = 0; i < 2048; ++i) {
+      if (mbar_test_wait(bar, parity)) return true;
+      if ((i & 63) == 63 && *abort_flag) return false;
+    }
+  }
+  return wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
+}
+// The same for a whole warp: one lane polls.  Every lane returns the same answer.
 template <bool kGiveUp>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
+  if ((threadIdx.x & 31) == 0) ok = spin_or_abort<kGiveUp>(bar, parity, abort_flag);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
