@@ -212,7 +212,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], s, s, x[2 * i], x[2 * i + 1]);
       };
       auto wait_block = [&](int64_t i) {  // the loads are collective: a warp leaves together
-        return __all_sync(0xffffffffu, spin_or_abort<GIVEUP>(&my_done[i % kTallStages], (uint32_t)((i / kTallStages) & 1), abort_flag));
+        return warp_wait<GIVEUP>(&my_done[i % kTallStages], (uint32_t)((i / kTallStages) & 1), abort_flag);
       };
       ok = wait_block(it);
       if (!ok) break;
@@ -224,7 +224,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         const bool more = kb + 1 < nkb;
         const int slot = (int)(grp & 1), kg = kb % kGroup;
         if (kg == 0) {
-          ok = __all_sync(0xffffffffu, spin_or_abort<GIVEUP>(&sc_full[slot], (uint32_t)((grp / 2) & 1), abort_flag));
+          ok = warp_wait<GIVEUP>(&sc_full[slot], (uint32_t)((grp / 2) & 1), abort_flag);
           if (!ok) break;
         }
         const float s = s_sa[(slot * kGroup + kg) * kScaleLd + row] * s_sb[(slot * kGroup + kg) * 2 + half];
@@ -444,8 +444,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         if (lane + 32 * i < BN) fw[lane + 32 * i] = f[i];
       __syncwarp();
       if (it + 1 < cnt) fetch(it + 1);
-      ok = spin_or_abort<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll

@@ -156,18 +156,34 @@ __device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, vo
   }
   return wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
 }
-// The same for a whole warp: one lane polls.  Every lane returns the same answer.
+// The same for a whole warp, which stays together: every branch is on a vote.  (Lanes that leave a polling
+// loop one by one, or one lane that polls for the others, stay apart afterwards, and the warp then runs the
+// work that follows once for each group.)
 template <bool kGiveUp>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = spin_or_abort<kGiveUp>(bar, parity, abort_flag);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  if constexpr (kGiveUp) {
+    *abort_flag = 1;
+    return false;
+  } else {
+    for (uint32_t i = 0; i < 20000000u; ++i) {
+      const bool done = i < 2048u ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+      if (__all_sync(0xffffffffu, done)) return true;
+      if ((i & 63u) == 63u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    }
+    *abort_flag = 1;
+    return false;
+  }
 }
 
 // One arrival for a whole warp, after all its lanes' work (each has executed the fence that work needs).
+// Predicated, not branched, for the same reason.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 st;\n setp.eq.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 st, [%0];\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(threadIdx.x & 31u)
+      : "memory");
 }
 
 // Waits for this thread's TMEM loads; the values pass through, so that nothing reads them earlier.
