@@ -21,8 +21,8 @@
 // state: sums start again at 0 after it, and pairs with such a token between them are masked, so that no
 // infinity meets another and a long sum loses no precision.
 //
-// Warps: 0-7 state and output (two per TMEM lane quadrant), 8-9 A, 10-13 K~, 14 copies and decays,
-// 15 (one lane) all MMAs.
+// Warps: 0-7 state (two per TMEM lane quadrant), 8-11 output, 12, 13 and 17 A, 18-25 K~, 14 copies and decays,
+// 15 the MMAs that do not need the state (D_A, D_U), 16 those that end in the output (D_1, D_2).
 //
 // Few long sequences would leave most of the device idle, so they are cut into segments: MODE 1 runs
 // compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
@@ -37,17 +37,21 @@ namespace {
 using namespace tcx;
 
 constexpr int kC = 64;                      // tokens of a chunk
-constexpr int kThreads = 512;
-constexpr int kStateWarps = 8, kMaskWarps = 2, kKeyWarps = 4;
-constexpr int kCopyWarp = 14, kMmaWarp = 15;
+constexpr int kThreads = 896;
+constexpr int kStateWarps = 8, kOutWarp = 8, kOutWarps = 4, kMaskWarps = 3, kCopyWarp = 14, kMmaWarp = 15, kMmaOutWarp = 16,
+              kKeyWarp = 18, kKeyWarps = 8;
+// Registers: the state warps hold 64 state values a thread; the five other groups of four give them theirs.
+constexpr int kStateRegs = 112, kOtherRegs = 56;
+static_assert(kStateWarps * 32 * kStateRegs + 20 * 32 * kOtherRegs <= kThreads * 72, "registers of the launch");
 constexpr int kStages = 3;
 // a stage: [Q | K] of the first 64 channels, [Q | K] of the second, V of the first 64 channels, of the second
 constexpr uint32_t kBlk = 8192;             // 64 tokens x 64 channels
 constexpr uint32_t kQ = 0, kKey = kBlk, kPair = 2 * kBlk, kV = 4 * kBlk, kStageBytes = 6 * kBlk;
 constexpr uint32_t kKt = kStages * kStageBytes;         // K~: three parts of two blocks
 constexpr uint32_t kA = kKt + 6 * kBlk;                 // A [64 i][64 j]
+constexpr uint32_t kOut = kA + kBlk, kOutBytes = 4096;  // output rows of each output warp's 32 value channels
 constexpr int kRing = 8;                                // decays: read until the state has been updated
-constexpr uint32_t kDecay = kA + kBlk;
+constexpr uint32_t kDecay = kOut + kOutWarps * kOutBytes;
 struct Decay {
   float G[kC];    // log2 of the decay from the chunk's start, or from the last emptying token, to token i
   float E[kC];    // e^{G_i} on the state before the chunk; 0 once it has been emptied
@@ -173,16 +177,18 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBar);  // [stages] tiles landed and decays written
-  uint64_t* empty = full + kStages;                         // [stages] all MMAs of the chunk done, decays seen by the state warps
+  uint64_t* empty = full + kStages;                         // [stages] the chunk's last products have been seen done
   uint64_t* a_done = empty + kStages;                       // D_A complete
   uint64_t* a_ready = a_done + 1;                           // A written, D_A read
-  uint64_t* kt_ready = a_done + 2;                          // K~ written (and V's rows past the sequence cleared)
-  uint64_t* u_full = a_done + 3;                            // [2] D_U complete
-  uint64_t* u_empty = a_done + 5;                           // [2] D_U read
-  uint64_t* s_ready = a_done + 7;                           // S^T in TMEM
-  uint64_t* o_full = a_done + 8;                            // D_1 and D_2 complete
-  uint64_t* bar_fin = a_done + 9;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 10);
+  uint64_t* kt_ready = a_done + 2;                          // [2] half of K~ written (and V's rows past the sequence cleared)
+  uint64_t* kt_free = a_done + 4;                           // first half of K~ read by its MMAs (the second: u_full)
+  uint64_t* u_full = a_done + 5;                            // [2] D_U complete
+  uint64_t* u_empty = a_done + 7;                           // [2] D_U read
+  uint64_t* s_ready = a_done + 9;                           // S^T in TMEM
+  uint64_t* o_full = a_done + 10;                           // D_1 and D_2 complete
+  uint64_t* o_read = a_done + 11;                           // D_1 and D_2 read
+  uint64_t* bar_fin = a_done + 12;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 13);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* seq_slot = reinterpret_cast<int*>(tmem_slot + 2);
   Decay* decay = reinterpret_cast<Decay*>(sm + kDecay);
@@ -195,16 +201,15 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   }
   const int seg = blockIdx.x % p.nseg, chain = blockIdx.x / p.nseg;
   const int h = chain % H, b = sequence_by_rank(p.cu, p.B, chain / H, seq_slot);
-  const int64_t t_begin = p.cu ? (int64_t)p.cu[b] : (int64_t)b * p.T;
-  const int64_t len = p.cu ? (int64_t)p.cu[b + 1] - p.cu[b] : p.T;
-  const int nchunks = (int)((len + kC - 1) / kC);
+  // token coordinates fit 32 bits
+  const int t_begin = p.cu ? p.cu[b] : b * (int)p.T;
+  const int len = p.cu ? p.cu[b + 1] - t_begin : (int)p.T;
+  const int nchunks = (int)(((int64_t)len + kC - 1) / kC);
   const int last_seg = nchunks > 0 ? (nchunks - 1) / p.seg_len : 0;
   if (MODE == 0 ? seg > last_seg : seg >= last_seg) return;
   const int c0 = seg * p.seg_len, nc = (nchunks < c0 + p.seg_len ? nchunks : c0 + p.seg_len) - c0;
-  const int64_t t0 = t_begin + (int64_t)c0 * kC;  // the segment's first token
-  const int64_t rows = len - (int64_t)c0 * kC;    // tokens from there to the sequence's end
-  const int64_t state_at = ((int64_t)b * H + h) * DK * dv;
-  const int64_t seg_at = (((int64_t)b * H + h) * p.nseg + seg);
+  const int t0 = t_begin + c0 * kC;  // the segment's first token
+  const int rows = len - c0 * kC;    // tokens from there to the sequence's end
 
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
@@ -213,20 +218,27 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   if (tid == 32) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 2);
-      mbar_init(&empty[i], 1 + kStateWarps);
+      mbar_init(&empty[i], kStateWarps + (MODE == 0 ? kOutWarps : 0));
     }
     mbar_init(a_done, 1);
     mbar_init(a_ready, kMaskWarps);
-    mbar_init(kt_ready, kKeyWarps);
+    mbar_init(kt_free, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&kt_ready[i], kKeyWarps);
       mbar_init(&u_full[i], 1);
       mbar_init(&u_empty[i], kStateWarps);
     }
     mbar_init(s_ready, kStateWarps);
     mbar_init(o_full, 1);
-    mbar_init(bar_fin, 1);
+    mbar_init(o_read, kOutWarps);
+    mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
+  }
+  if (MODE == 0 && warp == 2) {  // rows 0-31 of A see no token past 31: that quarter is cleared once
+#pragma unroll
+    for (int j = 4; j < 8; ++j) *reinterpret_cast<uint4*>(sm + kA + row_chunk(lane, j)) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -234,117 +246,34 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   const uint32_t tmem = *tmem_slot;
   int issued = 0;  // stages whose copies have been started (warp 14)
 
-  if (warp == kCopyWarp) {
-    // ======================== copies and decays
-    const int vb = dv / 64;
-    const uint32_t bytes = (uint32_t)((MODE == 0 ? 2 * KB : KB) + vb) * kBlk;
-    double total = 0.0;  // log2 of the segment's decay
-    bool any = false;
-    auto load_g = [&](int c, int i) -> float {
-      const int64_t r = (int64_t)c * kC + i;
-      if (r >= rows) return 0.f;
-      return kLog2e * (p.g_per_token ? __ldg(p.g + (t0 + r) * H + h) : __ldg(p.g + h));
-    };
-    float g0 = nc > 0 ? load_g(0, 2 * lane) : 0.f, g1 = nc > 0 ? load_g(0, 2 * lane + 1) : 0.f;
-    bool ok = true;
-    for (; issued < nc; ++issued) {
-      const int c = issued, s = c % kStages;
-      if (c >= kStages) ok = warp_wait<GIVEUP>(&empty[s], (uint32_t)((c / kStages - 1) & 1), abort_flag);
-      if (!ok) break;
-      if (lane == 0) {
-        uint8_t* st = sm + s * kStageBytes;
-        const int y = (int)(t0 + (int64_t)c * kC);
-        mbar_arrive_expect_tx(&full[s], bytes);
-        for (int i = 0; i < KB; ++i) {
-          if (MODE == 0) tma_load_2d(st + kQ + i * kPair, &maps.q, h * DK + 64 * i, y, &full[s]);
-          tma_load_2d(st + kKey + i * kPair, &maps.k, h * DK + 64 * i, y, &full[s]);
-        }
-        for (int i = 0; i < vb; ++i) tma_load_2d(st + kV + i * kBlk, &maps.v, h * dv + 64 * i, y, &full[s]);
-      }
-      const int64_t left = rows - (int64_t)c * kC;
-      bool emptied;
-      total += chunk_decay(&decay[c % kRing], g0, g1, (int)(left < kC ? left : kC), lane, emptied);
-      any |= emptied;
-      warp_arrive(&full[s]);
-      if (c + 1 < nc) {
-        g0 = load_g(c + 1, 2 * lane);
-        g1 = load_g(c + 1, 2 * lane + 1);
-      }
-    }
-    if (MODE == 1 && lane == 0) p.seg_decay[seg_at] = any ? 0.f : (float)exp2(total);
-  } else if (warp == kMmaWarp) {
-    // ======================== all MMAs
-    if (lane == 0) {
-      constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, true, true),
-                         id_1 = idesc_bf16_f32(128, kC, false, false), id_2 = idesc_bf16_f32(128, kC, true, false);
-      const uint64_t d_kt = smem_desc_sw128(smem_u32(sm + kKt), kBlk, 1024);
-      const uint64_t d_a = smem_desc_sw128(smem_u32(sm + kA), 16, 1024);
-      bool ok = true;
-      auto scores = [&](int c) {  // D_A of chunk c
-        const int s = c % kStages;
-        if (!spin_or_abort<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag)) return false;
-        tc_fence_after();
-        const uint8_t* st = sm + s * kStageBytes;
-        const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          const uint32_t off = (i / 4) * kPair + (i % 4) * 32;
-          mma_bf16_ss(tmem + kTmA, desc_add(dq, off), desc_add(dk, off), id_a, i > 0);
-        }
-        mma_commit(a_done);
-        return true;
-      };
-      if (MODE == 0 && nc > 0) ok = scores(0);
-      for (int c = 0; c < nc && ok; ++c) {
-        const int s = c % kStages;
-        const uint8_t* st = sm + s * kStageBytes;
-        const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
-        ok = spin_or_abort<GIVEUP>(kt_ready, (uint32_t)(c & 1), abort_flag);
-        if (ok && c >= 2) ok = spin_or_abort<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-#pragma unroll
-          for (int j = 0; j < kC / 16; ++j)
-            mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, j * 2048), desc_add(d_kt, i * 2 * kBlk + j * 2048), id_u,
-                        i + j > 0);
-        mma_commit(&u_full[c & 1]);
-        if constexpr (MODE == 0) {
-          ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
-          // D_1 and D_2 of the chunk before have been read once S^T is there
-          ok = ok && spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < kC / 16; ++j)
-            mma_bf16_ss(tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, j * 32), id_2, j > 0);
-#pragma unroll
-          for (int i = 0; i < DK / 16; ++i)
-            mma_f16_ts(tmem + kTm1, tmem + kTmS + 8 * i, desc_add(d_q, (i / 4) * kPair + (i % 4) * 32), id_1, i > 0);
-          mma_commit(o_full);
-          mma_commit(&empty[s]);
-          if (c + 1 < nc) ok = scores(c + 1);
-        } else {
-          mma_commit(&empty[s]);
-        }
-      }
-    }
-  } else if (warp < 8) {
-    // ======================== state and output
+  if (warp < kStateWarps) {
+    // ======================== state
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // value channel
     const uint32_t tl = tmem_lane(tmem, warp);
     const bool live = row < dv;
     float S[KC];
     {
-      const float* init = MODE == 1 ? nullptr : p.nseg > 1 ? p.seg_state + seg_at * DK * dv : p.h0 ? p.h0 + state_at : nullptr;
+      const float* init = MODE == 1 ? nullptr
+                          : p.nseg > 1 ? p.seg_state + (((int64_t)b * H + h) * p.nseg + seg) * DK * dv
+                          : p.h0 ? p.h0 + ((int64_t)b * H + h) * DK * dv : nullptr;
+      if (init && live) {
+        init += (int64_t)KC * half * dv + row;
 #pragma unroll
-      for (int i = 0; i < KC; ++i) S[i] = init && live ? init[(int64_t)(KC * half + i) * dv + row] : 0.f;
+        for (int i = 0; i < KC; ++i) S[i] = init[(int64_t)i * dv];
+      } else {
+#pragma unroll
+        for (int i = 0; i < KC; ++i) S[i] = 0.f;
+      }
     }
     bool ok = true;
+#pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-      const Decay* d = &decay[c % kRing];
       if constexpr (MODE == 0) {
+        // the products that read the S^T before this one
+        if (c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int i = 0; i < KC / 32; ++i) {
           uint32_t w[16];
@@ -356,147 +285,296 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         tc_fence_before();
         warp_arrive(s_ready);
       }
-      ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-      if (!ok) break;
-      warp_arrive(&empty[c % kStages]);  // so that the stage's phase cannot pass by unseen
       ok = warp_wait<GIVEUP>(&u_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
       if (!ok) break;
+      warp_arrive(&empty[c % kStages]);
       tc_fence_after();
-      const float all = d->all;
+      const float all = decay[c % kRing].all;
 #pragma unroll
-      for (int i = 0; i < KC / 16; ++i) {
-        float u[16];
-        tmem_ld16(tl + kTmU + 128 * (c & 1) + KC * half + 16 * i, u);
+      for (int i = 0; i < KC / 32; ++i) {
+        float u[32];
+        tmem_ld32(tl + kTmU + 128 * (c & 1) + KC * half + 32 * i, u);
         tmem_landed(u);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) S[16 * i + j] = fmaf(all, S[16 * i + j], u[j]);
-      }
-      tc_fence_before();
-      warp_arrive(&u_empty[c & 1]);
-      if constexpr (MODE == 0) {
-        ok = warp_wait<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
-          if (!ok) break;
-        tc_fence_after();
-        const int64_t left = rows - (int64_t)c * kC;
-        const int64_t out_step = (int64_t)H * dv;
-        Tout* dst = static_cast<Tout*>(p.out) + ((t0 + (int64_t)c * kC + 32 * half) * H + h) * dv + row;
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int tok = 32 * half + 16 * i;
-          float x[16], y[16];
-          tmem_ld16(tl + kTm1 + tok, x);
-          tmem_ld16(tl + kTm2 + tok, y);
-          tmem_landed(x);
-          tmem_landed(y);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float o = p.scale * fmaf(d->E[tok + j], x[j], y[j]);
-            if (live && tok + j < left) *dst = from_f32<Tout>(o);
-            dst += out_step;
-          }
+        if (i == KC / 32 - 1) {
+          tc_fence_before();
+          warp_arrive(&u_empty[c & 1]);
         }
-        tc_fence_before();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[32 * i + j] = fmaf(all, S[32 * i + j], u[j]);
       }
     }
     if (ok && live) {
-      float* dst = MODE == 1 ? p.seg_state + seg_at * DK * dv : p.hT && seg == last_seg ? p.hT + state_at : nullptr;
+      float* dst = MODE == 1 ? p.seg_state + (((int64_t)b * H + h) * p.nseg + seg) * DK * dv
+                   : p.hT && seg == last_seg ? p.hT + ((int64_t)b * H + h) * DK * dv : nullptr;
       if (dst) {
+        dst += (int64_t)KC * half * dv + row;
 #pragma unroll
-        for (int i = 0; i < KC; ++i) dst[(int64_t)(KC * half + i) * dv + row] = S[i];
-      }
-    }
-  } else if (warp < 10) {
-    // ======================== A: masked, decayed, to bf16
-    if constexpr (MODE == 0) {
-      const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
-      const uint32_t tl = tmem_lane(tmem, warp & 1);
-      const int jend = (warp & 1) ? kC : kC / 2;  // tokens 0-31 see none past 31
-      bool ok = true;
-      for (int c = 0; c < nc; ++c) {
-        const Decay* d = &decay[c % kRing];
-        ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-        ok = ok && warp_wait<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
-        // the products that read A of the chunk before
-        if (ok && c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
-          if (!ok) break;
-        tc_fence_after();
-        const float Gi = d->G[i];
-        const uint32_t first = (uint32_t)d->first[i], span = (uint32_t)i - first;
-#pragma unroll 1
-        for (int j0 = 0; j0 < kC; j0 += 16) {
-          float x[16];
-          if (j0 < jend) {
-            tmem_ld16(tl + kTmA + j0, x);
-            tmem_landed(x);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float e = ex2(Gi - d->G[j0 + j]);
-              x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * e : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float* y = x + 8 * e;
-            *reinterpret_cast<uint4*>(sm + kA + row_chunk(i, j0 / 8 + e)) =
-                make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
-          }
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        warp_arrive(a_ready);
+        for (int i = 0; i < KC; ++i) dst[(int64_t)i * dv] = S[i];
       }
     }
   } else {
-    // ======================== K~ = w k as three bf16 parts (8 bits each: their sum is exact)
-    const int t = tid - 10 * 32, r = t & 63, blk = t >> 6;
-    bool ok = true;
-    for (int c = 0; c < nc; ++c) {
-      uint8_t* st = sm + (c % kStages) * kStageBytes;
-      ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-      if (ok && c > 0) ok = warp_wait<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
-      if (!ok) break;
-      const float w = decay[c % kRing].W[r];
-      if (blk < KB) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ======================== copies and decays
+      const int vb = dv / 64;
+      const uint32_t bytes = (uint32_t)((MODE == 0 ? 2 * KB : KB) + vb) * kBlk;
+      float total = 0.f, lost = 0.f;  // log2 of the segment's decay, with the sum's rounding error
+      bool any = false;
+      auto load_g = [&](int c, int i) -> float {
+        const int r = c * kC + i;
+        if (r >= rows) return 0.f;
+        return kLog2e * (p.g_per_token ? __ldg(p.g + (int64_t)(t0 + r) * H + h) : __ldg(p.g + h));
+      };
+      float g0 = nc > 0 ? load_g(0, 2 * lane) : 0.f, g1 = nc > 0 ? load_g(0, 2 * lane + 1) : 0.f;
+      bool ok = true;
 #pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
-          const uint4 kk = *reinterpret_cast<const uint4*>(st + kKey + blk * kPair + row_chunk(r, j));
-          const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
-          uint32_t p0[4], p1[4], p2[4];
+      for (; issued < nc; ++issued) {
+        const int c = issued, s = c % kStages;
+        if (c >= kStages) ok = warp_wait<GIVEUP>(&empty[s], (uint32_t)((c / kStages - 1) & 1), abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* st = sm + s * kStageBytes;
+          const int y = t0 + c * kC;
+          mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
-            const float a = w == 0.f ? 0.f : w * __uint_as_float(in[e] << 16);
-            const float z = w == 0.f ? 0.f : w * __uint_as_float(in[e] & 0xffff0000u);
-            const uint32_t ah = __float_as_uint(a) & 0xffff0000u, zh = __float_as_uint(z) & 0xffff0000u;
-            const float ar = a - __uint_as_float(ah), zr = z - __uint_as_float(zh);
-            const uint32_t am = __float_as_uint(ar) & 0xffff0000u, zm = __float_as_uint(zr) & 0xffff0000u;
-            const float al = ar - __uint_as_float(am), zl = zr - __uint_as_float(zm);
-            p0[e] = (ah >> 16) | zh;
-            p1[e] = (am >> 16) | zm;
-            p2[e] = (__float_as_uint(al) >> 16) | (__float_as_uint(zl) & 0xffff0000u);
+          for (int i = 0; i < KB; ++i) {
+            if (MODE == 0) tma_load_2d(st + kQ + i * kPair, &maps.q, h * DK + 64 * i, y, &full[s]);
+            tma_load_2d(st + kKey + i * kPair, &maps.k, h * DK + 64 * i, y, &full[s]);
           }
-          uint8_t* dst = sm + kKt + blk * kBlk + row_chunk(r, j);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
-          *reinterpret_cast<uint4*>(dst + 2 * kBlk) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4*>(dst + 4 * kBlk) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          for (int i = 0; i < vb; ++i) tma_load_2d(st + kV + i * kBlk, &maps.v, h * dv + 64 * i, y, &full[s]);
+        }
+        __syncwarp();
+        const int left = rows - c * kC;
+        bool emptied;
+        const float x = chunk_decay(&decay[c % kRing], g0, g1, left < kC ? left : kC, lane, emptied) + lost;
+        const float sum = total + x;
+        lost = x - (sum - total);
+        total = sum;
+        any |= emptied;
+        warp_arrive(&full[s]);
+        if (c + 1 < nc) {
+          g0 = load_g(c + 1, 2 * lane);
+          g1 = load_g(c + 1, 2 * lane + 1);
         }
       }
-      // values past the sequence's end meet weights of 0, but may hold anything: clear them
-      if (r >= rows - (int64_t)c * kC && 64 * blk < dv) {
+      if (MODE == 1 && lane == 0) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = any ? 0.f : exp2f(total + lost);
+    } else if (warp == kMmaWarp) {
+      // ======================== D_A and D_U
+      if (lane == 0) {
+        constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, true, true);
+        const uint64_t d_kt = smem_desc_sw128(smem_u32(sm + kKt), kBlk, 1024);
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          const int s = c % kStages;
+          const uint8_t* st = sm + s * kStageBytes;
+          if constexpr (MODE == 0) {
+            ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
+            if (ok && c > 0) ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)((c - 1) & 1), abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
+#pragma unroll 1
+            for (int i = 0; i < DK / 16; ++i) {
+              const uint32_t off = (i / 4) * kPair + (i % 4) * 32;
+              mma_bf16_ss(tmem + kTmA, desc_add(dq, off), desc_add(dk, off), id_a, i > 0);
+            }
+            mma_commit(a_done);
+          }
+          if (c >= 2) ok = spin_or_abort<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+          const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024);
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {  // by halves of 32 tokens
+            ok = ok && spin_or_abort<GIVEUP>(&kt_ready[hf], (uint32_t)(c & 1), abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 2 * hf; j < 2 * hf + 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(st + kV + blk * kBlk + r * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < 3; ++i)
+                mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, j * 2048), desc_add(d_kt, i * 2 * kBlk + j * 2048), id_u,
+                            i + j > 0);
+            mma_commit(hf == 0 ? kt_free : &u_full[c & 1]);
+          }
+          if (!ok) break;
+        }
       }
-      fence_proxy_async_smem();
-      warp_arrive(kt_ready);
+    } else if (warp == kMmaOutWarp) {
+      // ======================== D_2 and D_1
+      if (MODE == 0 && lane == 0) {
+        constexpr uint32_t id_1 = idesc_bf16_f32(128, kC, false, false), id_2 = idesc_bf16_f32(128, kC, true, false);
+        const uint64_t d_a = smem_desc_sw128(smem_u32(sm + kA), 16, 1024);
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          const uint8_t* st = sm + (c % kStages) * kStageBytes;
+          const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
+          ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
+          if (ok && c > 0) ok = spin_or_abort<GIVEUP>(o_read, (uint32_t)((c - 1) & 1), abort_flag);
+          if (ok && c == nc - 1) {
+            // V's rows past the sequence are cleared with K~; the state tells that the chunk before has passed there
+            ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
+                 spin_or_abort<GIVEUP>(&kt_ready[0], (uint32_t)(c & 1), abort_flag) &&
+                 spin_or_abort<GIVEUP>(&kt_ready[1], (uint32_t)(c & 1), abort_flag);
+          }
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < kC / 16; ++j)
+            mma_bf16_ss(tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, j * 32), id_2, j > 0);
+          if (c < nc - 1) ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < DK / 16; ++i)
+            mma_f16_ts(tmem + kTm1, tmem + kTmS + 8 * i, desc_add(d_q, (i / 4) * kPair + (i % 4) * 32), id_1, i > 0);
+          mma_commit(o_full);
+        }
+      }
+    } else if (warp < kOutWarp + kOutWarps) {
+      // ======================== output: tokens of this warp's 32 value channels, by way of shared memory
+      if constexpr (MODE == 0) {
+        constexpr int kTok = kOutBytes / (32 * sizeof(Tout));      // tokens at a time: 64, or 32 in fp32
+        constexpr int kLanes = 32 * sizeof(Tout) / 16;             // lanes that store a token's 16-byte pieces
+        const uint32_t tl = tmem_lane(tmem, warp);
+        const bool live = (warp & 3) * 32 < dv;
+        uint8_t* stage = sm + kOut + (warp - kOutWarp) * kOutBytes;
+        // this lane's 16 bytes of the first token it stores
+        const int64_t step = (int64_t)H * dv * sizeof(Tout);
+        int r0 = lane / kLanes;  // ... and that token's place in the segment
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t0 + r0) * step + ((int64_t)h * dv + (warp & 3) * 32) * sizeof(Tout) +
+                       lane % kLanes * 16;
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          ok = warp_wait<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
+          if (!ok) break;
+          warp_arrive(&empty[c % kStages]);
+          tc_fence_after();
+          const float* E = decay[c % kRing].E;
+#pragma unroll 1
+          for (int tk = 0; tk < kC; tk += 8) {
+            float x[8], y[8];
+            tmem_ld8x2_wait(tl + kTm1 + tk, tl + kTm2 + tk, x, y);
+            Tout* at = reinterpret_cast<Tout*>(stage) + tk % kTok * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const float4 e = *reinterpret_cast<const float4*>(E + tk + j);
+              at[(j + 0) * 32] = from_f32<Tout>(p.scale * fmaf(e.x, x[j], y[j]));
+              at[(j + 1) * 32] = from_f32<Tout>(p.scale * fmaf(e.y, x[j + 1], y[j + 1]));
+              at[(j + 2) * 32] = from_f32<Tout>(p.scale * fmaf(e.z, x[j + 2], y[j + 2]));
+              at[(j + 3) * 32] = from_f32<Tout>(p.scale * fmaf(e.w, x[j + 3], y[j + 3]));
+            }
+            if (tk == kC - 8) {
+              tc_fence_before();
+              warp_arrive(o_read);
+            }
+            if ((tk + 8) % kTok == 0) {
+              __syncwarp();
+#pragma unroll 2
+              for (int i = 0; i < kTok * kLanes / 32; ++i) {
+                if (live && r0 < rows) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(stage + i * 512 + lane * 16);
+                dst += (32 / kLanes) * step;
+                r0 += 32 / kLanes;
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+    } else if (warp < kCopyWarp || warp == 17) {
+      // ======================== A: masked, decayed, to bf16, 32 columns a warp
+      if constexpr (MODE == 0) {
+        const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
+        const uint32_t tl = tmem_lane(tmem, warp & 1);
+        const int col = warp == 17 ? 32 : 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          const Decay* d = &decay[c % kRing];
+          ok = warp_wait<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
+          // the product that read A of the chunk before
+          if (ok && c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const float Gi = d->G[i];
+          const uint32_t first = (uint32_t)d->first[i], span = (uint32_t)i - first;
+#pragma unroll 1
+          for (int j0 = col; j0 < col + 32; j0 += 8) {
+            float x[8];
+            tmem_ld8_wait(tl + kTmA + j0, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float e = ex2(Gi - d->G[j0 + j]);
+              x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * e : 0.f;
+            }
+            *reinterpret_cast<uint4*>(sm + kA + row_chunk(i, j0 / 8)) =
+                make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          warp_arrive(a_ready);
+        }
+      }
+    } else if (warp >= kKeyWarp && warp < kKeyWarp + kKeyWarps) {
+      // ======================== K~ = w k as three bf16 parts (8 bits each: their sum is exact)
+      const int group = warp - kKeyWarp, vb = dv / 64;  // 16-byte pieces of a row: KB (vb) to a warp
+      bool ok = true;
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c) {
+        uint8_t* st = sm + (c % kStages) * kStageBytes;
+        ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          // the products that read this half of the chunk before
+          if (ok && c > 0)
+            ok = hf == 0 ? warp_wait<GIVEUP>(kt_free, (uint32_t)((c - 1) & 1), abort_flag)
+                         : warp_wait<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+          if (!ok) break;
+          const int r = 32 * hf + lane;
+          const float w = decay[c % kRing].W[r];
+#pragma unroll 1
+          for (int i = 0; i < KB; ++i) {
+            const int blk = (group * KB + i) >> 3, j = (group * KB + i) & 7;
+            const uint4 kk = *reinterpret_cast<const uint4*>(st + kKey + blk * kPair + row_chunk(r, j));
+            const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
+            uint32_t p0[4], p1[4], p2[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
+              const float a = w == 0.f ? 0.f : w * __uint_as_float(in[e] << 16);
+              const float z = w == 0.f ? 0.f : w * __uint_as_float(in[e] & 0xffff0000u);
+              const uint32_t ah = __float_as_uint(a) & 0xffff0000u, zh = __float_as_uint(z) & 0xffff0000u;
+              const float ar = a - __uint_as_float(ah), zr = z - __uint_as_float(zh);
+              const uint32_t am = __float_as_uint(ar) & 0xffff0000u, zm = __float_as_uint(zr) & 0xffff0000u;
+              const float al = ar - __uint_as_float(am), zl = zr - __uint_as_float(zm);
+              p0[e] = __byte_perm(ah, zh, 0x7632);
+              p1[e] = __byte_perm(am, zm, 0x7632);
+              p2[e] = __byte_perm(__float_as_uint(al), __float_as_uint(zl), 0x7632);
+            }
+            uint8_t* dst = sm + kKt + blk * kBlk + row_chunk(r, j);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
+            *reinterpret_cast<uint4*>(dst + 2 * kBlk) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+            *reinterpret_cast<uint4*>(dst + 4 * kBlk) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          }
+          // values past the sequence's end meet weights of 0, but may hold anything: clear them
+          if (r >= rows - c * kC) {
+            for (int i = 0; i < vb; ++i) {
+              const int blk = (group * vb + i) >> 3, j = (group * vb + i) & 7;
+              *reinterpret_cast<uint4*>(st + kV + blk * kBlk + r * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+          warp_arrive(&kt_ready[hf]);
+        }
+        if (!ok) break;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  drain_after_abort<kStages>(abort_flag, tid == kCopyWarp * 32, tid == kMmaWarp * 32, full, issued, bar_fin, p.err);
+  drain_after_abort<kStages>(abort_flag, tid == kCopyWarp * 32, tid == kMmaWarp * 32 || tid == kMmaOutWarp * 32, full, issued,
+                             bar_fin, p.err);
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -524,16 +602,18 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
   *reinterpret_cast<float4*>(p) = S;
 }
 
-// Segments: only where at least half of the device would be idle, of 8 chunks at least, and so long that
-// all chunks together give each SM one.
+// Segments: only where at least half of the device would be idle, of 8 chunks at least, and so long that all
+// chunks, with one short segment for each (sequence, head), make at most one CTA an SM (a second wave would cost
+// as much as the first).
 constexpr int kMinSplitChunks = 32, kMinSegChunks = 8;
 void segments(int B, int64_t T, int64_t T_tot, bool has_cu, int H, int sms, int* nseg, int* seg_len) {
   const int64_t longest = (T + kC - 1) / kC;  // of a sequence, at most
+  const int64_t chains = (int64_t)B * H;
   *nseg = 1;
   *seg_len = longest > 0 ? (int)longest : 1;
-  if ((int64_t)B * H * 2 > sms || longest < kMinSplitChunks) return;
-  const int64_t chunks = has_cu ? (T_tot + kC - 1) / kC : (int64_t)B * longest;
-  int64_t n = (chunks * H + sms - 1) / sms;
+  if (chains * 2 > sms || longest < kMinSplitChunks) return;
+  const int64_t chunks = has_cu ? (T_tot + kC - 1) / kC : B * longest;
+  int64_t n = (chunks * H + sms - chains - 1) / (sms - chains);
   if (n < kMinSegChunks) n = kMinSegChunks;
   if (n >= longest) return;
   *nseg = (int)((longest + n - 1) / n);

@@ -166,8 +166,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return false;
   } else {
     for (uint32_t i = 0; i < 20000000u; ++i) {
-      const bool done = i < 2048u ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
-      if (__all_sync(0xffffffffu, done)) return true;
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
       if ((i & 63u) == 63u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
     }
     *abort_flag = 1;
@@ -203,6 +202,34 @@ __device__ __forceinline__ void tmem_landed(float (&v)[16]) {
                :
                : "memory");
 }
+// 8 consecutive columns of this thread's TMEM lane; valid on return.
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The same columns of two accumulators.
+__device__ __forceinline__ void tmem_ld8x2_wait(uint32_t ta, uint32_t tb, float (&v)[8], float (&w)[8]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = __uint_as_float(r[i]);
+    w[i] = __uint_as_float(r[8 + i]);
+  }
+}
+
 // At the end of a CTA (all threads, after a barrier, so that the flag is final): if a wait ran out, the
 // copies and MMAs that may still be in flight are waited for, with a limit, before shared memory and TMEM
 // are given back.  Without an abort every MMA, and with it every copy, was waited for by its readers.
