@@ -12,7 +12,7 @@
 // the value channel as the tensor core's row (M = 128; with dv = 64 the upper rows are not used):
 //   D_A [128 x 64]  = [Q ; K] K^T     rows 0-63 are q_i . k_j (the stack fills the 128 rows an MMA has)
 //   D_U [dv x dk]   = V^T K~          K~ = w_j k_j as the exact sum of three bf16 parts, so U has fp32 accuracy
-//   D_2 [dv x 64]   = V^T A^T         A masked, scaled and rounded to bf16 in shared memory
+//   D_2 [dv x 64]   = V^T A^T         A masked, decayed, scaled and rounded to bf16 in shared memory
 //   D_1 [dv x 64]   = S^T Q^T         S^T rounded to bf16 in TMEM
 // with S^T itself (fp32) in the registers of warps 0-7.  So out is off by the roundings of A and S to
 // bf16 (half a step each, of its terms), like its own rounding; the states are not rounded below fp32.
@@ -54,7 +54,7 @@ constexpr int kRing = 8;                                // decays: read until th
 constexpr uint32_t kDecay = kOut + kOutWarps * kOutBytes;
 struct Decay {
   float G[kC];    // log2 of the decay from the chunk's start, or from the last emptying token, to token i
-  float E[kC];    // e^{G_i} on the state before the chunk; 0 once it has been emptied
+  float E[kC];    // scale e^{G_i} on the state before the chunk; 0 once it has been emptied
   float W[kC];    // w_j; 0 for tokens past the sequence
   int first[kC];  // the first token that reaches token i
   float all;      // decay of the state over the whole chunk
@@ -120,7 +120,7 @@ __device__ __forceinline__ int sequence_by_rank(const int32_t* __restrict__ cu, 
 
 // Decays of one chunk (one warp, tokens 2 lane and 2 lane + 1).  Returns log2 of the chunk's decay and
 // whether a token emptied the state.
-__device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n, int lane, bool& emptied) {
+__device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n, float scale, int lane, bool& emptied) {
   const int i0 = 2 * lane, i1 = i0 + 1;
   const bool e0 = g0 <= kEmpty, e1 = g1 <= kEmpty;
   const float a0 = e0 ? 0.f : g0, a1 = e1 ? 0.f : g1;
@@ -157,8 +157,8 @@ __device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n
   const int final_last = __shfl_sync(0xffffffffu, l1, 31);
   d->G[i0] = G0;
   d->G[i1] = G1;
-  d->E[i0] = l0 < 0 ? exp2f(G0) : 0.f;
-  d->E[i1] = l1 < 0 ? exp2f(G1) : 0.f;
+  d->E[i0] = l0 < 0 ? scale * exp2f(G0) : 0.f;
+  d->E[i1] = l1 < 0 ? scale * exp2f(G1) : 0.f;
   d->W[i0] = i0 < n && i0 >= final_last ? exp2f(a1 + after) : 0.f;
   d->W[i1] = i1 < n && i1 >= final_last ? exp2f(after) : 0.f;
   d->first[i0] = l0 < 0 ? 0 : l0;
@@ -300,7 +300,11 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           warp_arrive(&u_empty[c & 1]);
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[32 * i + j] = fmaf(all, S[32 * i + j], u[j]);
+        for (int j = 0; j < 32; j += 2) {
+          const float2 s = fma2(make_float2(all, all), make_float2(S[32 * i + j], S[32 * i + j + 1]), make_float2(u[j], u[j + 1]));
+          S[32 * i + j] = s.x;
+          S[32 * i + j + 1] = s.y;
+        }
       }
     }
     if (ok && live) {
@@ -346,7 +350,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
         const int left = rows - c * kC;
         bool emptied;
-        const float x = chunk_decay(&decay[c % kRing], g0, g1, left < kC ? left : kC, lane, emptied) + lost;
+        const float x = chunk_decay(&decay[c % kRing], g0, g1, left < kC ? left : kC, p.scale, lane, emptied) + lost;
         const float sum = total + x;
         lost = x - (sum - total);
         total = sum;
@@ -375,10 +379,10 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             tc_fence_after();
             const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
 #pragma unroll 1
-            for (int i = 0; i < DK / 16; ++i) {
-              const uint32_t off = (i / 4) * kPair + (i % 4) * 32;
-              mma_bf16_ss(tmem + kTmA, desc_add(dq, off), desc_add(dk, off), id_a, i > 0);
-            }
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_bf16_ss(tmem + kTmA, desc_add(dq, b * kPair + i * 32), desc_add(dk, b * kPair + i * 32), id_a, b + i > 0);
             mma_commit(a_done);
           }
           if (c >= 2) ok = spin_or_abort<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
@@ -388,12 +392,12 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             ok = ok && spin_or_abort<GIVEUP>(&kt_ready[hf], (uint32_t)(c & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int j = 2 * hf; j < 2 * hf + 2; ++j)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 3; ++i)
-                mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, j * 2048), desc_add(d_kt, i * 2 * kBlk + j * 2048), id_u,
-                            i + j > 0);
+                mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, hf * 4096 + j * 2048),
+                            desc_add(d_kt, i * 2 * kBlk + hf * 4096 + j * 2048), id_u, hf + i + j > 0);
             mma_commit(hf == 0 ? kt_free : &u_full[c & 1]);
           }
           if (!ok) break;
@@ -419,15 +423,17 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           }
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1
+#pragma unroll
           for (int j = 0; j < kC / 16; ++j)
             mma_bf16_ss(tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, j * 32), id_2, j > 0);
           if (c < nc - 1) ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int i = 0; i < DK / 16; ++i)
-            mma_f16_ts(tmem + kTm1, tmem + kTmS + 8 * i, desc_add(d_q, (i / 4) * kPair + (i % 4) * 32), id_1, i > 0);
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16_ts(tmem + kTm1, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
           mma_commit(o_full);
         }
       }
@@ -460,10 +466,10 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
               const float4 e = *reinterpret_cast<const float4*>(E + tk + j);
-              at[(j + 0) * 32] = from_f32<Tout>(p.scale * fmaf(e.x, x[j], y[j]));
-              at[(j + 1) * 32] = from_f32<Tout>(p.scale * fmaf(e.y, x[j + 1], y[j + 1]));
-              at[(j + 2) * 32] = from_f32<Tout>(p.scale * fmaf(e.z, x[j + 2], y[j + 2]));
-              at[(j + 3) * 32] = from_f32<Tout>(p.scale * fmaf(e.w, x[j + 3], y[j + 3]));
+              at[(j + 0) * 32] = from_f32<Tout>(fmaf(e.x, x[j], y[j]));
+              at[(j + 1) * 32] = from_f32<Tout>(fmaf(e.y, x[j + 1], y[j + 1]));
+              at[(j + 2) * 32] = from_f32<Tout>(fmaf(e.z, x[j + 2], y[j + 2]));
+              at[(j + 3) * 32] = from_f32<Tout>(fmaf(e.w, x[j + 3], y[j + 3]));
             }
             if (tk == kC - 8) {
               tc_fence_before();
@@ -488,6 +494,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
         const uint32_t tl = tmem_lane(tmem, warp & 1);
         const int col = warp == 17 ? 32 : 0;
+        const float scale = p.scale;
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -506,7 +513,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float e = ex2(Gi - d->G[j0 + j]);
-              x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * e : 0.f;
+              x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * (scale * e) : 0.f;
             }
             *reinterpret_cast<uint4*>(sm + kA + row_chunk(i, j0 / 8)) =
                 make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
@@ -533,6 +540,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           if (!ok) break;
           const int r = 32 * hf + lane;
           const float w = decay[c % kRing].W[r];
+          // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
+          const uint32_t keep = w == 0.f ? 0u : 0xffffffffu;
 #pragma unroll 1
           for (int i = 0; i < KB; ++i) {
             const int blk = (group * KB + i) >> 3, j = (group * KB + i) & 7;
@@ -541,16 +550,15 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
-              const float a = w == 0.f ? 0.f : w * __uint_as_float(in[e] << 16);
-              const float z = w == 0.f ? 0.f : w * __uint_as_float(in[e] & 0xffff0000u);
-              const uint32_t ah = __float_as_uint(a) & 0xffff0000u, zh = __float_as_uint(z) & 0xffff0000u;
-              const float ar = a - __uint_as_float(ah), zr = z - __uint_as_float(zh);
-              const uint32_t am = __float_as_uint(ar) & 0xffff0000u, zm = __float_as_uint(zr) & 0xffff0000u;
-              const float al = ar - __uint_as_float(am), zl = zr - __uint_as_float(zm);
-              p0[e] = __byte_perm(ah, zh, 0x7632);
-              p1[e] = __byte_perm(am, zm, 0x7632);
-              p2[e] = __byte_perm(__float_as_uint(al), __float_as_uint(zl), 0x7632);
+              const uint32_t kw = in[e] & keep;
+              const float2 x = mul2(make_float2(w, w), make_float2(__uint_as_float(kw << 16), __uint_as_float(kw & 0xffff0000u)));
+              const uint32_t h0 = __float_as_uint(x.x), h1 = __float_as_uint(x.y);
+              const float2 y = sub2(x, make_float2(__uint_as_float(h0 & 0xffff0000u), __uint_as_float(h1 & 0xffff0000u)));
+              const uint32_t m0 = __float_as_uint(y.x), m1 = __float_as_uint(y.y);
+              const float2 z = sub2(y, make_float2(__uint_as_float(m0 & 0xffff0000u), __uint_as_float(m1 & 0xffff0000u)));
+              p0[e] = __byte_perm(h0, h1, 0x7632);
+              p1[e] = __byte_perm(m0, m1, 0x7632);
+              p2[e] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
             }
             uint8_t* dst = sm + kKt + blk * kBlk + row_chunk(r, j);
             *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);

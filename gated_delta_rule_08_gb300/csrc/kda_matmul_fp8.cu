@@ -46,7 +46,7 @@ __device__ __forceinline__ void mma_block(uint32_t d, const uint8_t* a, const ui
 }
 
 // acc (two fp32 lanes) += s * d
-__device__ __forceinline__ void fma2(uint64_t& acc, float s0, float s1, float d0, float d1) {
+__device__ __forceinline__ void acc_fma2(uint64_t& acc, float s0, float s1, float d0, float d1) {
   asm("{\n .reg .b64 rs, rd;\n mov.b64 rs, {%1, %2};\n mov.b64 rd, {%3, %4};\n fma.rn.f32x2 %0, rs, rd, %0;\n}"
       : "+l"(acc)
       : "f"(s0), "f"(s1), "f"(d0), "f"(d1));
@@ -209,7 +209,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       float v[32], w[32];
       auto add = [&](const float (&x)[32], int c, float s) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], s, s, x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 16; ++i) acc_fma2(acc[16 * c + i], s, s, x[2 * i], x[2 * i + 1]);
       };
       auto wait_block = [&](int64_t i) {  // the loads are collective: a warp leaves together
         return warp_wait<GIVEUP>(&my_done[i % kTallStages], (uint32_t)((i / kTallStages) & 1), abort_flag);
@@ -459,8 +459,8 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 s = *reinterpret_cast<const float4*>(fw + 16 * c + 4 * i);
-          fma2(acc[8 * c + 2 * i], s.x, s.y, v[4 * i], v[4 * i + 1]);
-          fma2(acc[8 * c + 2 * i + 1], s.z, s.w, v[4 * i + 2], v[4 * i + 3]);
+          acc_fma2(acc[8 * c + 2 * i], s.x, s.y, v[4 * i], v[4 * i + 1]);
+          acc_fma2(acc[8 * c + 2 * i + 1], s.z, s.w, v[4 * i + 2], v[4 * i + 3]);
         }
       }
     }
