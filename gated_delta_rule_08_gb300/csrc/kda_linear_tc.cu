@@ -21,8 +21,9 @@
 // state: sums start again at 0 after it, and pairs with such a token between them are masked, so that no
 // infinity meets another and a long sum loses no precision.
 //
-// Warps: 0-7 state (two per TMEM lane quadrant), 8-11 output, 12, 13 and 17 A, 18-25 K~, 14 copies and decays,
-// 15 the MMAs that do not need the state (D_A, D_U), 16 those that end in the output (D_1, D_2).
+// Warps: 0 copies and decays, 1 the MMAs that do not need the state (D_A, D_U), 2 those that end in the output
+// (D_1, D_2), 4-11 state, 12-19 output (two per TMEM lane quadrant each), 20, 21 and 25 A, the others from 22 to 30
+// K~.  A, D_1 and D_2 lie twice, so that A is made and the output read while the next chunk's products run.
 //
 // Few long sequences would leave most of the device idle, so they are cut into segments: MODE 1 runs
 // compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
@@ -37,25 +38,27 @@ namespace {
 using namespace tcx;
 
 constexpr int kC = 64;                      // tokens of a chunk
-constexpr int kThreads = 896;
-constexpr int kStateWarps = 8, kOutWarp = 8, kOutWarps = 4, kMaskWarps = 3, kCopyWarp = 14, kMmaWarp = 15, kMmaOutWarp = 16,
-              kKeyWarp = 18, kKeyWarps = 8;
-// Registers: the state warps hold 64 state values a thread; the five other groups of four give them theirs.
-constexpr int kStateRegs = 112, kOtherRegs = 56;
-static_assert(kStateWarps * 32 * kStateRegs + 20 * 32 * kOtherRegs <= kThreads * 72, "registers of the launch");
+constexpr int kThreads = 1024;
+constexpr int kCopyWarp = 0, kMmaWarp = 1, kMmaOutWarp = 2, kStateWarp = 4, kStateWarps = 8, kOutWarp = 12, kOutWarps = 8,
+              kMaskWarps = 3, kKeyWarps = 8;
+__device__ __forceinline__ bool is_mask_warp(int w) { return w == 20 || w == 21 || w == 25; }  // lanes 0-63 of TMEM
+__device__ __forceinline__ int key_warp(int w) { return w < 25 ? w - 22 : w - 23; }            // 0-7 of 22-24 and 26-30
+// Registers: the state warps hold 64 state values a thread; the other groups of four give them theirs.
+constexpr int kStateRegs = 112, kOtherRegs = 48;
+static_assert(kStateWarps * 32 * kStateRegs + 24 * 32 * kOtherRegs <= kThreads * 64, "registers of the launch");
 constexpr int kStages = 3;
 // a stage: [Q | K] of the first 64 channels, [Q | K] of the second, V of the first 64 channels, of the second
 constexpr uint32_t kBlk = 8192;             // 64 tokens x 64 channels
 constexpr uint32_t kQ = 0, kKey = kBlk, kPair = 2 * kBlk, kV = 4 * kBlk, kStageBytes = 6 * kBlk;
 constexpr uint32_t kKt = kStages * kStageBytes;         // K~: three parts of two blocks
-constexpr uint32_t kA = kKt + 6 * kBlk;                 // A [64 i][64 j]
-constexpr uint32_t kOut = kA + kBlk, kOutBytes = 4096;  // output rows of each output warp's 32 value channels
+constexpr uint32_t kA = kKt + 6 * kBlk;                 // A [64 i][64 j], twice
+constexpr uint32_t kOut = kA + 2 * kBlk, kOutBytes = 1024;  // output rows of each output warp's 32 value channels
 constexpr int kRing = 8;                                // decays: read until the state has been updated
 constexpr uint32_t kDecay = kOut + kOutWarps * kOutBytes;
 struct Decay {
   float G[kC];    // log2 of the decay from the chunk's start, or from the last emptying token, to token i
   float E[kC];    // scale e^{G_i} on the state before the chunk; 0 once it has been emptied
-  float W[kC];    // w_j; 0 for tokens past the sequence
+  float W[kC];    // w_j; 0 for tokens past the sequence (before: the log decays)
   int first[kC];  // the first token that reaches token i
   float all;      // decay of the state over the whole chunk
   int pad[3];
@@ -65,7 +68,7 @@ constexpr uint32_t kSmem = kBar + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // TMEM columns
-constexpr uint32_t kTmA = 0, kTm1 = 64, kTm2 = 128, kTmS = 192, kTmU = 256;  // D_U twice
+constexpr uint32_t kTmA = 0, kTmS = 64, kTm1 = 128, kTm2 = 256, kTmU = 384;  // D_1 and D_2 twice, 64 columns apart
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kEmpty = -150.f;
@@ -179,16 +182,16 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBar);  // [stages] tiles landed and decays written
   uint64_t* empty = full + kStages;                         // [stages] the chunk's last products have been seen done
   uint64_t* a_done = empty + kStages;                       // D_A complete
-  uint64_t* a_ready = a_done + 1;                           // A written, D_A read
-  uint64_t* kt_ready = a_done + 2;                          // [2] half of K~ written (and V's rows past the sequence cleared)
-  uint64_t* kt_free = a_done + 4;                           // first half of K~ read by its MMAs (the second: u_full)
-  uint64_t* u_full = a_done + 5;                            // [2] D_U complete
-  uint64_t* u_empty = a_done + 7;                           // [2] D_U read
-  uint64_t* s_ready = a_done + 9;                           // S^T in TMEM
-  uint64_t* o_full = a_done + 10;                           // D_1 and D_2 complete
-  uint64_t* o_read = a_done + 11;                           // D_1 and D_2 read
-  uint64_t* bar_fin = a_done + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 13);
+  uint64_t* a_ready = a_done + 1;                           // [2] A written, D_A read
+  uint64_t* kt_ready = a_done + 3;                          // [2] half of K~ written (and V's rows past the sequence cleared)
+  uint64_t* kt_free = a_done + 5;                           // first half of K~ read by its MMAs (the second: u_full)
+  uint64_t* u_full = a_done + 6;                            // D_U complete
+  uint64_t* u_empty = a_done + 7;                           // D_U read
+  uint64_t* s_ready = a_done + 8;                           // S^T in TMEM
+  uint64_t* o_full = a_done + 9;                            // [2] D_1 and D_2 complete
+  uint64_t* o_read = a_done + 11;                           // [2] D_1 and D_2 read
+  uint64_t* bar_fin = a_done + 13;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* seq_slot = reinterpret_cast<int*>(tmem_slot + 2);
   Decay* decay = reinterpret_cast<Decay*>(sm + kDecay);
@@ -221,23 +224,26 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       mbar_init(&empty[i], kStateWarps + (MODE == 0 ? kOutWarps : 0));
     }
     mbar_init(a_done, 1);
-    mbar_init(a_ready, kMaskWarps);
     mbar_init(kt_free, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&kt_ready[i], kKeyWarps);
-      mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], kStateWarps);
-    }
+    mbar_init(u_full, 1);
+    mbar_init(u_empty, kStateWarps);
     mbar_init(s_ready, kStateWarps);
-    mbar_init(o_full, 1);
-    mbar_init(o_read, kOutWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_ready[i], kMaskWarps);
+      mbar_init(&kt_ready[i], kKeyWarps);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_read[i], kOutWarps);
+    }
     mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
   }
   if (MODE == 0 && warp == 2) {  // rows 0-31 of A see no token past 31: that quarter is cleared once
 #pragma unroll
-    for (int j = 4; j < 8; ++j) *reinterpret_cast<uint4*>(sm + kA + row_chunk(lane, j)) = make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 4; j < 8; ++j) {
+      *reinterpret_cast<uint4*>(sm + kA + row_chunk(lane, j)) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(sm + kA + kBlk + row_chunk(lane, j)) = make_uint4(0u, 0u, 0u, 0u);
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -246,10 +252,10 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   const uint32_t tmem = *tmem_slot;
   int issued = 0;  // stages whose copies have been started (warp 14)
 
-  if (warp < kStateWarps) {
+  if (warp >= kStateWarp && warp < kStateWarp + kStateWarps) {
     // ======================== state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // value channel
+    const int half = (warp - kStateWarp) >> 2, row = (warp & 3) * 32 + lane;  // value channel
     const uint32_t tl = tmem_lane(tmem, warp);
     const bool live = row < dv;
     float S[KC];
@@ -271,7 +277,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int c = 0; c < nc; ++c) {
       if constexpr (MODE == 0) {
         // the products that read the S^T before this one
-        if (c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+        if (c > 0) ok = warp_wait<GIVEUP>(&o_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -285,7 +291,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         tc_fence_before();
         warp_arrive(s_ready);
       }
-      ok = warp_wait<GIVEUP>(&u_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
+      ok = warp_wait<GIVEUP>(u_full, (uint32_t)(c & 1), abort_flag);
       if (!ok) break;
       warp_arrive(&empty[c % kStages]);
       tc_fence_after();
@@ -293,11 +299,11 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
       for (int i = 0; i < KC / 32; ++i) {
         float u[32];
-        tmem_ld32(tl + kTmU + 128 * (c & 1) + KC * half + 32 * i, u);
+        tmem_ld32(tl + kTmU + KC * half + 32 * i, u);
         tmem_landed(u);
         if (i == KC / 32 - 1) {
           tc_fence_before();
-          warp_arrive(&u_empty[c & 1]);
+          warp_arrive(u_empty);
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
@@ -324,12 +330,21 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       const uint32_t bytes = (uint32_t)((MODE == 0 ? 2 * KB : KB) + vb) * kBlk;
       float total = 0.f, lost = 0.f;  // log2 of the segment's decay, with the sum's rounding error
       bool any = false;
-      auto load_g = [&](int c, int i) -> float {
-        const int r = c * kC + i;
-        if (r >= rows) return 0.f;
-        return kLog2e * (p.g_per_token ? __ldg(p.g + (int64_t)(t0 + r) * H + h) : __ldg(p.g + h));
+      // The decays of the chunks ahead go to where their weights will be: a load takes longer than a chunk.
+      constexpr int kAhead = 4;
+      auto fetch_g = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = c * kC + 2 * lane + i;
+          const float* src = p.g + (r < rows && p.g_per_token ? (int64_t)(t0 + r) * H + h : (int64_t)h);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&decay[c % kRing].W[2 * lane + i])), "l"(src),
+                       "r"(r < rows ? 4 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      float g0 = nc > 0 ? load_g(0, 2 * lane) : 0.f, g1 = nc > 0 ? load_g(0, 2 * lane + 1) : 0.f;
+#pragma unroll 1
+      for (int i = 0; i < kAhead && nc > 0; ++i) fetch_g(i);
       bool ok = true;
 #pragma unroll 1
       for (; issued < nc; ++issued) {
@@ -350,17 +365,18 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
         const int left = rows - c * kC;
         bool emptied;
-        const float x = chunk_decay(&decay[c % kRing], g0, g1, left < kC ? left : kC, p.scale, lane, emptied) + lost;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        Decay* d = &decay[c % kRing];
+        const float g0 = kLog2e * d->W[2 * lane], g1 = kLog2e * d->W[2 * lane + 1];
+        const float x = chunk_decay(d, g0, g1, left < kC ? left : kC, p.scale, lane, emptied) + lost;
         const float sum = total + x;
         lost = x - (sum - total);
         total = sum;
         any |= emptied;
         warp_arrive(&full[s]);
-        if (c + 1 < nc) {
-          g0 = load_g(c + 1, 2 * lane);
-          g1 = load_g(c + 1, 2 * lane + 1);
-        }
+        fetch_g(c + kAhead);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (MODE == 1 && lane == 0) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = any ? 0.f : exp2f(total + lost);
     } else if (warp == kMmaWarp) {
       // ======================== D_A and D_U
@@ -374,7 +390,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const uint8_t* st = sm + s * kStageBytes;
           if constexpr (MODE == 0) {
             ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
-            if (ok && c > 0) ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)((c - 1) & 1), abort_flag);
+            if (ok && c > 0) ok = spin_or_abort<GIVEUP>(&a_ready[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
@@ -385,7 +401,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
                 mma_bf16_ss(tmem + kTmA, desc_add(dq, b * kPair + i * 32), desc_add(dk, b * kPair + i * 32), id_a, b + i > 0);
             mma_commit(a_done);
           }
-          if (c >= 2) ok = spin_or_abort<GIVEUP>(&u_empty[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+          if (c > 0) ok = spin_or_abort<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // by halves of 32 tokens
@@ -396,9 +412,9 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 3; ++i)
-                mma_bf16_ss(tmem + kTmU + 128 * (c & 1), desc_add(d_v, hf * 4096 + j * 2048),
+                mma_bf16_ss(tmem + kTmU, desc_add(d_v, hf * 4096 + j * 2048),
                             desc_add(d_kt, i * 2 * kBlk + hf * 4096 + j * 2048), id_u, hf + i + j > 0);
-            mma_commit(hf == 0 ? kt_free : &u_full[c & 1]);
+            mma_commit(hf == 0 ? kt_free : u_full);
           }
           if (!ok) break;
         }
@@ -413,8 +429,9 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         for (int c = 0; c < nc; ++c) {
           const uint8_t* st = sm + (c % kStages) * kStageBytes;
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
-          ok = spin_or_abort<GIVEUP>(a_ready, (uint32_t)(c & 1), abort_flag);
-          if (ok && c > 0) ok = spin_or_abort<GIVEUP>(o_read, (uint32_t)((c - 1) & 1), abort_flag);
+          const uint32_t buf = c & 1;
+          ok = spin_or_abort<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
+          if (ok && c >= 2) ok = spin_or_abort<GIVEUP>(&o_read[buf], (uint32_t)((c / 2 - 1) & 1), abort_flag);
           if (ok && c == nc - 1) {
             // V's rows past the sequence are cleared with K~; the state tells that the chunk before has passed there
             ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
@@ -425,7 +442,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
-            mma_bf16_ss(tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, j * 32), id_2, j > 0);
+            mma_bf16_ss(tmem + kTm2 + 64 * buf, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
           if (c < nc - 1) ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -433,35 +450,37 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ts(tmem + kTm1, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
-          mma_commit(o_full);
+              mma_f16_ts(tmem + kTm1 + 64 * buf, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
+          mma_commit(&o_full[buf]);
         }
       }
-    } else if (warp < kOutWarp + kOutWarps) {
-      // ======================== output: tokens of this warp's 32 value channels, by way of shared memory
+    } else if (warp >= kOutWarp && warp < kOutWarp + kOutWarps) {
+      // ======================== output: 32 tokens of 32 value channels, by way of shared memory
       if constexpr (MODE == 0) {
-        constexpr int kTok = kOutBytes / (32 * sizeof(Tout));      // tokens at a time: 64, or 32 in fp32
+        constexpr int kTok = kOutBytes / (32 * sizeof(Tout));      // tokens at a time: 16, or 8 in fp32
         constexpr int kLanes = 32 * sizeof(Tout) / 16;             // lanes that store a token's 16-byte pieces
         const uint32_t tl = tmem_lane(tmem, warp);
         const bool live = (warp & 3) * 32 < dv;
         uint8_t* stage = sm + kOut + (warp - kOutWarp) * kOutBytes;
         // this lane's 16 bytes of the first token it stores
         const int64_t step = (int64_t)H * dv * sizeof(Tout);
-        int r0 = lane / kLanes;  // ... and that token's place in the segment
+        const int tok0 = 32 * ((warp - kOutWarp) >> 2);
+        int r0 = tok0 + lane / kLanes;  // ... and that token's place in the segment
         uint8_t* dst = static_cast<uint8_t*>(p.out) + (int64_t)(t0 + r0) * step + ((int64_t)h * dv + (warp & 3) * 32) * sizeof(Tout) +
                        lane % kLanes * 16;
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-          ok = warp_wait<GIVEUP>(o_full, (uint32_t)(c & 1), abort_flag);
+          ok = warp_wait<GIVEUP>(&o_full[c & 1], (uint32_t)((c / 2) & 1), abort_flag);
           if (!ok) break;
           warp_arrive(&empty[c % kStages]);
           tc_fence_after();
-          const float* E = decay[c % kRing].E;
+          const float* E = decay[c % kRing].E + tok0;
+          const uint32_t ta = tl + 64 * (c & 1) + tok0;
 #pragma unroll 1
-          for (int tk = 0; tk < kC; tk += 8) {
+          for (int tk = 0; tk < 32; tk += 8) {
             float x[8], y[8];
-            tmem_ld8x2_wait(tl + kTm1 + tk, tl + kTm2 + tk, x, y);
+            tmem_ld8x2_wait(ta + kTm1 + tk, ta + kTm2 + tk, x, y);
             Tout* at = reinterpret_cast<Tout*>(stage) + tk % kTok * 32 + lane;
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
@@ -471,9 +490,9 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
               at[(j + 2) * 32] = from_f32<Tout>(fmaf(e.z, x[j + 2], y[j + 2]));
               at[(j + 3) * 32] = from_f32<Tout>(fmaf(e.w, x[j + 3], y[j + 3]));
             }
-            if (tk == kC - 8) {
+            if (tk == 24) {
               tc_fence_before();
-              warp_arrive(o_read);
+              warp_arrive(&o_read[c & 1]);
             }
             if ((tk + 8) % kTok == 0) {
               __syncwarp();
@@ -486,24 +505,27 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
               __syncwarp();
             }
           }
+          dst += 32 * step;  // the other half's tokens
+          r0 += 32;
         }
       }
-    } else if (warp < kCopyWarp || warp == 17) {
+    } else if (is_mask_warp(warp)) {
       // ======================== A: masked, decayed, to bf16, 32 columns a warp
       if constexpr (MODE == 0) {
         const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
         const uint32_t tl = tmem_lane(tmem, warp & 1);
-        const int col = warp == 17 ? 32 : 0;
+        const int col = warp == 25 ? 32 : 0;
         const float scale = p.scale;
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
           const Decay* d = &decay[c % kRing];
           ok = warp_wait<GIVEUP>(a_done, (uint32_t)(c & 1), abort_flag);
-          // the product that read A of the chunk before
-          if (ok && c > 0) ok = warp_wait<GIVEUP>(o_full, (uint32_t)((c - 1) & 1), abort_flag);
+          // the product that read the A that lies here
+          if (ok && c >= 2) ok = warp_wait<GIVEUP>(&o_full[c & 1], (uint32_t)((c / 2 - 1) & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
+          uint8_t* at = sm + kA + (c & 1) * kBlk;
           const float Gi = d->G[i];
           const uint32_t first = (uint32_t)d->first[i], span = (uint32_t)i - first;
 #pragma unroll 1
@@ -515,17 +537,17 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
               const float e = ex2(Gi - d->G[j0 + j]);
               x[j] = (uint32_t)(j0 + j) - first <= span ? x[j] * (scale * e) : 0.f;
             }
-            *reinterpret_cast<uint4*>(sm + kA + row_chunk(i, j0 / 8)) =
+            *reinterpret_cast<uint4*>(at + row_chunk(i, j0 / 8)) =
                 make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(a_ready);
+          warp_arrive(&a_ready[c & 1]);
         }
       }
-    } else if (warp >= kKeyWarp && warp < kKeyWarp + kKeyWarps) {
+    } else if (warp >= 22 && warp <= 30) {
       // ======================== K~ = w k as three bf16 parts (8 bits each: their sum is exact)
-      const int group = warp - kKeyWarp, vb = dv / 64;  // 16-byte pieces of a row: KB (vb) to a warp
+      const int group = key_warp(warp), vb = dv / 64;  // 16-byte pieces of a row: KB (vb) to a warp
       bool ok = true;
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
@@ -536,7 +558,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           // the products that read this half of the chunk before
           if (ok && c > 0)
             ok = hf == 0 ? warp_wait<GIVEUP>(kt_free, (uint32_t)((c - 1) & 1), abort_flag)
-                         : warp_wait<GIVEUP>(&u_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+                         : warp_wait<GIVEUP>(u_full, (uint32_t)((c - 1) & 1), abort_flag);
           if (!ok) break;
           const int r = 32 * hf + lane;
           const float w = decay[c % kRing].W[r];
