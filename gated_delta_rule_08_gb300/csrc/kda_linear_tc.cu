@@ -178,7 +178,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int KB = DK / 64;   // 64-channel blocks of q and k
   constexpr int KC = DK / 2;    // state columns of a thread
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBar);  // [stages] tiles landed and decays written
   uint64_t* empty = full + kStages;                         // [stages] the chunk's last products have been seen done
   uint64_t* a_done = empty + kStages;                       // D_A complete

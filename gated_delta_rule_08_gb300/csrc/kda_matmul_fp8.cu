@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kTallThreads, 1)
 matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
                 Tout* __restrict__ out, int M, int N, int nkb, int tiles_m, int tiles, unsigned int* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kTallBar);  // [stages] tiles landed
   uint64_t* mma_done = full + kTallStages;                      // [half][stages] accumulator complete, stage read
   uint64_t* acc_empty = mma_done + 2 * kTallStages;             // [half][2] accumulator read
@@ -351,7 +351,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
                 Tout* __restrict__ out, int M, int N, int nkb, int split, unsigned int* __restrict__ err) {
   using F = Flat<BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kBar);
   uint64_t* empty = full + F::kStages;
   uint64_t* acc_full = empty + F::kStages;

@@ -144,6 +144,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// try_wait that may sleep for up to `ns` nanoseconds.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
 // wait_or_abort_t for hand-overs that take less than a microsecond: polls first (a poll takes 15 clocks),
 // because a thread that try_wait has suspended comes back some hundreds of clocks late.
 template <bool kGiveUp>
@@ -156,9 +166,14 @@ __device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, vo
   }
   return wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
 }
+// The start of dynamic shared memory, rounded up to the swizzle's 1024 bytes, as a pointer that the compiler
+// still knows to be shared memory.
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) { return raw + ((0u - smem_u32(raw)) & 1023u); }
+
 // The same for a whole warp, which stays together: every branch is on a vote.  (Lanes that leave a polling
 // loop one by one, or one lane that polls for the others, stay apart afterwards, and the warp then runs the
 // work that follows once for each group.)
+constexpr uint32_t kPollNs = 1000000;
 template <bool kGiveUp>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if constexpr (kGiveUp) {
@@ -166,7 +181,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return false;
   } else {
     for (uint32_t i = 0; i < 20000000u; ++i) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kPollNs))) return true;
       if ((i & 63u) == 63u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
     }
     *abort_flag = 1;
