@@ -498,38 +498,71 @@ def kda_state_compose(P, b, S0=None, out=None):
 
 
 # ------------------------------------------------------------- operators around a recurrent layer
+# Calls for one token take a few microseconds on the device, so their marshalling is kept short: pointers
+# are passed as integers, and a tensor that is as it should be is recognised by four cheap comparisons.
 _BLOCK = 128  # values that share a scale
+_FP8 = torch.float8_e4m3fn
+_CODES = {torch.bfloat16: KDA_DTYPE_BF16, torch.float32: KDA_DTYPE_FP32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _code(t: torch.Tensor) -> int:
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def _device_index(t: torch.Tensor, name: str) -> int:
+    """Index of the tensor's device, which has to be the current one."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if index != _current_device():
+        raise ValueError(f"{name} is on cuda:{index}, the current device is cuda:{_current_device()}")
+    return index
+
+
+def _data(t: Optional[torch.Tensor], name: str, dtype, shape, index: int):
+    """The address of a dense tensor of that type, shape and device (None for None)."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        _check(t, name, dtype, shape, torch.device("cuda", index))
+    return t.data_ptr()
 
 
 def kda_rmsnorm_quant(x, weight=None, residual=None, *, eps: float = 1e-6, y=None, y_scale=None, residual_out=None):
     """RMS norm of x (+ residual) with e4m3 output and one scale for each 128 values.  x, residual:
     [rows, D], bf16 or fp32; weight: fp32 [D] or None.  residual_out may be the residual (in place).
     Returns (y [rows, D] float8_e4m3fn, y_scale [rows, ceil(D / 128)] fp32, x + residual or None)."""
-    lib = load_library()
-    dev = x.device
-    rows, D = x.shape
-    code = _dtype_code(x)
-    _check(x, "x", device=dev)
-    _check(residual, "residual", x.dtype, (rows, D), dev)
-    _check(weight, "weight", torch.float32, (D,), dev)
+    lib = _lib or load_library()
+    code = _code(x)
+    dev = _device_index(x, "x")
+    rows, D = shape = x.shape
+    px = _data(x, "x", x.dtype, shape, dev)
+    pr = _data(residual, "residual", x.dtype, shape, dev)
+    pw = _data(weight, "weight", torch.float32, (D,), dev)
+    blocks = (rows, (D + _BLOCK - 1) // _BLOCK)
     if y is None:
-        y = torch.empty(rows, D, device=dev, dtype=torch.float8_e4m3fn)
+        y = torch.empty_like(x, dtype=_FP8)
     else:
-        _check(y, "y", torch.float8_e4m3fn, (rows, D), dev)
-    blocks = (D + _BLOCK - 1) // _BLOCK
+        _data(y, "y", _FP8, shape, dev)
     if y_scale is None:
-        y_scale = torch.empty(rows, blocks, device=dev, dtype=torch.float32)
+        y_scale = torch.empty(blocks, device=x.device, dtype=torch.float32)
     else:
-        _check(y_scale, "y_scale", torch.float32, (rows, blocks), dev)
+        _data(y_scale, "y_scale", torch.float32, blocks, dev)
+    po = None
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
     elif residual_out is None:
         residual_out = torch.empty_like(x)
+        po = residual_out.data_ptr()
     else:
-        _check(residual_out, "residual_out", x.dtype, (rows, D), dev)
-    st = lib.kda_rmsnorm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(y_scale), rows,
-                               D, float(eps), code, _stream(dev))
+        po = _data(residual_out, "residual_out", x.dtype, shape, dev)
+    st = lib.kda_rmsnorm_quant(px, pr, pw, po, y.data_ptr(), y_scale.data_ptr(), rows, D, eps, code, _raw_stream(dev))
     if st != 0:
         raise KdaError("kda_rmsnorm_quant", st)
     return y, y_scale, residual_out
@@ -539,46 +572,39 @@ def kda_matmul_fp8(a, a_scale, b, b_scale, out=None, *, out_dtype: Optional[torc
     """a @ b.T of e4m3 rows with block scales.  a: [M, K] float8_e4m3fn with a_scale [M, ceil(K / 128)];
     b: [N, K] float8_e4m3fn (a weight) with b_scale [ceil(N / 128), ceil(K / 128)], scales fp32.
     Returns out [M, N] (out_dtype: bf16 unless given; bf16 or fp32)."""
-    lib = load_library()
-    dev = a.device
+    lib = _lib or load_library()
+    dev = _device_index(a, "a")
     M, K = a.shape
     N = b.shape[0]
     kb, nb = (K + _BLOCK - 1) // _BLOCK, (N + _BLOCK - 1) // _BLOCK
-    _check(a, "a", torch.float8_e4m3fn, (M, K), dev)
-    _check(a_scale, "a_scale", torch.float32, (M, kb), dev)
-    _check(b, "b", torch.float8_e4m3fn, (N, K), dev)
-    _check(b_scale, "b_scale", torch.float32, (nb, kb), dev)
+    pa = _data(a, "a", _FP8, (M, K), dev)
+    psa = _data(a_scale, "a_scale", torch.float32, (M, kb), dev)
+    pb = _data(b, "b", _FP8, (N, K), dev)
+    psb = _data(b_scale, "b_scale", torch.float32, (nb, kb), dev)
     if out is None:
-        out = torch.empty(M, N, device=dev, dtype=out_dtype or torch.bfloat16)
+        out = torch.empty((M, N), device=a.device, dtype=out_dtype or torch.bfloat16)
     else:
-        _check(out, "out", out_dtype, (M, N), dev)
-    st = lib.kda_matmul_fp8(_ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(out), M, N, K, _dtype_code(out),
-                            _stream(dev))
+        _data(out, "out", out_dtype or out.dtype, (M, N), dev)
+    st = lib.kda_matmul_fp8(pa, psa, pb, psb, out.data_ptr(), M, N, K, _code(out), _raw_stream(dev))
     if st != 0:
         raise KdaError("kda_matmul_fp8", st)
     return out
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+def _token_rows(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
     """Checks [tokens, H, d] whose heads are dense and whose tokens may lie further apart; returns the
     distance of two tokens in elements."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, H, d = shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else H * d
-
-
-def _head_decay(g: torch.Tensor, rows: int, H: int, device) -> int:
-    """1 if g is [rows, H] (a decay per token), 0 if it is [H]."""
-    per_token = g.dim() == 2
-    _check(g, "g", torch.float32, (rows, H) if per_token else (H,), device)
-    return int(per_token)
+    return s0 if n > 1 else H * d
 
 
 def kda_linear_chunk_fwd_workspace_size(B: int, T: int, H: int, dk: int, dv: int,
@@ -595,14 +621,13 @@ def kda_linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None
     [T_tot, H] or one constant per head [H]; h0: [B, H, dk, dv] fp32 or None; cu_seqlens: int32 [B+1]
     on the device or None (then B sequences of T_tot/B tokens).
     Returns (out [T_tot, H, dv], hT [B, H, dk, dv] or None)."""
-    lib = load_library()
-    dev = q.device
+    lib = _lib or load_library()
+    code = _code(q)
+    dev = _device_index(q, "q")
     T_tot, H, dk = q.shape
     dv = v.shape[2]
     dt = q.dtype
-    code = _dtype_code(q)
     if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", torch.int32, device=dev)
         nB = cu_seqlens.numel() - 1
         if B is not None and B != nB:
             raise ValueError("B does not match cu_seqlens")
@@ -612,26 +637,33 @@ def kda_linear_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, out=None, hT=None
         if T_tot % B:
             raise ValueError("without cu_seqlens, T_tot must be a multiple of B")
         T_arg = T_tot // B
+    pcu = _data(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
     qs = _token_rows(q, "q", dt, (T_tot, H, dk), dev)
     ks = _token_rows(k, "k", dt, (T_tot, H, dk), dev)
     vs = _token_rows(v, "v", dt, (T_tot, H, dv), dev)
-    per_token = _head_decay(g, T_tot, H, dev)
-    _check(h0, "h0", torch.float32, (B, H, dk, dv), dev)
+    per_token = g.dim() == 2
+    pg = _data(g, "g", torch.float32, (T_tot, H) if per_token else (H,), dev)
+    states = (B, H, dk, dv)
+    ph0 = _data(h0, "h0", torch.float32, states, dev)
     if out is None:
-        out = torch.empty(T_tot, H, dv, device=dev, dtype=out_dtype or dt)
-    _check(out, "out", out_dtype, (T_tot, H, dv), dev)
-    if hT is None and output_final_state:
-        hT = torch.empty(B, H, dk, dv, device=dev, dtype=torch.float32)
-    _check(hT, "hT", torch.float32, (B, H, dk, dv), dev)
-    need = int(lib.kda_linear_chunk_fwd_workspace_size(B, T_arg, H, dk, dv, code))
+        out = torch.empty((T_tot, H, dv), device=q.device, dtype=out_dtype or dt)
+    else:
+        _data(out, "out", out_dtype or out.dtype, (T_tot, H, dv), dev)
+    if hT is not None:
+        _data(hT, "hT", torch.float32, states, dev)
+    elif output_final_state:
+        hT = torch.empty(states, device=q.device, dtype=torch.float32)
+    need = lib.kda_linear_chunk_fwd_workspace_size(B, T_arg, H, dk, dv, code)
     if need == 0:
         raise KdaError("kda_linear_chunk_fwd_workspace_size", 2)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-    _check(workspace, "workspace", torch.uint8, None, dev)
-    st = lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(h0), _ptr(cu_seqlens), _ptr(out),
-                                  _ptr(hT), B, T_arg, H, dk, dv, qs, ks, vs, float(scale), code, _dtype_code(out),
-                                  _ptr(workspace), workspace.numel(), _stream(dev))
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    else:
+        need = workspace.numel()
+        _data(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    st = lib.kda_linear_chunk_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), pg, per_token, ph0, pcu, out.data_ptr(),
+                                  None if hT is None else hT.data_ptr(), B, T_arg, H, dk, dv, qs, ks, vs, scale, code,
+                                  _code(out), workspace.data_ptr(), need, _raw_stream(dev))
     if st != 0:
         raise KdaError("kda_linear_chunk_fwd", st)
     return out, hT
@@ -642,25 +674,26 @@ def kda_linear_decode_step(q, k, v, g, state_pool, slot_idx, out=None, *, scale:
     """One token of linear attention per request.  q, k: [N, H, dk]; v: [N, H, dv] (rows may be
     strided); g: log decay, fp32, [N, H] or one constant per head [H]; state_pool:
     [num_slots, H, dk, dv] fp32 (updated in place); slot_idx: int32 [N].  Returns out [N, H, dv]."""
-    lib = load_library()
-    dev = q.device
+    lib = _lib or load_library()
+    code = _code(q)
+    dev = _device_index(q, "q")
     N, H, dk = q.shape
     dv = v.shape[2]
     dt = q.dtype
-    code = _dtype_code(q)
     num_slots = state_pool.shape[0]
     qs = _token_rows(q, "q", dt, (N, H, dk), dev)
     ks = _token_rows(k, "k", dt, (N, H, dk), dev)
     vs = _token_rows(v, "v", dt, (N, H, dv), dev)
-    per_token = _head_decay(g, N, H, dev)
-    _check(state_pool, "state_pool", torch.float32, (num_slots, H, dk, dv), dev)
-    _check(slot_idx, "slot_idx", torch.int32, (N,), dev)
+    per_token = g.dim() == 2
+    pg = _data(g, "g", torch.float32, (N, H) if per_token else (H,), dev)
+    pp = _data(state_pool, "state_pool", torch.float32, (num_slots, H, dk, dv), dev)
+    ps = _data(slot_idx, "slot_idx", torch.int32, (N,), dev)
     if out is None:
-        out = torch.empty(N, H, dv, device=dev, dtype=out_dtype or dt)
-    _check(out, "out", out_dtype, (N, H, dv), dev)
-    st = lib.kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), per_token, _ptr(state_pool), _ptr(slot_idx),
-                                    _ptr(out), N, H, dk, dv, num_slots, qs, ks, vs, float(scale), code,
-                                    _dtype_code(out), _stream(dev))
+        out = torch.empty((N, H, dv), device=q.device, dtype=out_dtype or dt)
+    else:
+        _data(out, "out", out_dtype or out.dtype, (N, H, dv), dev)
+    st = lib.kda_linear_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), pg, per_token, pp, ps, out.data_ptr(), N, H, dk,
+                                    dv, num_slots, qs, ks, vs, scale, code, _code(out), _raw_stream(dev))
     if st != 0:
         raise KdaError("kda_linear_decode_step", st)
     return out

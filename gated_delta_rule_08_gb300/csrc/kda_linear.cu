@@ -18,8 +18,24 @@ namespace {
 
 // ------------------------------------------------------------------------------ sequences
 constexpr int kCols = 16;  // value columns of a CTA
-constexpr int kTile = 16;  // tokens staged at a time
+constexpr int kTile = 8;   // tokens of a stage
+constexpr int kRecStages = 6;  // the copies run five stages ahead: a token takes less time than a load
 constexpr int kRecThreads = 128;
+
+template <int DK>
+struct RecStage {
+  float k[kTile][DK], q[kTile][DK], v[kTile][kCols], g[kTile];
+};
+
+// `bytes` (4 or 16) of global memory to shared memory without registers; zeros if not `in`
+template <int bytes>
+__device__ __forceinline__ void cp_async_zero(void* dst, const void* src, bool in) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
 
 template <int DK, typename Tout>
 __global__ void __launch_bounds__(kRecThreads)
@@ -29,13 +45,14 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
                         float* hT, int B, int64_t T, int64_t T_tot, int H, int dv, float scale,
                         unsigned int* __restrict__ err) {
   constexpr int NI = DK / 32;  // groups of four rows of a thread
-  constexpr int kPer = kTile * DK / kRecThreads;
-  __shared__ __align__(16) float sk[kTile][DK], sq[kTile][DK];
-  __shared__ float sv[kTile][kCols], so[kTile][kCols], se[kTile];
+  extern __shared__ __align__(16) uint8_t rec_smem[];
+  RecStage<DK>* stages = reinterpret_cast<RecStage<DK>*>(rec_smem);
+  __shared__ float so[kTile][kCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = dv / kCols;
   const int slice = blockIdx.x % slices, bh = blockIdx.x / slices, h = bh % H, b = bh / H;
-  int64_t t0 = (int64_t)b * T, n = T;
+  int64_t t0 = (int64_t)b * T;
+  int n = (int)T;  // token counts fit 32 bits
   if (cu != nullptr) {
     if (!offsets_ok(cu, B, T_tot)) {
       if (tid == 0) atomicOr(err, KDA_DEVERR_BAD_SEQLENS);
@@ -52,56 +69,87 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[i][j] = h0 ? h0[soff + (int64_t)(32 * i + 4 * rg + j) * dv] : 0.f;
 
-  for (int64_t c = 0; c < n; c += kTile) {
-    const int m = (int)(n - c < kTile ? n - c : kTile);
-    float rk[kPer], rq[kPer];
+  // This thread's pieces of a stage: a row of k and q every kRowStep tokens, a piece of v, a decay.  Tokens past
+  // the sequence come as zeros with no decay (read from the sequence's first, of size 0).
+  constexpr int kRowStep = kRecThreads / (DK / 4), kRows = kTile / kRowStep;
+  const int r0 = tid / (DK / 4), d0 = tid % (DK / 4) * 4, rv = tid / (kCols / 4), dv0 = tid % (kCols / 4) * 4;
+  const float* pk = k + (t0 + r0) * k_stride + h * DK + d0;
+  const float* pq = q + (t0 + r0) * q_stride + h * DK + d0;
+  const float* pv = v + (t0 + rv) * v_stride + (int64_t)h * dv + slice * kCols + dv0;
+  const float* pg = g + (g_per_token ? (t0 + tid) * H + h : h);
+  const int64_t g_step = g_per_token ? (int64_t)kTile * H : 0;
+  int fetched = 0, put = 0;
+  auto fetch = [&] {
+    if (fetched < n) {
+      RecStage<DK>& st = stages[put];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kRecThreads, r = e / DK, d = e % DK;
-      const bool in = r < m;
-      rk[i] = in ? k[(t0 + c + r) * k_stride + h * DK + d] : 0.f;
-      rq[i] = in ? q[(t0 + c + r) * q_stride + h * DK + d] : 0.f;
-    }
-    float rv[kTile * kCols / kRecThreads];
-#pragma unroll
-    for (int i = 0; i < kTile * kCols / kRecThreads; ++i) {
-      const int e = tid + i * kRecThreads, r = e / kCols, d = e % kCols;
-      rv[i] = r < m ? v[(t0 + c + r) * v_stride + (int64_t)h * dv + slice * kCols + d] : 0.f;
-    }
-    float re = 1.f;
-    if (tid < m) re = expf(g_per_token ? g[(t0 + c + tid) * H + h] : g[h]);
-    __syncthreads();  // the previous tile has been read and its outputs stored
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid + i * kRecThreads;
-      (&sk[0][0])[e] = rk[i];
-      (&sq[0][0])[e] = rq[i];
-    }
-#pragma unroll
-    for (int i = 0; i < kTile * kCols / kRecThreads; ++i) (&sv[0][0])[tid + i * kRecThreads] = rv[i];
-    if (tid < kTile) se[tid] = re;
-    __syncthreads();
-#pragma unroll 4
-    for (int t = 0; t < m; ++t) {
-      const float e = se[t], x = sv[t][col];
-      float acc = 0.f;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&sk[t][32 * i + 4 * rg]);
-        const float4 q4 = *reinterpret_cast<const float4*>(&sq[t][32 * i + 4 * rg]);
-        s[i][0] = fmaf(k4.x, x, e * s[i][0]);
-        s[i][1] = fmaf(k4.y, x, e * s[i][1]);
-        s[i][2] = fmaf(k4.z, x, e * s[i][2]);
-        s[i][3] = fmaf(k4.w, x, e * s[i][3]);
-        acc = fmaf(q4.x, s[i][0], fmaf(q4.y, s[i][1], fmaf(q4.z, s[i][2], fmaf(q4.w, s[i][3], acc))));
+      for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i * kRowStep;
+        const bool in = fetched + r < n;
+        cp_async_zero<16>(&st.k[r][d0], in ? pk + i * kRowStep * k_stride : k, in);
+        cp_async_zero<16>(&st.q[r][d0], in ? pq + i * kRowStep * q_stride : q, in);
       }
+      if (tid < kTile * kCols / 4) cp_async_zero<16>(&st.v[rv][dv0], fetched + rv < n ? pv : v, fetched + rv < n);
+      if (tid < kTile) cp_async_zero<4>(&st.g[tid], fetched + tid < n ? pg : g, fetched + tid < n);
+      pk += kTile * k_stride;
+      pq += kTile * q_stride;
+      pv += kTile * v_stride;
+      pg += g_step;
+      fetched += kTile;
+      put = put + 1 < kRecStages ? put + 1 : 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRecStages - 1; ++i) fetch();
+  Tout* po = out + ((t0 + tid / kCols) * H + h) * dv + slice * kCols + tid % kCols;
+  int get = 0;
+#pragma unroll 1
+  for (int c = 0; c < n; c += kTile) {
+    const int m = n - c < kTile ? n - c : kTile;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRecStages - 2) : "memory");
+    __syncthreads();  // this stage has landed, and the one before has been read and its outputs stored
+    fetch();
+    const RecStage<DK>& st = stages[get];
+    get = get + 1 < kRecStages ? get + 1 : 0;
+    // Four tokens at a time: their states follow one another, but nothing else does, so the loads and the
+    // read-outs of one run beside the others'.
+#pragma unroll 1
+    for (int t = 0; t < kTile; t += 4) {
+      float acc[4];
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      if (rg == 0) so[t][col] = acc;
+      for (int u = 0; u < 4; ++u) {
+        const float e = expf(st.g[t + u]), x = st.v[t + u][col];
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float4 k4 = *reinterpret_cast<const float4*>(&st.k[t + u][32 * i + 4 * rg]);
+          const float4 q4 = *reinterpret_cast<const float4*>(&st.q[t + u][32 * i + 4 * rg]);
+          s[i][0] = fmaf(k4.x, x, e * s[i][0]);
+          s[i][1] = fmaf(k4.y, x, e * s[i][1]);
+          s[i][2] = fmaf(k4.z, x, e * s[i][2]);
+          s[i][3] = fmaf(k4.w, x, e * s[i][3]);
+          a0 = fmaf(q4.x, s[i][0], a0);
+          a1 = fmaf(q4.y, s[i][1], a1);
+          a0 = fmaf(q4.z, s[i][2], a0);
+          a1 = fmaf(q4.w, s[i][3], a1);
+        }
+        acc[u] = a0 + a1;
+      }
+      // sums over the eight row groups; lane rg keeps token t + (rg & 3)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float give = rg & 1 ? acc[2 * u] : acc[2 * u + 1];
+        acc[u] = (rg & 1 ? acc[2 * u + 1] : acc[2 * u]) + __shfl_xor_sync(0xffffffffu, give, 1);
+      }
+      float o = (rg & 2 ? acc[1] : acc[0]) + __shfl_xor_sync(0xffffffffu, rg & 2 ? acc[0] : acc[1], 2);
+      o += __shfl_xor_sync(0xffffffffu, o, 4);
+      if (rg < 4) so[t + rg][col] = o;
     }
     __syncthreads();
-    for (int e = tid; e < m * kCols; e += kRecThreads)
-      out[((t0 + c + e / kCols) * H + h) * dv + slice * kCols + e % kCols] = from_f32<Tout>(scale * (&so[0][0])[e]);
+    static_assert(kTile * kCols == kRecThreads, "one output a thread");
+    if (tid < m * kCols) *po = from_f32<Tout>(scale * (&so[0][0])[tid]);
+    po += (int64_t)kTile * H * dv;
   }
   if (hT) {
 #pragma unroll
@@ -115,9 +163,17 @@ template <typename Tout>
 cudaError_t recurrent_typed(const LinearArgs& a, cudaStream_t st) {
   const int64_t grid = (int64_t)a.B * a.H * (a.dv / kCols);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  static DeviceOnce once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  constexpr int kSmem = kRecStages * (int)sizeof(RecStage<128>);
+  const cudaError_t e = once.run(dev, [] {
+    return cudaFuncSetAttribute(linear_recurrent_kernel<128, Tout>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (e != cudaSuccess) return e;
   auto* kernel = a.dk == 64 ? linear_recurrent_kernel<64, Tout> : linear_recurrent_kernel<128, Tout>;
   TraceScope ts("kda_linear_recurrent", st);
-  kernel<<<(unsigned)grid, kRecThreads, 0, st>>>(
+  kernel<<<(unsigned)grid, kRecThreads, a.dk == 64 ? kRecStages * sizeof(RecStage<64>) : kSmem, st>>>(
       static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), a.q_stride,
       a.k_stride, a.v_stride, a.g, a.g_per_token, a.h0, a.cu_seqlens, static_cast<Tout*>(a.out), a.hT, a.B, a.T, a.T_tot, a.H,
       a.dv, a.scale, a.err);
