@@ -399,3 +399,32 @@ def test_same_call_same_bits():
                kda.kda_matmul_fp8(*mm)]
         assert ref is None or all(torch.equal(a, b) for a, b in zip(got, ref))
         ref = got
+
+
+# ------------------------------------------------------------------ waits that run out
+@pytest.mark.parametrize("what", ["matmul many rows", "matmul few rows", "linear", "linear in segments"])
+def test_waits_that_run_out_are_reported_and_the_device_stays_usable(what, monkeypatch):
+    """KDA_TEST_WAIT_TIMEOUT launches the variants whose waits give up at once: the call reports it, and the next
+    ordinary call is right."""
+    if what.startswith("matmul"):
+        ins = matmul_inputs(31, *((1280, 2304, 640) if "many" in what else (5, 300, 4096)))
+
+        def call():
+            check_matmul(ins, kda.kda_matmul_fp8(*ins))
+    else:
+        lengths = (2500,) if "segments" in what else (300, 70)
+        ins = linear_inputs(32, lengths, 2, 128, 128, BF, "token", True, False)
+
+        def call():
+            out, hT = kda.kda_linear_chunk_fwd(ins["q"], ins["k"], ins["v"], ins["g"], h0=ins["h0"], cu_seqlens=ins["cu"])
+            check_linear(ins, lengths, out, hT, 1.0)
+    monkeypatch.setenv("KDA_TEST_WAIT_TIMEOUT", "1")
+    if what.startswith("matmul"):
+        kda.kda_matmul_fp8(*ins)
+    else:
+        kda.kda_linear_chunk_fwd(ins["q"], ins["k"], ins["v"], ins["g"], h0=ins["h0"], cu_seqlens=ins["cu"])
+    assert binding.kda_get_device_error() & binding.DEVERR_WAIT_TIMEOUT
+    monkeypatch.delenv("KDA_TEST_WAIT_TIMEOUT")
+    for _ in range(2):
+        call()
+        no_device_error()
