@@ -313,19 +313,22 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
 }
 
 // ------------------------------------------------------------------------------ few rows
-constexpr int kFlatRows = 128;     // weight rows of a tile
-constexpr int kFlatThreads = 192;  // warps 0-3: read accumulators, scale, add up; warp 4 copies, warp 5 multiplies
+constexpr int kFlatRows = 128;  // weight rows of a tile
+// Warps 0-3 read accumulators, scale, add up: a thread owns a weight row; 4 copies, 5 multiplies, 6 makes the factors.
+constexpr int kFlatCopyWarp = 4, kFlatMmaWarp = 5, kFlatScaleWarp = 6, kFlatThreads = 224;
 
 template <int BN>
 struct Flat {
-  static constexpr int kBufs = BN <= 64 ? 4 : 2;  // accumulators; two CTAs share an SM's 512 columns
-  static constexpr uint32_t kCols = kBufs * BN < 32 ? 32 : kBufs * BN;
+  static constexpr int kBufs = 4;  // accumulators; two CTAs share an SM's 512 columns
+  static constexpr uint32_t kCols = kBufs * BN;
   static constexpr uint32_t kW = kFlatRows * kK, kStage = kW + BN * kK;
   static constexpr int kStages = 98304 / kStage;  // 96 KB: two CTAs per SM
+  static constexpr int kLd = BN + 4;              // factors of a block: one for each activation row
   static constexpr uint32_t kPart = BN * kFlatRows * 4;  // partial sums, over the stages once they are read
-  static constexpr uint32_t kScale = (kStages * kStage > kPart ? kStages * kStage : kPart);
-  static constexpr uint32_t kBar = kScale + 4 * 2 * BN * 4;  // factors: [warp][2][BN]
+  static constexpr uint32_t kScale = kStages * kStage;
+  static constexpr uint32_t kBar = kScale + 2 * kGroup * kLd * 4;
   static constexpr uint32_t kSmem = kBar + 256 + 1024;
+  static_assert(kPart <= kScale && kStages >= kBufs, "an accumulator is read before its stage's next MMAs");
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -336,14 +339,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// fp32 at the same shared-memory offset of CTA `rank` of the cluster
-__device__ __forceinline__ float load_peer(const float* p, uint32_t rank) {
+// four fp32 at the same shared-memory offset of CTA `rank` of the cluster
+__device__ __forceinline__ float4 load_peer(const float* p, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
+constexpr int kMaxSplit = 8;
 
 template <int BN, typename Tout, bool GIVEUP>
 __global__ void __launch_bounds__(kFlatThreads)
@@ -352,14 +356,16 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   using F = Flat<BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kBar);
-  uint64_t* empty = full + F::kStages;
-  uint64_t* acc_full = empty + F::kStages;
-  uint64_t* acc_empty = acc_full + F::kBufs;
-  uint64_t* bar_fin = acc_empty + F::kBufs;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kBar);  // [stages] tiles landed
+  uint64_t* mma_done = full + F::kStages;                      // [stages] accumulator complete, stage read
+  uint64_t* acc_empty = mma_done + F::kStages;                 // [bufs] accumulator read
+  uint64_t* sc_full = acc_empty + F::kBufs;                    // [2] group of factors there
+  uint64_t* sc_empty = sc_full + 2;                            // [2] group of factors read
+  uint64_t* bar_fin = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_fin + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* part = reinterpret_cast<float*>(sm);
+  float* fac = reinterpret_cast<float*>(sm + F::kScale);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
   const int n0 = blockIdx.x / split * kFlatRows, m0 = blockIdx.y * BN;
@@ -373,11 +379,12 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   if (tid == 32) {
     for (int i = 0; i < F::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&mma_done[i], 1);
     }
-    for (int i = 0; i < F::kBufs; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+    for (int i = 0; i < F::kBufs; ++i) mbar_init(&acc_empty[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sc_full[i], 1);
+      mbar_init(&sc_empty[i], 4);
     }
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
@@ -387,14 +394,14 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int issued = 0;  // stages whose copies warp 4 has started
+  int issued = 0;  // stages whose copies have been started
 
-  if (warp == 4) {
+  if (warp == kFlatCopyWarp) {
     if (lane == 0) {
       bool ok = true;
       for (; issued < cnt; ++issued) {
         const int it = issued, s = it % F::kStages;
-        if (it >= F::kStages) ok = spin_or_abort<GIVEUP>(&empty[s], (uint32_t)((it / F::kStages - 1) & 1), abort_flag);
+        if (it >= F::kStages) ok = spin_or_abort<GIVEUP>(&mma_done[s], (uint32_t)((it / F::kStages - 1) & 1), abort_flag);
         if (!ok) break;
         uint8_t* st = sm + s * F::kStage;
         mbar_arrive_expect_tx(&full[s], F::kStage);
@@ -402,7 +409,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         tma_load_2d(st + F::kW, &maps.a, (kb0 + it) * kK, m0, &full[s]);
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kFlatMmaWarp) {
     if (lane == 0) {
       bool ok = true;
       for (int it = 0; it < cnt && ok; ++it) {
@@ -414,39 +421,44 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         tc_fence_after();
         const uint8_t* st = sm + s * F::kStage;
         mma_block(tmem + BN * buf, st, st + F::kW, idesc_e4m3(kFlatRows, BN));
-        mma_commit(&empty[s]);
-        mma_commit(&acc_full[buf]);
+        mma_commit(&mma_done[s]);
       }
     }
-  } else {
-    constexpr int kPer = (BN + 31) / 32;  // factors a lane fetches
-    const uint32_t tl = tmem_lane(tmem, warp);
-    float* fac = reinterpret_cast<float*>(sm + F::kScale) + warp * 2 * BN;
+  } else if (warp == kFlatScaleWarp) {
+    bool ok = true;
     const float* pb = b_scale + (int64_t)(n0 / 128) * nkb + kb0;
+    for (int k0 = 0, grp = 0; k0 < cnt; k0 += kGroup, ++grp) {
+      const int slot = grp & 1, kb = k0 + (lane & 7);
+      if (grp >= 2) ok = warp_wait<GIVEUP>(&sc_empty[slot], (uint32_t)((grp / 2 - 1) & 1), abort_flag);
+      if (!ok) break;
+      if (kb < cnt) {
+        float* d = fac + (slot * kGroup + (lane & 7)) * F::kLd;
+        const float sb = __ldg(pb + kb);
+        float sa[BN / 4];
+#pragma unroll
+        for (int i = 0; i < BN / 4; ++i) {
+          const int m = m0 + (lane >> 3) + 4 * i;
+          sa[i] = m < M ? __ldg(a_scale + (int64_t)m * nkb + kb0 + kb) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < BN / 4; ++i) d[(lane >> 3) + 4 * i] = sa[i] * sb;
+      }
+      warp_arrive(&sc_full[slot]);
+    }
+  } else {
+    const uint32_t tl = tmem_lane(tmem, warp);
     uint64_t acc[BN / 2];
 #pragma unroll
     for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
-    float f[kPer];
-    auto fetch = [&](int it) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int j = lane + 32 * i, m = m0 + j;
-        f[i] = j < BN && m < M ? __ldg(a_scale + (int64_t)m * nkb + kb0 + it) * __ldg(pb + it) : 0.f;
-      }
-    };
-    if (cnt > 0) fetch(0);
     bool ok = true;
+#pragma unroll 1
     for (int it = 0; it < cnt; ++it) {
-      const int buf = it % F::kBufs;
-      float* fw = fac + (it & 1) * BN;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (lane + 32 * i < BN) fw[lane + 32 * i] = f[i];
-      __syncwarp();
-      if (it + 1 < cnt) fetch(it + 1);
-      ok = warp_wait<GIVEUP>(&acc_full[buf], (uint32_t)((it / F::kBufs) & 1), abort_flag);
+      const int s = it % F::kStages, buf = it % F::kBufs, slot = (it / kGroup) & 1, kg = it % kGroup;
+      if (kg == 0) ok = warp_wait<GIVEUP>(&sc_full[slot], (uint32_t)((it / kGroup / 2) & 1), abort_flag);
+      ok = ok && warp_wait<GIVEUP>(&mma_done[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
       if (!ok) break;
       tc_fence_after();
+      const float* f = fac + (slot * kGroup + kg) * F::kLd;
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c) {
         float v[16];
@@ -458,11 +470,12 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 s = *reinterpret_cast<const float4*>(fw + 16 * c + 4 * i);
-          acc_fma2(acc[8 * c + 2 * i], s.x, s.y, v[4 * i], v[4 * i + 1]);
-          acc_fma2(acc[8 * c + 2 * i + 1], s.z, s.w, v[4 * i + 2], v[4 * i + 3]);
+          const float4 w = *reinterpret_cast<const float4*>(f + 16 * c + 4 * i);
+          acc_fma2(acc[8 * c + 2 * i], w.x, w.y, v[4 * i], v[4 * i + 1]);
+          acc_fma2(acc[8 * c + 2 * i + 1], w.z, w.w, v[4 * i + 2], v[4 * i + 3]);
         }
       }
+      if (kg == kGroup - 1) warp_arrive(&sc_empty[slot]);
     }
     // Every copy has landed and every MMA has read its stage once the last accumulator is complete (the
     // MMAs complete in order), so the partial sums may lie over the stages.  After a wait that ran out the
@@ -479,21 +492,42 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   }
   tc_fence_before();
   __syncthreads();
-  drain_after_abort<F::kStages>(abort_flag, tid == 4 * 32, tid == 5 * 32, full, issued, bar_fin, err);
+  drain_after_abort<F::kStages>(abort_flag, tid == kFlatCopyWarp * 32, tid == kFlatMmaWarp * 32, full, issued, bar_fin, err);
   if (split > 1) cluster_sync();
   tc_fence_after();
-  // the activation rows are dealt to the CTAs of the cluster; each sums the partial sums in rank order
-  const int rows = M - m0 < BN ? M - m0 : BN;
+  // The activation rows are dealt to the warps of the cluster's CTAs; each sums the partial sums in rank order, four
+  // columns a thread.
+  const int rows = M - m0 < BN ? M - m0 : BN, n = n0 + 4 * lane;
   if (!*abort_flag) {
-    for (int j = rank; j < rows; j += split) {
-      for (int n = tid; n < kFlatRows; n += kFlatThreads) {
-        if (n0 + n >= N) continue;
-        const float* p = part + j * kFlatRows + n;
-        float x = 0.f;
-        if (split == 1) x = *p;
-        else
-          for (int r = 0; r < split; ++r) x += load_peer(p, r);
-        out[(int64_t)(m0 + j) * N + n0 + n] = from_f32<Tout>(x);
+    for (int j = rank + split * warp; j < rows; j += split * (kFlatThreads / 32)) {
+      const float* p = part + j * kFlatRows + 4 * lane;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (split == 1) {
+        x = *reinterpret_cast<const float4*>(p);
+      } else {
+        float4 y[kMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split) y[r] = load_peer(p, r);
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split) x = make_float4(x.x + y[r].x, x.y + y[r].y, x.z + y[r].z, x.w + y[r].w);
+      }
+      Tout* dst = out + (int64_t)(m0 + j) * N + n;
+      if (N % 4 == 0) {
+        if (n < N) {
+          if constexpr (sizeof(Tout) == 4) {
+            *reinterpret_cast<float4*>(dst) = x;
+          } else {
+            const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+            *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(h);
+          }
+        }
+      } else {
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) dst[e] = from_f32<Tout>(v[e]);
       }
     }
   }
@@ -531,7 +565,6 @@ cudaError_t prepare_device(int* sms) {
     if (e == cudaSuccess) e = allow_flat<16>();
     if (e == cudaSuccess) e = allow_flat<32>();
     if (e == cudaSuccess) e = allow_flat<64>();
-    if (e == cudaSuccess) e = allow_flat<128>();
     if (e != cudaSuccess) return e;
     return cudaDeviceGetAttribute(&g_state.sms[dev], cudaDevAttrMultiProcessorCount, dev);
   });
@@ -551,7 +584,7 @@ cudaError_t launch_flat(const MatmulArgs& a, int sms, cudaStream_t st) {
   // as many CTAs as fit two to an SM, with two blocks each at least
   int64_t split = 2 * (int64_t)sms / (tiles * rows);
   if (split > nkb / 2) split = nkb / 2;
-  if (split > 8) split = 8;
+  if (split > kMaxSplit) split = kMaxSplit;
   if (split < 1) split = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)rows);
@@ -576,12 +609,11 @@ cudaError_t launch(const MatmulArgs& a, cudaStream_t st) {
   const cudaError_t e = prepare_device(&sms);
   if (e != cudaSuccess) return e;
   const int64_t tiles_m = (a.M + kTallM - 1) / kTallM, tiles = tiles_m * ((a.N + kTallN - 1) / kTallN);
-  if (tiles * 2 < sms) {
-    if (a.M <= 16) return launch_flat<16, Tout>(a, sms, st);
-    if (a.M <= 32) return launch_flat<32, Tout>(a, sms, st);
-    if (a.M <= 64) return launch_flat<64, Tout>(a, sms, st);
-    return launch_flat<128, Tout>(a, sms, st);
-  }
+  // Few rows, or so few tiles that most SMs would have none (256 x 4096 x 4096, 32 tiles of 152 SMs: 15.3 against
+  // 19.5 us; 128 x 12288 x 4096, 48 tiles: over 25 against 20.3)
+  if (a.M <= 16) return launch_flat<16, Tout>(a, sms, st);
+  if (a.M <= 32) return launch_flat<32, Tout>(a, sms, st);
+  if (a.M <= 64 || tiles * 4 < sms) return launch_flat<64, Tout>(a, sms, st);
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
   Maps maps;
   if (!tensor_map_2d(&maps.a, a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.K, kTallM, kK) ||
