@@ -380,7 +380,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (MODE == 1 && lane == 0) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = any ? 0.f : exp2f(total + lost);
     } else if (warp == kMmaWarp) {
       // ======================== D_A and D_U
-      if (lane == 0) {
+      {
+        const bool leader = lane == 0;
         constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, true, true);
         const uint64_t d_kt = smem_desc_sw128(smem_u32(sm + kKt), kBlk, 1024);
         bool ok = true;
@@ -389,8 +390,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const int s = c % kStages;
           const uint8_t* st = sm + s * kStageBytes;
           if constexpr (MODE == 0) {
-            ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
-            if (ok && c > 0) ok = spin_or_abort<GIVEUP>(&a_ready[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+            ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
+            if (ok && c > 0) ok = warp_wait<GIVEUP>(&a_ready[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
@@ -398,30 +399,31 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             for (int b = 0; b < KB; ++b)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                mma_bf16_ss(tmem + kTmA, desc_add(dq, b * kPair + i * 32), desc_add(dk, b * kPair + i * 32), id_a, b + i > 0);
-            mma_commit(a_done);
+                mma_bf16_ss_by(leader, tmem + kTmA, desc_add(dq, b * kPair + i * 32), desc_add(dk, b * kPair + i * 32), id_a, b + i > 0);
+            mma_commit_by(leader, a_done);
           }
-          if (c > 0) ok = spin_or_abort<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
+          if (c > 0) ok = warp_wait<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // by halves of 32 tokens
-            ok = ok && spin_or_abort<GIVEUP>(&kt_ready[hf], (uint32_t)(c & 1), abort_flag);
+            ok = ok && warp_wait<GIVEUP>(&kt_ready[hf], (uint32_t)(c & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 3; ++i)
-                mma_bf16_ss(tmem + kTmU, desc_add(d_v, hf * 4096 + j * 2048),
+                mma_bf16_ss_by(leader, tmem + kTmU, desc_add(d_v, hf * 4096 + j * 2048),
                             desc_add(d_kt, i * 2 * kBlk + hf * 4096 + j * 2048), id_u, hf + i + j > 0);
-            mma_commit(hf == 0 ? kt_free : u_full);
+            mma_commit_by(leader, hf == 0 ? kt_free : u_full);
           }
           if (!ok) break;
         }
       }
     } else if (warp == kMmaOutWarp) {
       // ======================== D_2 and D_1
-      if (MODE == 0 && lane == 0) {
+      if constexpr (MODE == 0) {
+        const bool leader = lane == 0;
         constexpr uint32_t id_1 = idesc_bf16_f32(128, kC, false, false), id_2 = idesc_bf16_f32(128, kC, true, false);
         const uint64_t d_a = smem_desc_sw128(smem_u32(sm + kA), 16, 1024);
         bool ok = true;
@@ -430,28 +432,28 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const uint8_t* st = sm + (c % kStages) * kStageBytes;
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
           const uint32_t buf = c & 1;
-          ok = spin_or_abort<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
-          if (ok && c >= 2) ok = spin_or_abort<GIVEUP>(&o_read[buf], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+          ok = warp_wait<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
+          if (ok && c >= 2) ok = warp_wait<GIVEUP>(&o_read[buf], (uint32_t)((c / 2 - 1) & 1), abort_flag);
           if (ok && c == nc - 1) {
             // V's rows past the sequence are cleared with K~; the state tells that the chunk before has passed there
-            ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
-                 spin_or_abort<GIVEUP>(&kt_ready[0], (uint32_t)(c & 1), abort_flag) &&
-                 spin_or_abort<GIVEUP>(&kt_ready[1], (uint32_t)(c & 1), abort_flag);
+            ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
+                 warp_wait<GIVEUP>(&kt_ready[0], (uint32_t)(c & 1), abort_flag) &&
+                 warp_wait<GIVEUP>(&kt_ready[1], (uint32_t)(c & 1), abort_flag);
           }
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
-            mma_bf16_ss(tmem + kTm2 + 64 * buf, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
-          if (c < nc - 1) ok = spin_or_abort<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
+            mma_bf16_ss_by(leader, tmem + kTm2 + 64 * buf, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
+          if (c < nc - 1) ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_f16_ts(tmem + kTm1 + 64 * buf, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
-          mma_commit(&o_full[buf]);
+              mma_bf16_ts_by(leader, tmem + kTm1 + 64 * buf, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
+          mma_commit_by(leader, &o_full[buf]);
         }
       }
     } else if (warp >= kOutWarp && warp < kOutWarp + kOutWarps) {

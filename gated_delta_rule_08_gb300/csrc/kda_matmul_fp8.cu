@@ -31,18 +31,11 @@ constexpr int kK = 128;  // values of a scale block = bytes of a stage's row
 constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-      : "memory");
-}
 // One block of 128: P = A B^T, K = 32 bytes per MMA.
-__device__ __forceinline__ void mma_block(uint32_t d, const uint8_t* a, const uint8_t* b, uint32_t idesc) {
+__device__ __forceinline__ void mma_block(bool leader, uint32_t d, const uint8_t* a, const uint8_t* b, uint32_t idesc) {
   const uint64_t da = smem_desc_sw128(smem_u32(a), 16, 1024), db = smem_desc_sw128(smem_u32(b), 16, 1024);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mma_f8(d, desc_add(da, 32 * i), desc_add(db, 32 * i), idesc, i > 0);
+  for (int i = 0; i < 4; ++i) mma_f8_ss_by(leader, d, desc_add(da, 32 * i), desc_add(db, 32 * i), idesc, i > 0);
 }
 
 // acc (two fp32 lanes) += s * d
@@ -147,7 +140,8 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
           tma_load_2d(st + kTallA, &maps.b, kb * kK, n0, &full[s]);
         }
       }
-    } else if (warp >= kTallMmaWarp && lane == 0) {
+    } else if (warp >= kTallMmaWarp) {
+      const bool leader = lane == 0;
       const int half = (warp - kTallMmaWarp) >> 1, buf = warp & 1;
       int64_t it = 0;
       bool ok = true;
@@ -155,14 +149,14 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
           if ((it & 1) != buf) continue;
           const int s = (int)(it % kTallStages);
-          ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
+          ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
           if (ok && it >= 2)
-            ok = spin_or_abort<GIVEUP>(&acc_empty[2 * half + buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
+            ok = warp_wait<GIVEUP>(&acc_empty[2 * half + buf], (uint32_t)((it / 2 - 1) & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint8_t* st = sm + s * kTallStage;
-          mma_block(tmem + 256 * buf + 128 * half, st, st + kTallA + half * 128 * kK, idesc_e4m3(kTallM, kTallN / 2));
-          mma_commit(&mma_done[half * kTallStages + s]);
+          mma_block(leader, tmem + 256 * buf + 128 * half, st, st + kTallA + half * 128 * kK, idesc_e4m3(kTallM, kTallN / 2));
+          mma_commit_by(leader, &mma_done[half * kTallStages + s]);
         }
       }
     } else if (warp == kTallScaleWarp) {
@@ -410,18 +404,19 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       }
     }
   } else if (warp == kFlatMmaWarp) {
-    if (lane == 0) {
+    {
+      const bool leader = lane == 0;
       bool ok = true;
       for (int it = 0; it < cnt && ok; ++it) {
         const int s = it % F::kStages, buf = it % F::kBufs;
-        ok = spin_or_abort<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
+        ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
         if (ok && it >= F::kBufs)
-          ok = spin_or_abort<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
+          ok = warp_wait<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint8_t* st = sm + s * F::kStage;
-        mma_block(tmem + BN * buf, st, st + F::kW, idesc_e4m3(kFlatRows, BN));
-        mma_commit(&mma_done[s]);
+        mma_block(leader, tmem + BN * buf, st, st + F::kW, idesc_e4m3(kFlatRows, BN));
+        mma_commit_by(leader, &mma_done[s]);
       }
     }
   } else if (warp == kFlatScaleWarp) {

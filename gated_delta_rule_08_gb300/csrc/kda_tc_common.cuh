@@ -200,6 +200,41 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
       : "memory");
 }
 
+// MMAs and commits that a whole warp runs through and one lane (`leader`) issues: with warp-uniform control
+// flow the descriptors stay in uniform registers, where the instruction wants them (in a branch of one lane
+// every one of them is moved there first, at some 200 clocks an MMA in a busy SM).
+__device__ __forceinline__ void mma_bf16_ss_by(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_by(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_ss_by(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(leader ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_by(bool leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(leader ? 1u : 0u)
+      : "memory");
+}
+
 // Two fp32 lanes per instruction (each lane rounded as the scalar operation).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
