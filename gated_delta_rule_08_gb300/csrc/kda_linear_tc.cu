@@ -11,7 +11,8 @@
 // A CTA walks over the chunks of one (sequence, head) or of a segment of it.  Everything is laid out with
 // the value channel as the tensor core's row (M = 128; with dv = 64 the upper rows are not used):
 //   D_A [128 x 64]  = [Q ; K] K^T     rows 0-63 are q_i . k_j (the stack fills the 128 rows an MMA has)
-//   D_U [dv x dk]   = V^T K~          K~ = w_j k_j as the exact sum of three bf16 parts, so U has fp32 accuracy
+//   D_U [dv x dk]   = V~^T K          V~ = w_j v_j as the exact sum of three bf16 parts, so U has fp32 accuracy;
+//                                     V~^T lies in TMEM, which keeps it off the shared memory that bounds the chunk
 //   D_2 [dv x 64]   = V^T A^T         A masked, decayed, scaled and rounded to bf16 in shared memory
 //   D_1 [dv x 64]   = S^T Q^T         S^T rounded to bf16 in TMEM
 // with S^T itself (fp32) in the registers of warps 0-7.  So out is off by the roundings of A and S to
@@ -21,9 +22,9 @@
 // state: sums start again at 0 after it, and pairs with such a token between them are masked, so that no
 // infinity meets another and a long sum loses no precision.
 //
-// Warps: 0 copies and decays, 1 the MMAs that do not need the state (D_A, D_U), 2 those that end in the output
-// (D_1, D_2), 4-11 state, 12-19 output (two per TMEM lane quadrant each), 20, 21 and 25 A, the others from 22 to 30
-// K~.  A, D_1 and D_2 lie twice, so that A is made and the output read while the next chunk's products run.
+// Warps: 0 copies and decays, 1, 28 and 29 A, 4-11 state, 12-19 output, 20-27 V~ (two per TMEM lane quadrant each;
+// in MODE 1 the output warps make V~ too), 30 the MMAs that do not need the state (D_A, D_U), 31 those that end in
+// the output (D_1, D_2).  A lies twice, so that the next chunk's is made while one is multiplied.
 //
 // Few long sequences would leave most of the device idle, so they are cut into segments: MODE 1 runs
 // compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
@@ -39,19 +40,17 @@ using namespace tcx;
 
 constexpr int kC = 64;                      // tokens of a chunk
 constexpr int kThreads = 1024;
-constexpr int kCopyWarp = 0, kMmaWarp = 1, kMmaOutWarp = 2, kStateWarp = 4, kStateWarps = 8, kOutWarp = 12, kOutWarps = 8,
-              kMaskWarps = 3, kKeyWarps = 8;
-__device__ __forceinline__ bool is_mask_warp(int w) { return w == 20 || w == 21 || w == 25; }  // lanes 0-63 of TMEM
-__device__ __forceinline__ int key_warp(int w) { return w < 25 ? w - 22 : w - 23; }            // 0-7 of 22-24 and 26-30
+constexpr int kCopyWarp = 0, kMmaWarp = 30, kMmaOutWarp = 31, kStateWarp = 4, kStateWarps = 8, kOutWarp = 12, kOutWarps = 8,
+              kValueWarp = 20, kValueWarps = 8, kMaskWarps = 3;
+__device__ __forceinline__ bool is_mask_warp(int w) { return w == 1 || w == 28 || w == 29; }  // lanes 0-63 of TMEM
 // Registers: the state warps hold 64 state values a thread; the other groups of four give them theirs.
 constexpr int kStateRegs = 112, kOtherRegs = 48;
 static_assert(kStateWarps * 32 * kStateRegs + 24 * 32 * kOtherRegs <= kThreads * 64, "registers of the launch");
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 // a stage: [Q | K] of the first 64 channels, [Q | K] of the second, V of the first 64 channels, of the second
 constexpr uint32_t kBlk = 8192;             // 64 tokens x 64 channels
 constexpr uint32_t kQ = 0, kKey = kBlk, kPair = 2 * kBlk, kV = 4 * kBlk, kStageBytes = 6 * kBlk;
-constexpr uint32_t kKt = kStages * kStageBytes;         // K~: three parts of two blocks
-constexpr uint32_t kA = kKt + 6 * kBlk;                 // A [64 i][64 j], twice
+constexpr uint32_t kA = kStages * kStageBytes;           // A [64 i][64 j], twice
 constexpr uint32_t kOut = kA + 2 * kBlk, kOutBytes = 1024;  // output rows of each output warp's 32 value channels
 constexpr int kRing = 8;                                // decays: read until the state has been updated
 constexpr uint32_t kDecay = kOut + kOutWarps * kOutBytes;
@@ -68,7 +67,7 @@ constexpr uint32_t kSmem = kBar + 256 + 1024;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // TMEM columns
-constexpr uint32_t kTmA = 0, kTmS = 64, kTm1 = 128, kTm2 = 256, kTmU = 384;  // D_1 and D_2 twice, 64 columns apart
+constexpr uint32_t kTmA = 0, kTmS = 64, kTm1 = 128, kTm2 = 192, kTmU = 256, kTmV = 384;  // V~^T: three parts of 32
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kEmpty = -150.f;
@@ -171,6 +170,72 @@ __device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n
   return total;
 }
 
+// V~^T = w_j v_j as three bf16 parts (8 bits each: their sum is exact) into TMEM, token pairs packed: TOK tokens of
+// 32 value channels (this warp's TMEM lane quadrant) of every chunk.
+template <int TOK, int KB, bool GIVEUP>
+__device__ __forceinline__ void make_values(uint8_t* sm, const Decay* decay, uint64_t* full, uint64_t* vt_ready, uint64_t* vt_free,
+                                            uint64_t* u_full, volatile int* abort_flag, uint32_t tmem, int set, int nc, int rows,
+                                            int dv) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tok0 = set * TOK, hf = tok0 / 32;
+  const int ch = (warp & 3) * 32 + lane;  // value channel
+  const uint32_t tl = tmem_lane(tmem, warp) + kTmV + tok0 / 2;
+  // the channel's place in a row: a 16-byte piece, permuted by the row, and two bytes of it
+  const uint32_t base = kV + (uint32_t)(ch >> 6) * kBlk + (uint32_t)tok0 * 128u + (uint32_t)(ch & 7) * 2u;
+  const uint32_t piece = (uint32_t)((ch & 63) >> 3) << 4;
+  const bool live = (warp & 3) * 32 < dv;
+  bool ok = true;
+#pragma unroll 1
+  for (int c = 0; c < nc; ++c) {
+    uint8_t* st = sm + (c % kStages) * kStageBytes;
+    ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
+    // the products that read this half of the chunk before
+    if (ok && c > 0) ok = warp_wait<GIVEUP>(hf == 0 ? vt_free : u_full, (uint32_t)((c - 1) & 1), abort_flag);
+    if (!ok) break;
+    tc_fence_after();
+    const int left = rows - c * kC;
+    if (left < tok0 + TOK) {
+      // rows past the sequence meet weights of 0, but may hold anything: clear them, a quarter of the channels a warp
+      for (int i = lane; i < TOK * 4; i += 32) {
+        const int r = tok0 + i / 4, j = (warp & 1) * 4 + i % 4, blk = (warp >> 1) & 1;
+        if (r < left) continue;
+        if (blk < KB) *reinterpret_cast<uint4*>(st + kKey + blk * kPair + row_chunk(r, j)) = make_uint4(0u, 0u, 0u, 0u);
+        if (live) *reinterpret_cast<uint4*>(st + kV + blk * kBlk + row_chunk(r, j)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    if (live) {
+      const float* W = decay[c % kRing].W + tok0;
+#pragma unroll 1
+      for (int b = 0; b < TOK / 16; ++b) {
+        uint32_t p0[8], p1[8], p2[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* r0 = st + base + (uint32_t)b * 2048u + (uint32_t)(2 * i) * 128u;
+          const uint32_t v0 = *reinterpret_cast<const uint16_t*>(r0 + (piece ^ ((2 * i) & 7) << 4));
+          const uint32_t v1 = *reinterpret_cast<const uint16_t*>(r0 + 128 + (piece ^ ((2 * i + 1) & 7) << 4));
+          const float2 w = *reinterpret_cast<const float2*>(W + 16 * b + 2 * i);
+          const float2 x = mul2(w, make_float2(__uint_as_float(v0 << 16), __uint_as_float(v1 << 16)));
+          const uint32_t h0 = __float_as_uint(x.x), h1 = __float_as_uint(x.y);
+          const float2 y = sub2(x, make_float2(__uint_as_float(h0 & 0xffff0000u), __uint_as_float(h1 & 0xffff0000u)));
+          const uint32_t m0 = __float_as_uint(y.x), m1 = __float_as_uint(y.y);
+          const float2 z = sub2(y, make_float2(__uint_as_float(m0 & 0xffff0000u), __uint_as_float(m1 & 0xffff0000u)));
+          p0[i] = __byte_perm(h0, h1, 0x7632);
+          p1[i] = __byte_perm(m0, m1, 0x7632);
+          p2[i] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
+        }
+        tmem_st8u(tl + 8 * b, p0);
+        tmem_st8u(tl + 32 + 8 * b, p1);
+        tmem_st8u(tl + 64 + 8 * b, p2);
+      }
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    warp_arrive(&vt_ready[hf]);
+  }
+}
+
 // MODE 0: states and outputs.  MODE 1: a segment's contribution to the state after it, and its decay.
 template <int DK, int MODE, typename Tout, bool GIVEUP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -183,13 +248,13 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint64_t* empty = full + kStages;                         // [stages] the chunk's last products have been seen done
   uint64_t* a_done = empty + kStages;                       // D_A complete
   uint64_t* a_ready = a_done + 1;                           // [2] A written, D_A read
-  uint64_t* kt_ready = a_done + 3;                          // [2] half of K~ written (and V's rows past the sequence cleared)
-  uint64_t* kt_free = a_done + 5;                           // first half of K~ read by its MMAs (the second: u_full)
+  uint64_t* vt_ready = a_done + 3;                          // [2] half of V~ written (and the rows past the sequence cleared)
+  uint64_t* vt_free = a_done + 5;                           // first half of V~ read by its MMAs (the second: u_full)
   uint64_t* u_full = a_done + 6;                            // D_U complete
   uint64_t* u_empty = a_done + 7;                           // D_U read
   uint64_t* s_ready = a_done + 8;                           // S^T in TMEM
   uint64_t* o_full = a_done + 9;                            // [2] D_1 and D_2 complete
-  uint64_t* o_read = a_done + 11;                           // [2] D_1 and D_2 read
+  uint64_t* o_read = a_done + 11;                           // D_1 and D_2 read
   uint64_t* bar_fin = a_done + 13;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(a_done + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -224,16 +289,16 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       mbar_init(&empty[i], kStateWarps + (MODE == 0 ? kOutWarps : 0));
     }
     mbar_init(a_done, 1);
-    mbar_init(kt_free, 1);
+    mbar_init(vt_free, 1);
     mbar_init(u_full, 1);
     mbar_init(u_empty, kStateWarps);
     mbar_init(s_ready, kStateWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&a_ready[i], kMaskWarps);
-      mbar_init(&kt_ready[i], kKeyWarps);
+      mbar_init(&vt_ready[i], (MODE == 0 ? kValueWarps : kValueWarps + kOutWarps) / 2);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_read[i], kOutWarps);
     }
+    mbar_init(o_read, kOutWarps);
     mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
@@ -382,8 +447,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       // ======================== D_A and D_U
       {
         const bool leader = lane == 0;
-        constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, true, true);
-        const uint64_t d_kt = smem_desc_sw128(smem_u32(sm + kKt), kBlk, 1024);
+        constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, false, true);
         bool ok = true;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -403,19 +467,19 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
             mma_commit_by(leader, a_done);
           }
           if (c > 0) ok = warp_wait<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
-          const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024);
+          const uint64_t d_k = smem_desc_sw128(smem_u32(st + kKey), kPair, 1024);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // by halves of 32 tokens
-            ok = ok && warp_wait<GIVEUP>(&kt_ready[hf], (uint32_t)(c & 1), abort_flag);
+            ok = ok && warp_wait<GIVEUP>(&vt_ready[hf], (uint32_t)(c & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int i = 0; i < 3; ++i)
-                mma_bf16_ss_by(leader, tmem + kTmU, desc_add(d_v, hf * 4096 + j * 2048),
-                            desc_add(d_kt, i * 2 * kBlk + hf * 4096 + j * 2048), id_u, hf + i + j > 0);
-            mma_commit_by(leader, hf == 0 ? kt_free : u_full);
+                mma_bf16_ts_by(leader, tmem + kTmU, tmem + kTmV + 32 * i + 16 * hf + 8 * j, desc_add(d_k, hf * 4096 + j * 2048),
+                               id_u, hf + i + j > 0);
+            mma_commit_by(leader, hf == 0 ? vt_free : u_full);
           }
           if (!ok) break;
         }
@@ -433,18 +497,18 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
           const uint32_t buf = c & 1;
           ok = warp_wait<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
-          if (ok && c >= 2) ok = warp_wait<GIVEUP>(&o_read[buf], (uint32_t)((c / 2 - 1) & 1), abort_flag);
+          if (ok && c > 0) ok = warp_wait<GIVEUP>(o_read, (uint32_t)((c - 1) & 1), abort_flag);
           if (ok && c == nc - 1) {
-            // V's rows past the sequence are cleared with K~; the state tells that the chunk before has passed there
+            // rows past the sequence are cleared with V~; the state tells that the chunk before has passed there
             ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
-                 warp_wait<GIVEUP>(&kt_ready[0], (uint32_t)(c & 1), abort_flag) &&
-                 warp_wait<GIVEUP>(&kt_ready[1], (uint32_t)(c & 1), abort_flag);
+                 warp_wait<GIVEUP>(&vt_ready[0], (uint32_t)(c & 1), abort_flag) &&
+                 warp_wait<GIVEUP>(&vt_ready[1], (uint32_t)(c & 1), abort_flag);
           }
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
-            mma_bf16_ss_by(leader, tmem + kTm2 + 64 * buf, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
+            mma_bf16_ss_by(leader, tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
           if (c < nc - 1) ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -452,14 +516,16 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_bf16_ts_by(leader, tmem + kTm1 + 64 * buf, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
+              mma_bf16_ts_by(leader, tmem + kTm1, tmem + kTmS + 32 * b + 8 * i, desc_add(d_q, b * kPair + i * 32), id_1, b + i > 0);
           mma_commit_by(leader, &o_full[buf]);
         }
       }
     } else if (warp >= kOutWarp && warp < kOutWarp + kOutWarps) {
       // ======================== output: 32 tokens of 32 value channels, by way of shared memory
-      if constexpr (MODE == 0) {
-        constexpr int kTok = kOutBytes / (32 * sizeof(Tout));      // tokens at a time: 16, or 8 in fp32
+      if constexpr (MODE == 1) {
+        make_values<16, KB, GIVEUP>(sm, decay, full, vt_ready, vt_free, u_full, abort_flag, tmem, 2 + ((warp - kOutWarp) >> 2), nc, rows,
+                                dv);
+      } else {
         constexpr int kLanes = 32 * sizeof(Tout) / 16;             // lanes that store a token's 16-byte pieces
         const uint32_t tl = tmem_lane(tmem, warp);
         const bool live = (warp & 3) * 32 < dv;
@@ -478,28 +544,55 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           warp_arrive(&empty[c % kStages]);
           tc_fence_after();
           const float* E = decay[c % kRing].E + tok0;
-          const uint32_t ta = tl + 64 * (c & 1) + tok0;
-#pragma unroll 1
-          for (int tk = 0; tk < 32; tk += 8) {
-            float x[8], y[8];
-            tmem_ld8x2_wait(ta + kTm1 + tk, ta + kTm2 + tk, x, y);
-            Tout* at = reinterpret_cast<Tout*>(stage) + tk % kTok * 32 + lane;
+          const uint32_t ta = tl + tok0;
+          if constexpr (sizeof(Tout) == 2) {
+            // read and rounded first, so that the next chunk's products can start, then stored
+            uint32_t o[16];
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const float4 e = *reinterpret_cast<const float4*>(E + tk + j);
-              at[(j + 0) * 32] = from_f32<Tout>(fmaf(e.x, x[j], y[j]));
-              at[(j + 1) * 32] = from_f32<Tout>(fmaf(e.y, x[j + 1], y[j + 1]));
-              at[(j + 2) * 32] = from_f32<Tout>(fmaf(e.z, x[j + 2], y[j + 2]));
-              at[(j + 3) * 32] = from_f32<Tout>(fmaf(e.w, x[j + 3], y[j + 3]));
+            for (int i = 0; i < 4; ++i) {
+              float x[8], y[8];
+              tmem_ld8x2_wait(ta + kTm1 + 8 * i, ta + kTm2 + 8 * i, x, y);
+#pragma unroll
+              for (int j = 0; j < 8; j += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(E + 8 * i + j);
+                o[4 * i + j / 2] = pack_bf2(fmaf(e.x, x[j], y[j]), fmaf(e.y, x[j + 1], y[j + 1]));
+                o[4 * i + j / 2 + 1] = pack_bf2(fmaf(e.z, x[j + 2], y[j + 2]), fmaf(e.w, x[j + 3], y[j + 3]));
+              }
             }
-            if (tk == 24) {
-              tc_fence_before();
-              warp_arrive(&o_read[c & 1]);
-            }
-            if ((tk + 8) % kTok == 0) {
+            tc_fence_before();
+            warp_arrive(o_read);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // 16 tokens
+              uint16_t* at = reinterpret_cast<uint16_t*>(stage) + lane;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                at[(2 * j) * 32] = (uint16_t)o[8 * g + j];
+                at[(2 * j + 1) * 32] = (uint16_t)(o[8 * g + j] >> 16);
+              }
               __syncwarp();
-#pragma unroll 2
-              for (int i = 0; i < kTok * kLanes / 32; ++i) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (live && r0 < rows) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(stage + i * 512 + lane * 16);
+                dst += (32 / kLanes) * step;
+                r0 += 32 / kLanes;
+              }
+              __syncwarp();
+            }
+          } else {
+#pragma unroll 1
+            for (int tk = 0; tk < 32; tk += 8) {
+              float x[8], y[8];
+              tmem_ld8x2_wait(ta + kTm1 + tk, ta + kTm2 + tk, x, y);
+              float* at = reinterpret_cast<float*>(stage) + lane;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) at[j * 32] = fmaf(E[tk + j], x[j], y[j]);
+              if (tk == 24) {
+                tc_fence_before();
+                warp_arrive(o_read);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
                 if (live && r0 < rows) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(stage + i * 512 + lane * 16);
                 dst += (32 / kLanes) * step;
                 r0 += 32 / kLanes;
@@ -516,7 +609,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       if constexpr (MODE == 0) {
         const int i = (warp & 1) * 32 + lane;  // token, TMEM lane
         const uint32_t tl = tmem_lane(tmem, warp & 1);
-        const int col = warp == 25 ? 32 : 0;
+        const int col = warp == 1 ? 32 : 0;
         const float scale = p.scale;
         bool ok = true;
 #pragma unroll 1
@@ -547,60 +640,10 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           warp_arrive(&a_ready[c & 1]);
         }
       }
-    } else if (warp >= 22 && warp <= 30) {
-      // ======================== K~ = w k as three bf16 parts (8 bits each: their sum is exact)
-      const int group = key_warp(warp), vb = dv / 64;  // 16-byte pieces of a row: KB (vb) to a warp
-      bool ok = true;
-#pragma unroll 1
-      for (int c = 0; c < nc; ++c) {
-        uint8_t* st = sm + (c % kStages) * kStageBytes;
-        ok = warp_wait<GIVEUP>(&full[c % kStages], (uint32_t)((c / kStages) & 1), abort_flag);
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          // the products that read this half of the chunk before
-          if (ok && c > 0)
-            ok = hf == 0 ? warp_wait<GIVEUP>(kt_free, (uint32_t)((c - 1) & 1), abort_flag)
-                         : warp_wait<GIVEUP>(u_full, (uint32_t)((c - 1) & 1), abort_flag);
-          if (!ok) break;
-          const int r = 32 * hf + lane;
-          const float w = decay[c % kRing].W[r];
-          // a row whose weight is 0 is 0 whatever it holds (the next sequence's tokens, among others)
-          const uint32_t keep = w == 0.f ? 0u : 0xffffffffu;
-#pragma unroll 1
-          for (int i = 0; i < KB; ++i) {
-            const int blk = (group * KB + i) >> 3, j = (group * KB + i) & 7;
-            const uint4 kk = *reinterpret_cast<const uint4*>(st + kKey + blk * kPair + row_chunk(r, j));
-            const uint32_t in[4] = {kk.x, kk.y, kk.z, kk.w};
-            uint32_t p0[4], p1[4], p2[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t kw = in[e] & keep;
-              const float2 x = mul2(make_float2(w, w), make_float2(__uint_as_float(kw << 16), __uint_as_float(kw & 0xffff0000u)));
-              const uint32_t h0 = __float_as_uint(x.x), h1 = __float_as_uint(x.y);
-              const float2 y = sub2(x, make_float2(__uint_as_float(h0 & 0xffff0000u), __uint_as_float(h1 & 0xffff0000u)));
-              const uint32_t m0 = __float_as_uint(y.x), m1 = __float_as_uint(y.y);
-              const float2 z = sub2(y, make_float2(__uint_as_float(m0 & 0xffff0000u), __uint_as_float(m1 & 0xffff0000u)));
-              p0[e] = __byte_perm(h0, h1, 0x7632);
-              p1[e] = __byte_perm(m0, m1, 0x7632);
-              p2[e] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
-            }
-            uint8_t* dst = sm + kKt + blk * kBlk + row_chunk(r, j);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
-            *reinterpret_cast<uint4*>(dst + 2 * kBlk) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-            *reinterpret_cast<uint4*>(dst + 4 * kBlk) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-          }
-          // values past the sequence's end meet weights of 0, but may hold anything: clear them
-          if (r >= rows - c * kC) {
-            for (int i = 0; i < vb; ++i) {
-              const int blk = (group * vb + i) >> 3, j = (group * vb + i) & 7;
-              *reinterpret_cast<uint4*>(st + kV + blk * kBlk + r * 128 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
-          fence_proxy_async_smem();
-          warp_arrive(&kt_ready[hf]);
-        }
-        if (!ok) break;
-      }
+    } else if (warp >= kValueWarp && warp < kValueWarp + kValueWarps) {
+      // ======================== V~
+      make_values<MODE == 0 ? 32 : 16, KB, GIVEUP>(sm, decay, full, vt_ready, vt_free, u_full, abort_flag, tmem,
+                                               (warp - kValueWarp) >> 2, nc, rows, dv);
     }
   }
   tc_fence_before();

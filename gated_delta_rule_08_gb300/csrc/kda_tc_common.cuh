@@ -278,6 +278,12 @@ __device__ __forceinline__ void tmem_landed(float (&v)[16]) {
                :
                : "memory");
 }
+// 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // 8 consecutive columns of this thread's TMEM lane; valid on return.
 __device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, float (&v)[8]) {
   uint32_t r[8];
