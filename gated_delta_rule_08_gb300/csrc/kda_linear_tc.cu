@@ -454,8 +454,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const int s = c % kStages;
           const uint8_t* st = sm + s * kStageBytes;
           if constexpr (MODE == 0) {
-            ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
-            if (ok && c > 0) ok = warp_wait<GIVEUP>(&a_ready[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
+            ok = warp_spin<GIVEUP>(&full[s], (uint32_t)((c / kStages) & 1), abort_flag);
+            if (ok && c > 0) ok = warp_spin<GIVEUP>(&a_ready[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dq = smem_desc_sw128(smem_u32(st + kQ), 16, 1024), dk = smem_desc_sw128(smem_u32(st + kKey), 16, 1024);
@@ -466,11 +466,11 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
                 mma_bf16_ss_by(leader, tmem + kTmA, desc_add(dq, b * kPair + i * 32), desc_add(dk, b * kPair + i * 32), id_a, b + i > 0);
             mma_commit_by(leader, a_done);
           }
-          if (c > 0) ok = warp_wait<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
+          if (c > 0) ok = warp_spin<GIVEUP>(u_empty, (uint32_t)((c - 1) & 1), abort_flag);
           const uint64_t d_k = smem_desc_sw128(smem_u32(st + kKey), kPair, 1024);
 #pragma unroll 1
           for (int hf = 0; hf < 2; ++hf) {  // by halves of 32 tokens
-            ok = ok && warp_wait<GIVEUP>(&vt_ready[hf], (uint32_t)(c & 1), abort_flag);
+            ok = ok && warp_spin<GIVEUP>(&vt_ready[hf], (uint32_t)(c & 1), abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -496,20 +496,20 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
           const uint8_t* st = sm + (c % kStages) * kStageBytes;
           const uint64_t d_v = smem_desc_sw128(smem_u32(st + kV), kBlk, 1024), d_q = smem_desc_sw128(smem_u32(st + kQ), 16, 1024);
           const uint32_t buf = c & 1;
-          ok = warp_wait<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
-          if (ok && c > 0) ok = warp_wait<GIVEUP>(o_read, (uint32_t)((c - 1) & 1), abort_flag);
+          ok = warp_spin<GIVEUP>(&a_ready[buf], (uint32_t)((c / 2) & 1), abort_flag);
+          if (ok && c > 0) ok = warp_spin<GIVEUP>(o_read, (uint32_t)((c - 1) & 1), abort_flag);
           if (ok && c == nc - 1) {
             // rows past the sequence are cleared with V~; the state tells that the chunk before has passed there
-            ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
-                 warp_wait<GIVEUP>(&vt_ready[0], (uint32_t)(c & 1), abort_flag) &&
-                 warp_wait<GIVEUP>(&vt_ready[1], (uint32_t)(c & 1), abort_flag);
+            ok = warp_spin<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag) &&
+                 warp_spin<GIVEUP>(&vt_ready[0], (uint32_t)(c & 1), abort_flag) &&
+                 warp_spin<GIVEUP>(&vt_ready[1], (uint32_t)(c & 1), abort_flag);
           }
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
             mma_bf16_ss_by(leader, tmem + kTm2, desc_add(d_v, j * 2048), desc_add(d_a, buf * kBlk + j * 32), id_2, j > 0);
-          if (c < nc - 1) ok = warp_wait<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
+          if (c < nc - 1) ok = warp_spin<GIVEUP>(s_ready, (uint32_t)(c & 1), abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1

@@ -409,9 +409,9 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       bool ok = true;
       for (int it = 0; it < cnt && ok; ++it) {
         const int s = it % F::kStages, buf = it % F::kBufs;
-        ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
+        ok = warp_spin<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
         if (ok && it >= F::kBufs)
-          ok = warp_wait<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
+          ok = warp_spin<GIVEUP>(&acc_empty[buf], (uint32_t)((it / F::kBufs - 1) & 1), abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint8_t* st = sm + s * F::kStage;

@@ -174,12 +174,18 @@ __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) { return raw + ((
 // loop one by one, or one lane that polls for the others, stay apart afterwards, and the warp then runs the
 // work that follows once for each group.)
 constexpr uint32_t kPollNs = 1000000;
-template <bool kGiveUp>
+template <bool kGiveUp, bool kSpin = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if constexpr (kGiveUp) {
     *abort_flag = 1;
     return false;
   } else {
+    if constexpr (kSpin) {
+#pragma unroll 1
+      for (uint32_t i = 0; i < 512u; ++i)
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    }
+#pragma unroll 1
     for (uint32_t i = 0; i < 20000000u; ++i) {
       if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kPollNs))) return true;
       if ((i & 63u) == 63u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
@@ -187,6 +193,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     *abort_flag = 1;
     return false;
   }
+}
+// ... for the warps that issue the MMAs, which everything waits for: polls at first (a suspended warp comes back
+// some hundreds of clocks late), at the price of issue slots.
+template <bool kGiveUp>
+__device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return warp_wait<kGiveUp, true>(bar, parity, abort_flag);
 }
 
 // One arrival for a whole warp, after all its lanes' work (each has executed the fence that work needs).
