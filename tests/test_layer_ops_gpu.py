@@ -36,7 +36,8 @@ def check_norm(x, residual, weight, eps, got):
 
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("rows,D", [(1, 16), (1, 4096), (5, 128), (3, 144), (130, 64), (37, 256), (33, 496), (9, 1008), (7, 2000),
-                                    (4, 4112), (3, 8192), (2, 16384), (2, 16400), (1, 32768)])
+                                    (4, 4112), (3, 8192), (2, 16384), (2, 16400), (1, 32768), (2050, 2080), (2100, 6000),
+                                    (2048, 9008)])
 @pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
 def test_norm(rows, D, residual, dtype):
     r = gen(rows * 40000 + D)
