@@ -263,8 +263,12 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = p.H, dv = p.dv;
+  // The merge may be scheduled while the segments run, and the last pass while it runs.  Every CTA of a grid
+  // waits for the grid before it, so that none completes before the one it follows.
+  if (MODE == 1) griddep_launch_dependents();
   if (p.cu != nullptr && !offsets_ok(p.cu, p.B, p.T_tot)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
+    griddep_wait();
     return;
   }
   const int seg = blockIdx.x % p.nseg, chain = blockIdx.x / p.nseg;
@@ -274,7 +278,10 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int len = p.cu ? p.cu[b + 1] - t_begin : (int)p.T;
   const int nchunks = (int)(((int64_t)len + kC - 1) / kC);
   const int last_seg = nchunks > 0 ? (nchunks - 1) / p.seg_len : 0;
-  if (MODE == 0 ? seg > last_seg : seg >= last_seg) return;
+  if (MODE == 0 ? seg > last_seg : seg >= last_seg) {
+    griddep_wait();
+    return;
+  }
   const int c0 = seg * p.seg_len, nc = (nchunks < c0 + p.seg_len ? nchunks : c0 + p.seg_len) - c0;
   const int t0 = t_begin + c0 * kC;  // the segment's first token
   const int rows = len - c0 * kC;    // tokens from there to the sequence's end
@@ -315,7 +322,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int issued = 0;  // stages whose copies have been started (warp 14)
+  griddep_wait();  // the segments' states are read below
+  int issued = 0;  // stages whose copies have been started
 
   if (warp >= kStateWarp && warp < kStateWarp + kStateWarps) {
     // ======================== state
@@ -661,7 +669,10 @@ __global__ void __launch_bounds__(kMergeThreads)
 linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu, float* __restrict__ seg_state,
                     const float* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
                     int elems, int parts) {
-  if (cu != nullptr && !offsets_ok(cu, B, T_tot)) return;
+  griddep_launch_dependents();
+  const bool ok = cu == nullptr || offsets_ok(cu, B, T_tot);
+  griddep_wait();
+  if (!ok) return;
   const int bh = blockIdx.x / parts, b = bh / H;
   const int at = (blockIdx.x % parts * kMergeThreads + threadIdx.x) * 4;
   const int64_t len = cu ? (int64_t)cu[b + 1] - cu[b] : T;
@@ -730,6 +741,22 @@ cudaError_t allow_all() {
   });
 }
 
+// A launch that may start while the kernel before it in the stream drains (`early`); the kernel waits for it itself.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, uint32_t smem, cudaStream_t st, bool early, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 template <int DK, bool GIVEUP>
 cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaStream_t st) {
   const unsigned grid = (unsigned)((int64_t)a.B * a.H * p.nseg);
@@ -740,15 +767,14 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaS
     }
     const int elems = DK * a.dv, parts = elems / (4 * kMergeThreads);
     TraceScope ts("kda_linear_merge", st);
-    linear_merge_kernel<<<(unsigned)(a.B * a.H * parts), kMergeThreads, 0, st>>>(
-        a.h0, a.cu_seqlens, p.seg_state, p.seg_decay, a.B, a.T, a.T_tot, a.H, p.nseg, p.seg_len, elems, parts);
+    const cudaError_t e = launch_after(linear_merge_kernel, (unsigned)(a.B * a.H * parts), kMergeThreads, 0, st, true, a.h0,
+                                       a.cu_seqlens, p.seg_state, (const float*)p.seg_decay, a.B, a.T, a.T_tot, a.H, p.nseg,
+                                       p.seg_len, elems, parts);
+    if (e != cudaSuccess) return e;
   }
-  {
-    TraceScope ts("kda_linear_chunk", st);
-    if (a.out_bf16) linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
-    else linear_chunk_kernel<DK, 0, float, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
-  }
-  return cudaGetLastError();
+  TraceScope ts("kda_linear_chunk", st);
+  return launch_after(a.out_bf16 ? linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP> : linear_chunk_kernel<DK, 0, float, GIVEUP>, grid,
+                      kThreads, kSmem, st, p.nseg > 1, maps, p);
 }
 
 }  // namespace

@@ -429,3 +429,22 @@ def test_waits_that_run_out_are_reported_and_the_device_stays_usable(what, monke
     for _ in range(2):
         call()
         no_device_error()
+
+
+def test_segments_in_a_graph():
+    """A call that runs as several kernels which may overlap, captured and replayed back to back on changed inputs."""
+    lin = linear_inputs(41, (2600,), 2, 128, 128, BF, "token", True, True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = kda.kda_linear_chunk_fwd(lin["q"], lin["k"], lin["v"], lin["g"], h0=lin["h0"])
+        second = kda.kda_linear_chunk_fwd(lin["q"], lin["k"], lin["v"], lin["g"], h0=first[1])
+    for factor in (1.0, 0.5):
+        lin["v"].mul_(factor)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = kda.kda_linear_chunk_fwd(lin["q"], lin["k"], lin["v"], lin["g"], h0=lin["h0"])
+        then = kda.kda_linear_chunk_fwd(lin["q"], lin["k"], lin["v"], lin["g"], h0=want[1])
+        for a, b in zip((*first, *second), (*want, *then)):
+            assert torch.equal(a, b)
+    no_device_error()
