@@ -680,12 +680,24 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
   float4 S = h0 ? *reinterpret_cast<const float4*>(h0 + (int64_t)bh * elems + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   float* p = seg_state + (int64_t)bh * nseg * elems + at;
   const float* e = seg_decay + (int64_t)bh * nseg;
-  for (int i = 0; i < last; ++i, p += elems) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    *reinterpret_cast<float4*>(p) = S;
-    S = f4_fma(e[i], S, u);
+  constexpr int kAhead = 4;  // loads under way at a time
+  for (int i0 = 0; i0 < last; i0 += kAhead, p += (int64_t)kAhead * elems) {
+    float4 u[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const bool in = i0 + i < last;
+      u[i] = in ? *reinterpret_cast<const float4*>(p + (int64_t)i * elems) : make_float4(0.f, 0.f, 0.f, 0.f);
+      d[i] = in ? e[i0 + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i0 + i < last) {
+        *reinterpret_cast<float4*>(p + (int64_t)i * elems) = S;
+        S = f4_fma(d[i], S, u[i]);
+      }
   }
-  *reinterpret_cast<float4*>(p) = S;
+  *reinterpret_cast<float4*>(seg_state + ((int64_t)bh * nseg + last) * elems + at) = S;
 }
 
 // Segments: only where at least half of the device would be idle, of 8 chunks at least, and so long that all
