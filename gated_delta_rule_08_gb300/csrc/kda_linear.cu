@@ -4,9 +4,11 @@
 //   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
 // the KDA recurrence (section 2.2 Eq. 1) without the delta rule's erase and with a scalar decay.
 //
-// linear_recurrent_kernel: whole sequences of fp32 inputs, token by token (bf16: kda_linear_tc.cu).  Value columns are independent of
-// one another, so a CTA takes 16 of them for the whole sequence and keeps its dk x 16 slice of the
-// state in registers; a thread owns dk / 8 rows of one column.
+// linear_recurrent_kernel: whole sequences of fp32 inputs, token by token (bf16: kda_linear_tc.cu), so that fp32
+// inputs are multiplied as fp32.  Value columns are independent of one another, so a CTA takes 16 of them for the
+// whole sequence and keeps its dk x 16 slice of the state in registers; a thread owns dk / 8 rows of one column.
+// Bound by the chain of tokens: ~95 ns a token at dk = 64 and ~130 ns at 128 (1024 tokens of one sequence: 96.2 and
+// 134 us); with every SM busy by the instructions (8 x 1024 tokens, H = 32, d = 128: 1.29 ms).
 //
 // linear_step_kernel: one token per request on a pool of states, in place (section 13.9's pooled
 // layout).  It streams each state in and out once.
@@ -183,32 +185,33 @@ cudaError_t recurrent_typed(const LinearArgs& a, cudaStream_t st) {
 // ------------------------------------------------------------------------------ one token
 constexpr int kStepThreads = 256;
 
-// CTA = (request, head, one of SPLIT groups of value columns).  A thread owns four columns of
-// DK / NG consecutive rows, so a warp's state accesses are whole 128-bit pieces of a row; the slice
-// stays in registers between load and store.
-template <int DK, int DV, int SPLIT, typename Tin, typename Tout>
+// CTA = (request, head).  A thread owns four columns of DK / NG consecutive rows, so a warp's state accesses are
+// whole 128-bit pieces of a row; the state stays in registers between load and store.
+//
+// Bound by the states' bytes, read once and written once: 256 requests x 32 heads of 128 x 128 take 157.6 us,
+// 6.8 TB/s (the rate of a plain copy).  Few requests are bound by the latency of a load, a product and a store:
+// 32 states 2.9 us, 128 states 3.1 us.
+template <int DK, int DV, typename Tin, typename Tout>
 __global__ void __launch_bounds__(kStepThreads)
 linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v, int64_t q_stride,
                    int64_t k_stride, int64_t v_stride, const float* __restrict__ g, int g_per_token,
                    float* __restrict__ pool, const int32_t* __restrict__ slot_idx, Tout* __restrict__ out, int H,
                    int num_slots, float scale, unsigned int* __restrict__ err) {
-  constexpr int DVS = DV / SPLIT;           // columns of this CTA
-  constexpr int TPR = DVS / 4;              // threads per row
+  constexpr int TPR = DV / 4;               // threads per row
   constexpr int NG = kStepThreads / TPR;    // row groups
   constexpr int RPG = DK / NG;              // rows per thread
   static_assert(DK % NG == 0, "rows must split evenly");
   __shared__ __align__(16) float sk[DK], sq[DK];
   __shared__ __align__(16) float4 part[NG][TPR];
 
-  const int part_id = blockIdx.x % SPLIT, nh = blockIdx.x / SPLIT;
-  const int n = nh / H, h = nh - n * H;
+  const int nh = blockIdx.x, n = nh / H, h = nh - n * H;
   const int tid = threadIdx.x, cg = tid % TPR, rg = tid / TPR;
   const int slot = slot_idx[n];
   if (slot < 0 || slot >= num_slots) {
-    if (tid == 0 && h == 0 && part_id == 0) atomicOr(err, KDA_DEVERR_BAD_SLOT);
+    if (tid == 0 && h == 0) atomicOr(err, KDA_DEVERR_BAD_SLOT);
     return;
   }
-  float* S = pool + ((int64_t)slot * H + h) * (DK * DV) + part_id * DVS + 4 * cg;
+  float* S = pool + ((int64_t)slot * H + h) * (DK * DV) + 4 * cg;
   float4 s[RPG];
 #pragma unroll
   for (int i = 0; i < RPG; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(S + (rg * RPG + i) * DV));
@@ -220,7 +223,7 @@ linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const T
   }
   float4 x;
   {
-    const Tin* vp = v + n * v_stride + h * DV + part_id * DVS + 4 * cg;
+    const Tin* vp = v + n * v_stride + h * DV + 4 * cg;
     x = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
   }
   __syncthreads();
@@ -234,18 +237,18 @@ linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const T
   }
   part[rg][cg] = acc;
   __syncthreads();
-  if (tid < DVS) {
+  if (tid < DV) {
     float o = 0.f;
 #pragma unroll
     for (int i = 0; i < NG; ++i) o += reinterpret_cast<const float*>(part[i])[tid];
-    out[(int64_t)nh * DV + part_id * DVS + tid] = from_f32<Tout>(scale * o);
+    out[(int64_t)nh * DV + tid] = from_f32<Tout>(scale * o);
   }
 }
 
 template <int DK, int DV, typename Tin, typename Tout>
 cudaError_t step_sized(const LinearStepArgs& a, cudaStream_t st) {
   TraceScope ts("kda_linear_step", st);
-  linear_step_kernel<DK, DV, 1, Tin, Tout><<<(unsigned)(a.N * a.H), kStepThreads, 0, st>>>(
+  linear_step_kernel<DK, DV, Tin, Tout><<<(unsigned)(a.N * a.H), kStepThreads, 0, st>>>(
       static_cast<const Tin*>(a.q), static_cast<const Tin*>(a.k), static_cast<const Tin*>(a.v), a.q_stride, a.k_stride,
       a.v_stride, a.g, a.g_per_token, a.state_pool, a.slot_idx, static_cast<Tout*>(a.out), a.H, a.num_slots, a.scale,
       a.err);

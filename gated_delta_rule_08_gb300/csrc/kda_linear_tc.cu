@@ -29,6 +29,12 @@
 // Few long sequences would leave most of the device idle, so they are cut into segments: MODE 1 runs
 // compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
 // folds them in order, and MODE 0 runs every segment from its state.
+//
+// Measured, bf16, H = 32, d = 128: 1 x 8192 tokens 128 us (segments 52, merge 8, last pass 78; of 272 MB, 2.1 TB/s),
+// 8 sequences of 512 to 8192 tokens 251 us (3.2 TB/s), where the longest's 128 chunks of 2 us follow one another.
+// Bound by the instructions and the shared-memory traffic of a chunk, not by HBM: 32 MMAs at one in 120-150 clocks,
+// four schedulers at half their issue rate, two state products whose operands change between TMEM, registers
+// and shared memory.
 #include "kda_internal.h"
 #include "kda_tc_common.cuh"
 #include "kda_tma.h"
@@ -700,20 +706,23 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
   *reinterpret_cast<float4*>(seg_state + ((int64_t)bh * nseg + last) * elems + at) = S;
 }
 
-// Segments: only where at least half of the device would be idle, of 8 chunks at least, and so long that all
-// chunks, with one short segment for each (sequence, head), make at most one CTA an SM (a second wave would cost
-// as much as the first).
-constexpr int kMinSplitChunks = 32, kMinSegChunks = 8;
+// Segments, of n chunks at least so long that all of them, with one short one for each (sequence, head), make at most
+// one CTA an SM (a second wave would cost as much as the first).  Measured, a pass over L chunks takes 2 L + 8 us and
+// the three launches of a cut one 3 n + 20 us, so a cut is taken where 3 n + 12 < 2 L.  Uncut against cut, us:
+//   1 x 640, H = 32: 28 / 32;  1 x 1024: 40 / 35;  1 x 2048: 69 / 48;  1 x 4096: 131 / 77;  2 x 4096: 132 / 165;
+//   1 x 4096, H = 8: 127 / 36.
+// Lengths given by offsets are on the device, so half of all tokens stands for the longest of several sequences.
+constexpr int kMinSegChunks = 4;
 void segments(int B, int64_t T, int64_t T_tot, bool has_cu, int H, int sms, int* nseg, int* seg_len) {
   const int64_t longest = (T + kC - 1) / kC;  // of a sequence, at most
-  const int64_t chains = (int64_t)B * H;
+  const int64_t chains = (int64_t)B * H, expected = has_cu && B > 1 ? longest / 2 : longest;
   *nseg = 1;
   *seg_len = longest > 0 ? (int)longest : 1;
-  if (chains * 2 > sms || longest < kMinSplitChunks) return;
+  if (chains >= sms) return;
   const int64_t chunks = has_cu ? (T_tot + kC - 1) / kC : B * longest;
   int64_t n = (chunks * H + sms - chains - 1) / (sms - chains);
   if (n < kMinSegChunks) n = kMinSegChunks;
-  if (n >= longest) return;
+  if (3 * n + 12 >= 2 * expected) return;
   *nseg = (int)((longest + n - 1) / n);
   *seg_len = (int)n;
 }

@@ -12,7 +12,7 @@
 // read once.  A piece is 8 values of fp32, 16 of bf16 (32 bytes each): neighbouring lanes hold one block of 128, and
 // longer pieces save shuffles (bf16, 8192 x 4096: 41.7 against 46.6 us with pieces of 8; fp32, 1237 x 2000: 4.5
 // against 3.8 us with pieces of 16).  Bound by HBM: 7 bytes per value for
-// bf16 with a residual.
+// bf16 with a residual (8192 x 4096: 41.6 us, 5.7 TB/s, 84 % of a plain copy's rate; one row of 4096: 2.4 us).
 #include <cuda_fp8.h>
 
 #include "kda_device.cuh"

@@ -200,6 +200,17 @@ def test_linear_chunk_long(H, T):
     no_device_error()
 
 
+@pytest.mark.parametrize("lengths", [(832,), (833,), (1000,), (1025,), (2000, 300, 0, 65), (64, 1500, 900)],
+                         ids=lambda n: ",".join(map(str, n)))
+@pytest.mark.parametrize("H", [2, 32])
+def test_linear_chunk_short_segments(lengths, H):
+    """Lengths around the shortest ones that are cut, and cut ones beside others that end in their first segment."""
+    ins = linear_inputs(H + sum(lengths), lengths, H, 128, 128, BF, "token", True, True)
+    out, hT = kda.kda_linear_chunk_fwd(ins["q"], ins["k"], ins["v"], ins["g"], h0=ins["h0"], cu_seqlens=ins["cu"], scale=0.1)
+    check_linear(ins, lengths, out, hT, 0.1)
+    no_device_error()
+
+
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
 def test_linear_chunk_decay_extremes(dtype):
     """No decay at all, decays that empty the state in a token (-inf, the type's lowest value, -200), and a
