@@ -54,6 +54,23 @@ __device__ __forceinline__ float2 split2(uint64_t v) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// four fp32 at the same shared-memory offset of CTA `rank` of the cluster
+__device__ __forceinline__ float4 load_peer(const float* p, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 struct Maps {
   CUtensorMap a, b;
 };
@@ -81,7 +98,8 @@ constexpr uint32_t kTallBar = kTallSb + 2 * kGroup * 2 * 4;
 constexpr uint32_t kTallSmem = kTallBar + 256 + 1024;
 static_assert(kTallSmem <= 232448, "shared memory of a CTA");
 
-template <typename Tout, bool GIVEUP>
+// PAIR: two CTAs of a cluster share a tile, each with half of the K blocks (so few tiles that every pair is resident).
+template <typename Tout, bool PAIR, bool GIVEUP>
 __global__ void __launch_bounds__(kTallThreads, 1)
 matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
                 Tout* __restrict__ out, int M, int N, int nkb, int tiles_m, int tiles, unsigned int* __restrict__ err) {
@@ -98,6 +116,9 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   float* s_sa = reinterpret_cast<float*>(sm + kTallSa);
   float* s_sb = reinterpret_cast<float*>(sm + kTallSb);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int tile0 = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, step = PAIR ? tiles : (int)gridDim.x;
+  const int kb0 = PAIR && rank == 1 ? nkb / 2 : 0, kb1 = PAIR && rank == 0 ? nkb / 2 : nkb;  // this CTA's blocks
 
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
@@ -128,9 +149,9 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kTallCopyWarp && lane == 0) {
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
         const int m0 = tile % tiles_m * kTallM, n0 = tile / tiles_m * kTallN;
-        for (int kb = 0; kb < nkb && ok; ++kb, ++issued) {
+        for (int kb = kb0; kb < kb1 && ok; ++kb, ++issued) {
           const int s = (int)(issued % kTallStages);
           if (issued >= kTallStages) {
             const uint32_t ph = (uint32_t)((issued / kTallStages - 1) & 1);
@@ -149,8 +170,8 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       const int half = (warp - kTallMmaWarp) >> 1, buf = warp & 1;
       int64_t it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
+        for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if ((it & 1) != buf) continue;
           const int s = (int)(it % kTallStages);
           ok = warp_wait<GIVEUP>(&full[s], (uint32_t)((it / kTallStages) & 1), abort_flag);
@@ -166,15 +187,15 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
     } else if (warp == kTallScaleWarp) {
       int64_t grp = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < tiles && ok; tile += step) {
         // rows and blocks past the edges take another's scale; their products are zero
         const int m0 = tile % tiles_m * kTallM, nb0 = tile / tiles_m * (kTallN / 128), nb = (N + 127) / 128;
-        for (int k0 = 0; k0 < nkb; k0 += kGroup, ++grp) {
+        for (int k0 = kb0; k0 < kb1; k0 += kGroup, ++grp) {
           const int slot = (int)(grp & 1), kb = k0 + (lane & 7);
           if (grp >= 2) ok = warp_wait<GIVEUP>(&sc_empty[slot], (uint32_t)((grp / 2 - 1) & 1), abort_flag);
           if (!ok) break;
           float* d = s_sa + slot * kGroup * kScaleLd + (lane & 7) * kScaleLd;
-          if (kb < nkb) {
+          if (kb < kb1) {
 #pragma unroll 8
             for (int r = lane >> 3; r < kTallM; r += 4) {
               const int m = m0 + r;
@@ -189,6 +210,11 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         }
       }
     }
+    if constexpr (PAIR) {  // the joins of the promoting warps
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -197,7 +223,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
     uint64_t* my_empty = acc_empty + 2 * half;
     int64_t it = 0, grp = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int tile = tile0; tile < tiles && ok; tile += step) {
       const int m = tile % tiles_m * kTallM + row, n0 = tile / tiles_m * kTallN + 128 * half;
       uint64_t acc[64];
 #pragma unroll
@@ -213,14 +239,15 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         return warp_wait<GIVEUP>(&my_done[i % kTallStages], (uint32_t)((i / kTallStages) & 1), abort_flag);
       };
       ok = wait_block(it);
-      if (!ok) break;
-      tc_fence_after();
-      tmem_ld32(tl + 256 * (uint32_t)(it & 1), v);
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32(tl + 256 * (uint32_t)(it & 1), v);
+      }
 #pragma unroll 1
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
+      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
         const uint32_t ta = tl + 256 * (uint32_t)(it & 1);
-        const bool more = kb + 1 < nkb;
-        const int slot = (int)(grp & 1), kg = kb % kGroup;
+        const bool more = kb + 1 < kb1;
+        const int slot = (int)(grp & 1), kg = (kb - kb0) % kGroup;
         if (kg == 0) {
           ok = warp_wait<GIVEUP>(&sc_full[slot], (uint32_t)((grp / 2) & 1), abort_flag);
           if (!ok) break;
@@ -251,6 +278,31 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
         }
         add(w, 3, s);
       }
+      if constexpr (PAIR) {
+        // CTA r finishes columns 64 r to 64 r + 63 of each half; the others' sums go to the peer by way of the
+        // stages.  All MMAs have read those once both halves' last accumulators are complete.
+        float* part = reinterpret_cast<float*>(sm) + 4 * tid;
+        ok = group_and(1, kPromoteWarps * 32, ok && !*abort_flag);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (ok && r != rank)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = split2(acc[32 * r + 2 * i]), y = split2(acc[32 * r + 2 * i + 1]);
+              *reinterpret_cast<float4*>(part + i * kPromoteWarps * 128) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        cluster_sync();
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (ok && r == rank)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 x = load_peer(part + i * kPromoteWarps * 128, (uint32_t)(rank ^ 1));
+              acc_fma2(acc[32 * r + 2 * i], 1.f, 1.f, x.x, x.y);
+              acc_fma2(acc[32 * r + 2 * i + 1], 1.f, 1.f, x.z, x.w);
+            }
+        cluster_sync();  // the peer's sums have been read
+      }
       if (!ok) break;
       // by 128 bytes of columns: to shared memory with the row's 16-byte pieces permuted, then out by rows
       constexpr int kCols = 128 / sizeof(Tout), kPiece = 16 / sizeof(Tout);
@@ -258,6 +310,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       const int m_warp = m - lane;
 #pragma unroll
       for (int c = 0; c < 128 / kCols; ++c) {
+        if (PAIR && c * kCols / 64 != rank) continue;
         const int nc = n0 + c * kCols;
         for (int h = 0; h < 2; ++h) {  // rows 0-15, then 16-31 of the warp
           if ((lane >> 4) == h) {
@@ -329,22 +382,6 @@ struct Flat {
   static_assert(kPart <= kScale && kStages >= kBufs, "an accumulator is read before its stage's next MMAs");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// four fp32 at the same shared-memory offset of CTA `rank` of the cluster
-__device__ __forceinline__ float4 load_peer(const float* p, uint32_t rank) {
-  uint32_t a;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
 constexpr int kMaxSplit = 8;
 
 template <int BN, typename Tout, bool GIVEUP>
@@ -553,14 +590,20 @@ cudaError_t allow_flat() {
   if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, float, true>, Flat<BN>::kSmem);
   return e;
 }
+template <typename Tout>
+cudaError_t allow_tall() {
+  cudaError_t e = allow_smem(matmul_fp8_tall<Tout, false, false>, kTallSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, false, true>, kTallSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, true, false>, kTallSmem);
+  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, true, true>, kTallSmem);
+  return e;
+}
 cudaError_t prepare_device(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const cudaError_t e = g_state.once.run(dev, [dev] {
-    cudaError_t e = allow_smem(matmul_fp8_tall<__nv_bfloat16, false>, kTallSmem);
-    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<float, false>, kTallSmem);
-    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<__nv_bfloat16, true>, kTallSmem);
-    if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<float, true>, kTallSmem);
+    cudaError_t e = allow_tall<__nv_bfloat16>();
+    if (e == cudaSuccess) e = allow_tall<float>();
     if (e == cudaSuccess) e = allow_flat<16>();
     if (e == cudaSuccess) e = allow_flat<32>();
     if (e == cudaSuccess) e = allow_flat<64>();
@@ -610,7 +653,7 @@ cudaError_t launch(const MatmulArgs& a, cudaStream_t st) {
   const int64_t tiles_m = (a.M + kTallM - 1) / kTallM, tiles = tiles_m * ((a.N + kTallN - 1) / kTallN);
   // Few rows, or so few tiles that most SMs would have none.  flat against tall: 64 x 12288 x 4096 15.4 against
   // 21.0 us; 256 x 4096 x 4096, 32 tiles of 152 SMs, 17.0 against 21.7; 128 x 12288 x 4096, 48 tiles, 23.1 against
-  // 21.2.  As narrow as the rows allow: 16 x 12288 x 4096 12.6 us with 16, 16.9 with 64; 32 rows 13.1 and 14.8.
+  // 21.2 (17.1 in pairs).  As narrow as the rows allow: 16 x 12288 x 4096 12.6 us with 16, 16.9 with 64; 32 rows 13.1 and 14.8.
   if (a.M <= 16) return launch_flat<16, Tout>(a, sms, st);
   if (a.M <= 32) return launch_flat<32, Tout>(a, sms, st);
   if (a.M <= 64 || tiles * 4 < sms) return launch_flat<64, Tout>(a, sms, st);
@@ -619,12 +662,26 @@ cudaError_t launch(const MatmulArgs& a, cudaStream_t st) {
   if (!tensor_map_2d(&maps.a, a.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.M, a.K, a.K, kTallM, kK) ||
       !tensor_map_2d(&maps.b, a.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.N, a.K, a.K, kTallN, kK))
     return cudaErrorInvalidValue;
+  const int nkb = (a.K + kK - 1) / kK;
+  // Two CTAs to a tile where every pair is resident and each has eight blocks: 128 x 12288 x 4096, 48 tiles, 17.1
+  // against 21.4 us; 512 x 4096 x 4096, 64 tiles, 18.2 against 21.4; four blocks, 512 x 4096 x 512, 15.2 against 12.8.
+  const bool pair = 2 * tiles <= sms && nkb >= 16;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(pair ? 2 * tiles : tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(kTallThreads);
+  cfg.dynamicSmemBytes = kTallSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 1 : 0;
   TraceScope ts("kda_matmul_fp8_tall", st);
-  auto* kernel = a.give_up ? matmul_fp8_tall<Tout, true> : matmul_fp8_tall<Tout, false>;
-  kernel<<<(unsigned)(tiles < sms ? tiles : sms), kTallThreads, kTallSmem, st>>>(
-      maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, (a.K + kK - 1) / kK, (int)tiles_m,
-      (int)tiles, a.err);
-  return cudaGetLastError();
+  auto* kernel = pair ? (a.give_up ? matmul_fp8_tall<Tout, true, true> : matmul_fp8_tall<Tout, true, false>)
+                      : (a.give_up ? matmul_fp8_tall<Tout, false, true> : matmul_fp8_tall<Tout, false, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, nkb,
+                            (int)tiles_m, (int)tiles, a.err);
 }
 
 }  // namespace

@@ -112,6 +112,15 @@ def test_matmul(M, N, K, out_dtype):
     no_device_error()
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 5001, 1040), (200, 4880, 2000), (300, 4208, 4096), (65, 12288, 2176), (1025, 1300, 2064)])
+@pytest.mark.parametrize("out_dtype", [BF, FP], ids=["bf16", "fp32"])
+def test_matmul_of_a_few_wide_tiles(M, N, K, out_dtype):
+    """Between a quarter and half as many tiles of 128 x 256 as the device has SMs: two CTAs to a tile."""
+    ins = matmul_inputs(M + N + K, M, N, K)
+    check_matmul(ins, kda.kda_matmul_fp8(*ins, out_dtype=out_dtype))
+    no_device_error()
+
+
 def test_matmul_extreme_values_and_scales():
     """e4m3's largest and smallest numbers, scales 40 powers of two apart, zero rows, and a NaN row that
     reaches its own row of the output only."""
@@ -440,6 +449,19 @@ def test_waits_that_run_out_are_reported_and_the_device_stays_usable(what, monke
     for _ in range(2):
         call()
         no_device_error()
+
+
+def test_waits_that_run_out_in_a_pair_of_ctas(monkeypatch):
+    """The same where two CTAs share a tile and join their sums, and the same bits from call to call."""
+    ins = matmul_inputs(33, 200, 4880, 2000)
+    monkeypatch.setenv("KDA_TEST_WAIT_TIMEOUT", "1")
+    kda.kda_matmul_fp8(*ins)
+    assert binding.kda_get_device_error() & binding.DEVERR_WAIT_TIMEOUT
+    monkeypatch.delenv("KDA_TEST_WAIT_TIMEOUT")
+    got = [kda.kda_matmul_fp8(*ins) for _ in range(3)]
+    check_matmul(ins, got[0])
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    no_device_error()
 
 
 def test_segments_in_a_graph():
