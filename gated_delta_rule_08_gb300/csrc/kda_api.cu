@@ -106,9 +106,10 @@ bool device_ready(unsigned int** err, bool* supported) {
   return true;
 }
 
-bool test_wait_timeout() {
+int test_wait_timeout() {
   const char* e = getenv("KDA_TEST_WAIT_TIMEOUT");
-  return e != nullptr && *e != '\0' && strcmp(e, "0") != 0;
+  if (e == nullptr || *e == '\0' || strcmp(e, "0") == 0) return 0;
+  return strcmp(e, "stall") == 0 ? 2 : 1;
 }
 
 bool debug_checks() {
@@ -183,7 +184,7 @@ kda_status chunk_fwd_common(const void* q, const void* k, const void* v, const f
   a.epi.eps = epi ? epi->eps : 0.f;
   a.workspace = workspace; a.workspace_bytes = workspace_bytes; a.err = err;
   a.ckpt = states; a.ckpt_chunks = states ? ckpt_chunks : 0;
-  a.give_up = test_wait_timeout();
+  a.give_up = test_wait_timeout() != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (debug_checks() &&
       launch_checks(g, T_tot * H * dk, beta, T_tot * H, nullptr, 0, 0, err, s) != cudaSuccess)
@@ -237,7 +238,7 @@ KDA_API kda_status kda_chunk_fwd_segment_map(const void* k, const void* v, const
   a.B = 1; a.T = T; a.T_tot = T; a.H = H; a.dk = dk; a.dv = dv;
   a.bf16 = true; a.out_bf16 = true;
   a.workspace = workspace; a.workspace_bytes = workspace_bytes; a.err = err;
-  a.give_up = test_wait_timeout();
+  a.give_up = test_wait_timeout() != 0;
   a.seg_P = P; a.seg_b = b;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (debug_checks() && launch_checks(g, T * H * dk, beta, T * H, nullptr, 0, 0, err, s) != cudaSuccess)

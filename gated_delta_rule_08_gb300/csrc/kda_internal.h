@@ -31,12 +31,14 @@ struct DeviceOnce {
 };
 
 // The tensor-core kernels' bounded waits on work of their own CTA (mbarrier phases of copies, MMAs
-// and hand-overs between warps) give up after ~2e7 polls.  With the environment variable
+// and hand-overs between warps) give up after about a second.  With the environment variable
 // KDA_TEST_WAIT_TIMEOUT set (any value but "" or "0"; read at every call) the launches use kernel
-// variants whose waits give up at once, so that a test can make them run out on purpose and check
+// variants whose waits give up at once (1), so that a test can make them run out on purpose and check
 // that the kernels report KDA_DEVERR_WAIT_TIMEOUT and leave the device usable.  Waits for a CTA's own
-// copies and MMAs to drain before it exits keep their bound in both variants.
-bool test_wait_timeout();
+// copies and MMAs to drain before it exits keep their bound in both variants.  With the value "stall" (2)
+// kda_matmul_fp8 and kda_linear_chunk_fwd launch variants with the ordinary waits whose first CTA starts no
+// MMA: its waits run out by themselves, and the other CTAs' do not.
+int test_wait_timeout();
 
 // KDA_DEBUG_CHECKS (environment variable, read at every call; any value but "" or "0" enables it):
 // before the hot-path kernels, a check kernel tests the documented preconditions on the device
@@ -195,7 +197,7 @@ struct LinearArgs {
   bool bf16, out_bf16;
   void* workspace;
   unsigned int* err;
-  bool give_up;
+  int waits;  // test_wait_timeout()
 };
 cudaError_t linear_recurrent_launch(const LinearArgs& a, cudaStream_t stream);  // fp32 inputs (kda_linear.cu)
 cudaError_t linear_tc_launch(const LinearArgs& a, cudaStream_t stream);         // bf16 inputs (kda_linear_tc.cu)
@@ -244,7 +246,7 @@ struct MatmulArgs {
   int N, K;
   bool out_bf16;
   unsigned int* err;
-  bool give_up;
+  int waits;  // test_wait_timeout()
 };
 cudaError_t matmul_fp8_launch(const MatmulArgs& a, cudaStream_t stream);
 

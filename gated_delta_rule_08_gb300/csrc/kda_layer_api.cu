@@ -65,7 +65,7 @@ KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void
   a.g = g; a.g_per_token = g_per_token != 0; a.h0 = h0; a.cu_seqlens = cu_seqlens; a.out = out; a.hT = hT;
   a.B = B; a.T = T; a.T_tot = T_tot; a.H = H; a.dk = dk; a.dv = dv; a.scale = scale;
   a.bf16 = dtype == KDA_DTYPE_BF16; a.out_bf16 = out_dtype == KDA_DTYPE_BF16;
-  a.workspace = workspace; a.err = err; a.give_up = test_wait_timeout();
+  a.workspace = workspace; a.err = err; a.waits = test_wait_timeout();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return done(a.bf16 ? linear_tc_launch(a, s) : linear_recurrent_launch(a, s));
 }
@@ -133,6 +133,6 @@ KDA_API kda_status kda_matmul_fp8(const void* a, const float* a_scale, const voi
   MatmulArgs m{};
   m.a = static_cast<const uint8_t*>(a); m.a_scale = a_scale; m.b = static_cast<const uint8_t*>(b); m.b_scale = b_scale;
   m.out = out; m.M = M; m.N = N; m.K = K; m.out_bf16 = out_dtype == KDA_DTYPE_BF16; m.err = err;
-  m.give_up = test_wait_timeout();
+  m.waits = test_wait_timeout();
   return done(matmul_fp8_launch(m, static_cast<cudaStream_t>(stream)));
 }

@@ -243,11 +243,12 @@ __device__ __forceinline__ void make_values(uint8_t* sm, const Decay* decay, uin
 }
 
 // MODE 0: states and outputs.  MODE 1: a segment's contribution to the state after it, and its decay.
-template <int DK, int MODE, typename Tout, bool GIVEUP>
+template <int DK, int MODE, typename Tout, int WAITS>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr int KB = DK / 64;   // 64-channel blocks of q and k
   constexpr int KC = DK / 2;    // state columns of a thread
+  constexpr bool GIVEUP = WAITS == kWaitsGiveUp;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBar);  // [stages] tiles landed and decays written
@@ -463,8 +464,9 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         const bool leader = lane == 0;
         constexpr uint32_t id_a = idesc_bf16_f32(128, kC, false, false), id_u = idesc_bf16_f32(128, DK, false, true);
         bool ok = true;
+        const int n = WAITS == kFirstCtaStalls && blockIdx.x == 0 ? 0 : nc;
 #pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < n; ++c) {
           const int s = c % kStages;
           const uint8_t* st = sm + s * kStageBytes;
           if constexpr (MODE == 0) {
@@ -733,11 +735,11 @@ struct DeviceState {
 };
 DeviceState g_state;
 
-template <int DK, bool GIVEUP>
+template <int DK, int WAITS>
 cudaError_t allow() {
-  cudaError_t e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, float, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 1, float, GIVEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, __nv_bfloat16, WAITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 0, float, WAITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_chunk_kernel<DK, 1, float, WAITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   return e;
 }
 cudaError_t device_sms(int* sms) {
@@ -754,10 +756,12 @@ cudaError_t allow_all() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   return once.run(dev, [] {
-    cudaError_t e = allow<64, false>();
-    if (e == cudaSuccess) e = allow<128, false>();
-    if (e == cudaSuccess) e = allow<64, true>();
-    if (e == cudaSuccess) e = allow<128, true>();
+    cudaError_t e = allow<64, kWaits>();
+    if (e == cudaSuccess) e = allow<128, kWaits>();
+    if (e == cudaSuccess) e = allow<64, kWaitsGiveUp>();
+    if (e == cudaSuccess) e = allow<128, kWaitsGiveUp>();
+    if (e == cudaSuccess) e = allow<64, kFirstCtaStalls>();
+    if (e == cudaSuccess) e = allow<128, kFirstCtaStalls>();
     return e;
   });
 }
@@ -778,13 +782,13 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, uint3
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-template <int DK, bool GIVEUP>
+template <int DK, int WAITS>
 cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaStream_t st) {
   const unsigned grid = (unsigned)((int64_t)a.B * a.H * p.nseg);
   if (p.nseg > 1) {
     {
       TraceScope ts("kda_linear_segments", st);
-      linear_chunk_kernel<DK, 1, float, GIVEUP><<<grid, kThreads, kSmem, st>>>(maps, p);
+      linear_chunk_kernel<DK, 1, float, WAITS><<<grid, kThreads, kSmem, st>>>(maps, p);
     }
     const int elems = DK * a.dv, parts = elems / (4 * kMergeThreads);
     TraceScope ts("kda_linear_merge", st);
@@ -794,8 +798,10 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaS
     if (e != cudaSuccess) return e;
   }
   TraceScope ts("kda_linear_chunk", st);
-  return launch_after(a.out_bf16 ? linear_chunk_kernel<DK, 0, __nv_bfloat16, GIVEUP> : linear_chunk_kernel<DK, 0, float, GIVEUP>, grid,
-                      kThreads, kSmem, st, p.nseg > 1, maps, p);
+  auto* kernel = a.out_bf16 ? linear_chunk_kernel<DK, 0, __nv_bfloat16, WAITS> : linear_chunk_kernel<DK, 0, float, WAITS>;
+  if (WAITS == kFirstCtaStalls && p.nseg > 1)  // a segment's contribution has stalled: the last pass does not
+    kernel = a.out_bf16 ? linear_chunk_kernel<DK, 0, __nv_bfloat16, kWaits> : linear_chunk_kernel<DK, 0, float, kWaits>;
+  return launch_after(kernel, grid, kThreads, kSmem, st, p.nseg > 1, maps, p);
 }
 
 }  // namespace
@@ -830,8 +836,10 @@ cudaError_t linear_tc_launch(const LinearArgs& a, cudaStream_t st) {
        !tensor_map_2d(&maps.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dk, a.k_stride * 2, kC, 64) ||
        !tensor_map_2d(&maps.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dv, a.v_stride * 2, kC, 64)))
     return cudaErrorInvalidValue;
-  if (a.dk == 64) return a.give_up ? launch<64, true>(a, maps, p, st) : launch<64, false>(a, maps, p, st);
-  return a.give_up ? launch<128, true>(a, maps, p, st) : launch<128, false>(a, maps, p, st);
+  auto* run = a.dk == 64 ? launch<64, kWaits> : launch<128, kWaits>;
+  if (a.waits == kWaitsGiveUp) run = a.dk == 64 ? launch<64, kWaitsGiveUp> : launch<128, kWaitsGiveUp>;
+  if (a.waits == kFirstCtaStalls) run = a.dk == 64 ? launch<64, kFirstCtaStalls> : launch<128, kFirstCtaStalls>;
+  return run(a, maps, p, st);
 }
 
 }  // namespace kda

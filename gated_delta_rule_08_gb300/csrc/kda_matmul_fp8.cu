@@ -99,10 +99,11 @@ constexpr uint32_t kTallSmem = kTallBar + 256 + 1024;
 static_assert(kTallSmem <= 232448, "shared memory of a CTA");
 
 // PAIR: two CTAs of a cluster share a tile, each with half of the K blocks (so few tiles that every pair is resident).
-template <typename Tout, bool PAIR, bool GIVEUP>
+template <typename Tout, bool PAIR, int WAITS>
 __global__ void __launch_bounds__(kTallThreads, 1)
 matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
                 Tout* __restrict__ out, int M, int N, int nkb, int tiles_m, int tiles, unsigned int* __restrict__ err) {
+  constexpr bool GIVEUP = WAITS == kWaitsGiveUp;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kTallBar);  // [stages] tiles landed
@@ -169,7 +170,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
       const bool leader = lane == 0;
       const int half = (warp - kTallMmaWarp) >> 1, buf = warp & 1;
       int64_t it = 0;
-      bool ok = true;
+      bool ok = !(WAITS == kFirstCtaStalls && blockIdx.x == 0);
       for (int tile = tile0; tile < tiles && ok; tile += step) {
         for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if ((it & 1) != buf) continue;
@@ -384,11 +385,12 @@ struct Flat {
 
 constexpr int kMaxSplit = 8;
 
-template <int BN, typename Tout, bool GIVEUP>
+template <int BN, typename Tout, int WAITS>
 __global__ void __launch_bounds__(kFlatThreads)
 matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_scale, const float* __restrict__ b_scale,
                 Tout* __restrict__ out, int M, int N, int nkb, int split, unsigned int* __restrict__ err) {
   using F = Flat<BN>;
+  constexpr bool GIVEUP = WAITS == kWaitsGiveUp;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + F::kBar);  // [stages] tiles landed
@@ -447,7 +449,7 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   } else if (warp == kFlatMmaWarp) {
     {
       const bool leader = lane == 0;
-      bool ok = true;
+      bool ok = !(WAITS == kFirstCtaStalls && blockIdx.x == 0 && blockIdx.y == 0);
       for (int it = 0; it < cnt && ok; ++it) {
         const int s = it % F::kStages, buf = it % F::kBufs;
         ok = warp_spin<GIVEUP>(&full[s], (uint32_t)((it / F::kStages) & 1), abort_flag);
@@ -578,24 +580,37 @@ struct DeviceState {
 };
 DeviceState g_state;
 
+// The kernels' variants, indexed by test_wait_timeout().
+template <int BN, typename Tout>
+auto* flat_kernel(int waits) {
+  return waits == kWaits ? matmul_fp8_flat<BN, Tout, kWaits>
+                         : (waits == kWaitsGiveUp ? matmul_fp8_flat<BN, Tout, kWaitsGiveUp> : matmul_fp8_flat<BN, Tout, kFirstCtaStalls>);
+}
+template <typename Tout, bool PAIR>
+auto* tall_kernel(int waits) {
+  return waits == kWaits ? matmul_fp8_tall<Tout, PAIR, kWaits>
+                         : (waits == kWaitsGiveUp ? matmul_fp8_tall<Tout, PAIR, kWaitsGiveUp> : matmul_fp8_tall<Tout, PAIR, kFirstCtaStalls>);
+}
 template <typename Kernel>
 cudaError_t allow_smem(Kernel* k, uint32_t bytes) {
   return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 template <int BN>
 cudaError_t allow_flat() {
-  cudaError_t e = allow_smem(matmul_fp8_flat<BN, __nv_bfloat16, false>, Flat<BN>::kSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, float, false>, Flat<BN>::kSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, __nv_bfloat16, true>, Flat<BN>::kSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_flat<BN, float, true>, Flat<BN>::kSmem);
+  cudaError_t e = cudaSuccess;
+  for (int w = kWaits; w <= kFirstCtaStalls; ++w) {
+    if (e == cudaSuccess) e = allow_smem(flat_kernel<BN, __nv_bfloat16>(w), Flat<BN>::kSmem);
+    if (e == cudaSuccess) e = allow_smem(flat_kernel<BN, float>(w), Flat<BN>::kSmem);
+  }
   return e;
 }
 template <typename Tout>
 cudaError_t allow_tall() {
-  cudaError_t e = allow_smem(matmul_fp8_tall<Tout, false, false>, kTallSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, false, true>, kTallSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, true, false>, kTallSmem);
-  if (e == cudaSuccess) e = allow_smem(matmul_fp8_tall<Tout, true, true>, kTallSmem);
+  cudaError_t e = cudaSuccess;
+  for (int w = kWaits; w <= kFirstCtaStalls; ++w) {
+    if (e == cudaSuccess) e = allow_smem(tall_kernel<Tout, false>(w), kTallSmem);
+    if (e == cudaSuccess) e = allow_smem(tall_kernel<Tout, true>(w), kTallSmem);
+  }
   return e;
 }
 cudaError_t prepare_device(int* sms) {
@@ -640,8 +655,7 @@ cudaError_t launch_flat(const MatmulArgs& a, int sms, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
   TraceScope ts("kda_matmul_fp8_flat", st);
-  auto* kernel = a.give_up ? matmul_fp8_flat<BN, Tout, true> : matmul_fp8_flat<BN, Tout, false>;
-  return cudaLaunchKernelEx(&cfg, kernel, maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, nkb,
+  return cudaLaunchKernelEx(&cfg, flat_kernel<BN, Tout>(a.waits), maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, nkb,
                             (int)split, a.err);
 }
 
@@ -678,8 +692,7 @@ cudaError_t launch(const MatmulArgs& a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = pair ? 1 : 0;
   TraceScope ts("kda_matmul_fp8_tall", st);
-  auto* kernel = pair ? (a.give_up ? matmul_fp8_tall<Tout, true, true> : matmul_fp8_tall<Tout, true, false>)
-                      : (a.give_up ? matmul_fp8_tall<Tout, false, true> : matmul_fp8_tall<Tout, false, false>);
+  auto* kernel = pair ? tall_kernel<Tout, true>(a.waits) : tall_kernel<Tout, false>(a.waits);
   return cudaLaunchKernelEx(&cfg, kernel, maps, a.a_scale, a.b_scale, static_cast<Tout*>(a.out), (int)a.M, a.N, nkb,
                             (int)tiles_m, (int)tiles, a.err);
 }

@@ -115,7 +115,7 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
 // Bounded mbarrier wait that also gives up once another role has raised the CTA's abort flag;
 // a wait that runs out raises the flag itself.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                              uint32_t max_spins = 20000000u) {
+                                              uint32_t max_spins = kWaitTries) {
   for (uint32_t i = 0; i < max_spins; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63u) == 63u && *abort_flag) return false;
@@ -144,15 +144,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// try_wait that may sleep for up to `ns` nanoseconds.
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
+// What a kernel's waits do: the product's; the variant whose waits give up at once; and the one whose first CTA
+// starts no MMA, so that its waits run out by themselves while the other CTAs go on (both for tests).
+enum Waits : int { kWaits = 0, kWaitsGiveUp = 1, kFirstCtaStalls = 2 };
+
+// Where other warps of a CTA are at a cluster barrier, a try_wait returns at once instead of blocking.  The waits
+// below, which clusters use, therefore keep late tries at least 4 us apart: half a second to a second in all.  (In
+// wait_or_abort the pause costs the KDA prefill 337 -> 348 us without being reached.)
+constexpr uint32_t kPausedTries = 130000u, kQuickTries = 4096u;
+__device__ __forceinline__ void pause_after(uint32_t tries) {
+  if (tries >= kQuickTries) __nanosleep(4000);
 }
 // wait_or_abort_t for hand-overs that take less than a microsecond: polls first (a poll takes 15 clocks),
 // because a thread that try_wait has suspended comes back some hundreds of clocks late.
@@ -163,8 +164,14 @@ __device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, vo
       if (mbar_test_wait(bar, parity)) return true;
       if ((i & 63) == 63 && *abort_flag) return false;
     }
+    for (uint32_t i = 0; i < kPausedTries; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      pause_after(i);
+    }
   }
-  return wait_or_abort_t<kGiveUp>(bar, parity, abort_flag);
+  *abort_flag = 1;
+  return false;
 }
 // The start of dynamic shared memory, rounded up to the swizzle's 1024 bytes, as a pointer that the compiler
 // still knows to be shared memory.
@@ -173,7 +180,6 @@ __device__ __forceinline__ uint8_t* aligned_smem(uint8_t* raw) { return raw + ((
 // The same for a whole warp, which stays together: every branch is on a vote.  (Lanes that leave a polling
 // loop one by one, or one lane that polls for the others, stay apart afterwards, and the warp then runs the
 // work that follows once for each group.)
-constexpr uint32_t kPollNs = 1000000;
 template <bool kGiveUp, bool kSpin = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if constexpr (kGiveUp) {
@@ -186,9 +192,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
         if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     }
 #pragma unroll 1
-    for (uint32_t i = 0; i < 20000000u; ++i) {
-      if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kPollNs))) return true;
-      if ((i & 63u) == 63u && __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    for (uint32_t i = 0; i < kPausedTries; ++i) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+      pause_after(i);
     }
     *abort_flag = 1;
     return false;

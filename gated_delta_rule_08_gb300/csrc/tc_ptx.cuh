@@ -37,9 +37,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait: returns false if the phase did not complete within ~max_spins tries
-// (each try_wait may itself block for a hardware-defined time slice).
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t max_spins = 20000000u) {
+// Bounded wait: returns false if the phase did not complete within max_spins tries.  A try on a phase that does not
+// complete blocks for 4.0 us (measured, whatever its suspend-time hint), so the default is a second.  A count,
+// not a clock: time in which the device runs another context does not use it up.
+constexpr uint32_t kWaitTries = 250000u;
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t max_spins = kWaitTries) {
   for (uint32_t i = 0; i < max_spins; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;

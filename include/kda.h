@@ -44,9 +44,11 @@
  *     beta outside [0, 1], or (decode) two requests name the same slot.  The check reads every
  *     g and beta once (decode: O(N^2) slot comparisons); it is off by default.
  *   - Testing: with the environment variable KDA_TEST_WAIT_TIMEOUT set (any value but "" or "0";
- *     read at every call) the prefill, kda_matmul_fp8 and kda_linear_chunk_fwd launch kernel variants whose bounded waits on work of
- *     their own CTA give up at once, so that a test can make them run out and see
- *     KDA_DEVERR_WAIT_TIMEOUT reported with the device left usable.  Not for production use.
+ *     read at every call) the prefill, kda_matmul_fp8 and kda_linear_chunk_fwd launch kernel variants
+ *     whose bounded waits on work of their own CTA give up at once, so that a test can make them run
+ *     out and see KDA_DEVERR_WAIT_TIMEOUT reported with the device left usable.  With the value
+ *     "stall" kda_matmul_fp8 and kda_linear_chunk_fwd launch variants whose first CTA starts no work,
+ *     so that its waits run out at their limit, about a second.  Not for production use.
  */
 #ifndef KDA_H_
 #define KDA_H_

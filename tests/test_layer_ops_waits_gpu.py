@@ -1,0 +1,63 @@
+"""Waits of the serving operators that reach their limit: KDA_TEST_WAIT_TIMEOUT=stall launches variants with the
+ordinary waits whose first CTA starts no MMA.  Nothing here traps or hangs: every wait is counted, and the time a
+call may take is part of the test."""
+import time
+
+import pytest
+import torch
+
+import gated_delta_rule_08_gb300 as kda
+from gated_delta_rule_08_gb300 import binding
+from layer_util import gen, linear_inputs, randn
+
+pytestmark = pytest.mark.gpu
+BF, FP8 = torch.bfloat16, torch.float8_e4m3fn
+
+#: rows, columns, depth.  "few rows": one CTA a tile; "cluster": K over eight CTAs; "pair": two CTAs a tile
+PRODUCTS = {"many rows": (1280, 2304, 640), "few rows": (5, 300, 256), "cluster": (5, 300, 4096), "pair": (200, 4880, 2000)}
+SEQUENCES = {"one pass": (300, 70), "segments": (2500,)}
+
+
+def product_inputs(M, N, K):
+    r = gen(M + N + K)
+    kb, nb = -(-K // 128), -(-N // 128)
+    a, b = ((80 * randn(r, n, K)).clamp(-448, 448).to(FP8) for n in (M, N))
+    return a, torch.exp(randn(r, M, kb)) / 80, b, torch.exp(randn(r, nb, kb)) / 80
+
+
+def stalled(call, monkeypatch):
+    """The result of a call whose first CTA stalls; a limit is a second, and a call has few of them in a row."""
+    torch.cuda.synchronize()
+    monkeypatch.setenv("KDA_TEST_WAIT_TIMEOUT", "stall")
+    start = time.monotonic()
+    got = call()
+    torch.cuda.synchronize()
+    took = time.monotonic() - start
+    monkeypatch.delenv("KDA_TEST_WAIT_TIMEOUT")
+    assert binding.kda_get_device_error() == binding.DEVERR_WAIT_TIMEOUT
+    assert took < 10, took
+    return got
+
+
+@pytest.mark.parametrize("what", PRODUCTS)
+def test_product_reports_a_wait_that_runs_out_within_seconds(what, monkeypatch):
+    ins = product_inputs(*PRODUCTS[what])
+    want = kda.kda_matmul_fp8(*ins)
+    stalled(lambda: kda.kda_matmul_fp8(*ins), monkeypatch)
+    for _ in range(2):
+        assert torch.equal(kda.kda_matmul_fp8(*ins), want)
+    assert binding.kda_get_device_error() == 0
+
+
+@pytest.mark.parametrize("what", SEQUENCES)
+def test_sequences_report_a_wait_that_runs_out_within_seconds(what, monkeypatch):
+    ins = linear_inputs(32, SEQUENCES[what], 2, 128, 128, BF, "token", True, False)
+
+    def call():
+        return kda.kda_linear_chunk_fwd(ins["q"], ins["k"], ins["v"], ins["g"], h0=ins["h0"], cu_seqlens=ins["cu"])
+
+    want = call()
+    stalled(call, monkeypatch)
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    assert binding.kda_get_device_error() == 0
