@@ -788,7 +788,8 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaS
   if (p.nseg > 1) {
     {
       TraceScope ts("kda_linear_segments", st);
-      linear_chunk_kernel<DK, 1, float, WAITS><<<grid, kThreads, kSmem, st>>>(maps, p);
+      const cudaError_t e = launch_after(linear_chunk_kernel<DK, 1, float, WAITS>, grid, kThreads, kSmem, st, false, maps, p);
+      if (e != cudaSuccess) return e;
     }
     const int elems = DK * a.dv, parts = elems / (4 * kMergeThreads);
     TraceScope ts("kda_linear_merge", st);
