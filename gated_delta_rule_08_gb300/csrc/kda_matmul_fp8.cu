@@ -71,6 +71,15 @@ __device__ __forceinline__ float4 load_peer(const float* p, uint32_t rank) {
   return v;
 }
 
+// the word at the same shared-memory offset of CTA `rank` of the cluster
+__device__ __forceinline__ int load_peer(const volatile int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(const_cast<const int*>(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 struct Maps {
   CUtensorMap a, b;
 };
@@ -293,6 +302,8 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
               *reinterpret_cast<float4*>(part + i * kPromoteWarps * 128) = make_float4(x.x, x.y, y.x, y.y);
             }
         cluster_sync();
+        // a peer that has given up has no sums to add: neither CTA stores
+        const bool peer_ok = load_peer(abort_flag, (uint32_t)(rank ^ 1)) == 0;
 #pragma unroll
         for (int r = 0; r < 2; ++r)
           if (ok && r == rank)
@@ -303,6 +314,7 @@ matmul_fp8_tall(const __grid_constant__ Maps maps, const float* __restrict__ a_s
               acc_fma2(acc[32 * r + 2 * i + 1], 1.f, 1.f, x.z, x.w);
             }
         cluster_sync();  // the peer's sums have been read
+        ok = ok && peer_ok;
       }
       if (!ok) break;
       // by 128 bytes of columns: to shared memory with the row's 16-byte pieces permuted, then out by rows
@@ -534,39 +546,41 @@ matmul_fp8_flat(const __grid_constant__ Maps maps, const float* __restrict__ a_s
   if (split > 1) cluster_sync();
   tc_fence_after();
   // The activation rows are dealt to the warps of the cluster's CTAs; each sums the partial sums in rank order, four
-  // columns a thread.
+  // columns a thread.  A CTA that has given up has no partial sums: then nobody stores (lane r asks CTA r, beside the
+  // sums' loads).
   const int rows = M - m0 < BN ? M - m0 : BN, n = n0 + 4 * lane;
-  if (!*abort_flag) {
-    for (int j = rank + split * warp; j < rows; j += split * (kFlatThreads / 32)) {
-      const float* p = part + j * kFlatRows + 4 * lane;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (split == 1) {
-        x = *reinterpret_cast<const float4*>(p);
-      } else {
-        float4 y[kMaxSplit];
+  for (int j = rank + split * warp; j < rows; j += split * (kFlatThreads / 32)) {
+    const float* p = part + j * kFlatRows + 4 * lane;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    int gave_up = *abort_flag;
+    if (split == 1) {
+      x = *reinterpret_cast<const float4*>(p);
+    } else {
+      float4 y[kMaxSplit];
+      if (lane < split) gave_up = load_peer(abort_flag, lane);
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split) y[r] = load_peer(p, r);
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) y[r] = load_peer(p, r);
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split) x = make_float4(x.x + y[r].x, x.y + y[r].y, x.z + y[r].z, x.w + y[r].w);
-      }
-      Tout* dst = out + (int64_t)(m0 + j) * N + n;
-      if (N % 4 == 0) {
-        if (n < N) {
-          if constexpr (sizeof(Tout) == 4) {
-            *reinterpret_cast<float4*>(dst) = x;
-          } else {
-            const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
-            *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(h);
-          }
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split) x = make_float4(x.x + y[r].x, x.y + y[r].y, x.z + y[r].z, x.w + y[r].w);
+    }
+    if (__any_sync(0xffffffffu, gave_up)) break;
+    Tout* dst = out + (int64_t)(m0 + j) * N + n;
+    if (N % 4 == 0) {
+      if (n < N) {
+        if constexpr (sizeof(Tout) == 4) {
+          *reinterpret_cast<float4*>(dst) = x;
+        } else {
+          const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+          *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(h);
         }
-      } else {
-        const float v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < N) dst[e] = from_f32<Tout>(v[e]);
       }
+    } else {
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) dst[e] = from_f32<Tout>(v[e]);
     }
   }
   if (split > 1) cluster_sync();  // the peers' partial sums stay until they are read

@@ -61,3 +61,17 @@ def test_sequences_report_a_wait_that_runs_out_within_seconds(what, monkeypatch)
     for _ in range(2):
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
     assert binding.kda_get_device_error() == 0
+
+
+@pytest.mark.parametrize("what", ["few rows", "cluster", "pair"])
+def test_product_of_a_stalled_cluster_is_not_written(what, monkeypatch):
+    """The CTAs that share a tile's depth add one another's sums.  If one of them has none, the tile is left as it
+    was, by all of them, and every other tile is right."""
+    ins = product_inputs(*PRODUCTS[what])
+    want = kda.kda_matmul_fp8(*ins)
+    out = torch.full_like(want, -7.0)
+    stalled(lambda: kda.kda_matmul_fp8(*ins, out=out), monkeypatch)
+    rows, cols = (128, 256) if what == "pair" else (want.shape[0], 128)
+    assert (out[:rows, :cols] == -7).all()
+    want[:rows, :cols] = -7
+    assert torch.equal(out, want)
