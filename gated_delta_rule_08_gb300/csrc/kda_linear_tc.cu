@@ -77,6 +77,7 @@ constexpr uint32_t kTmA = 0, kTmS = 64, kTm1 = 128, kTm2 = 192, kTmU = 256, kTmV
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kEmpty = -150.f;
+constexpr float kNoSegment = -1.f;  // no decay: the segment's kernel has given up (a decay is 0 at least, or NaN)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -106,7 +107,7 @@ struct Params {
   int nseg;
   int seg_len;       // chunks of a segment
   float* seg_state;  // [B H][nseg][dk dv]: MODE 1 writes U_seg, the merge turns it into the state before the segment
-  float* seg_decay;  // [B H][nseg]
+  float* seg_decay;  // [B H][nseg]; kNoSegment where a segment, and in the last one's place where any, is missing
 };
 
 // Sequence of a CTA, in shared memory, by all threads: the longest first, so that no long one starts
@@ -353,8 +354,13 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       }
     }
     bool ok = true;
+    if (MODE == 0 && p.nseg > 1 && p.seg_decay[((int64_t)b * H + h) * p.nseg + last_seg] == kNoSegment) {
+      ok = false;  // the states of this (sequence, head) are not there: every role leaves by the abort flag
+      *abort_flag = 1;
+    }
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
+      if (!ok) break;
       if constexpr (MODE == 0) {
         // the products that read the S^T before this one
         if (c > 0) ok = warp_wait<GIVEUP>(&o_full[(c - 1) & 1], (uint32_t)(((c - 1) / 2) & 1), abort_flag);
@@ -666,6 +672,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   __syncthreads();
   drain_after_abort<kStages>(abort_flag, tid == kCopyWarp * 32, tid == kMmaWarp * 32 || tid == kMmaOutWarp * 32, full, issued,
                              bar_fin, p.err);
+  // (by the thread that wrote the decay)
+  if (MODE == 1 && tid == kCopyWarp * 32 && *abort_flag) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = kNoSegment;
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -675,7 +683,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 constexpr int kMergeThreads = 128;
 __global__ void __launch_bounds__(kMergeThreads)
 linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu, float* __restrict__ seg_state,
-                    const float* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
+                    float* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
                     int elems, int parts) {
   griddep_launch_dependents();
   const bool ok = cu == nullptr || offsets_ok(cu, B, T_tot);
@@ -687,7 +695,8 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
   const int nchunks = (int)((len + kC - 1) / kC), last = nchunks > 0 ? (nchunks - 1) / seg_len : 0;
   float4 S = h0 ? *reinterpret_cast<const float4*>(h0 + (int64_t)bh * elems + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   float* p = seg_state + (int64_t)bh * nseg * elems + at;
-  const float* e = seg_decay + (int64_t)bh * nseg;
+  float* e = seg_decay + (int64_t)bh * nseg;
+  bool missing = false;
   constexpr int kAhead = 4;  // loads under way at a time
   for (int i0 = 0; i0 < last; i0 += kAhead, p += (int64_t)kAhead * elems) {
     float4 u[kAhead];
@@ -697,6 +706,7 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
       const bool in = i0 + i < last;
       u[i] = in ? *reinterpret_cast<const float4*>(p + (int64_t)i * elems) : make_float4(0.f, 0.f, 0.f, 0.f);
       d[i] = in ? e[i0 + i] : 0.f;
+      missing |= d[i] == kNoSegment;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
@@ -706,6 +716,7 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
       }
   }
   *reinterpret_cast<float4*>(seg_state + ((int64_t)bh * nseg + last) * elems + at) = S;
+  if (blockIdx.x % parts == 0 && threadIdx.x == 0) e[last] = missing ? kNoSegment : 0.f;
 }
 
 // Segments, of n chunks at least so long that all of them, with one short one for each (sequence, head), make at most
@@ -794,7 +805,7 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, const Params& p, cudaS
     const int elems = DK * a.dv, parts = elems / (4 * kMergeThreads);
     TraceScope ts("kda_linear_merge", st);
     const cudaError_t e = launch_after(linear_merge_kernel, (unsigned)(a.B * a.H * parts), kMergeThreads, 0, st, true, a.h0,
-                                       a.cu_seqlens, p.seg_state, (const float*)p.seg_decay, a.B, a.T, a.T_tot, a.H, p.nseg,
+                                       a.cu_seqlens, p.seg_state, p.seg_decay, a.B, a.T, a.T_tot, a.H, p.nseg,
                                        p.seg_len, elems, parts);
     if (e != cudaSuccess) return e;
   }

@@ -75,3 +75,21 @@ def test_product_of_a_stalled_cluster_is_not_written(what, monkeypatch):
     assert (out[:rows, :cols] == -7).all()
     want[:rows, :cols] = -7
     assert torch.equal(out, want)
+
+
+def test_sequence_of_a_stalled_segment_is_not_written(monkeypatch):
+    """A (sequence, head) of which a segment's contribution is missing keeps what was in out and hT, in all its
+    segments; the other head and the other sequence are right."""
+    ins = linear_inputs(33, (2500, 1400), 2, 128, 128, BF, "token", True, False)
+
+    def call(**kw):
+        return kda.kda_linear_chunk_fwd(ins["q"], ins["k"], ins["v"], ins["g"], h0=ins["h0"], cu_seqlens=ins["cu"], **kw)
+
+    want = call()
+    out, hT = torch.full_like(want[0], -7.0), torch.full_like(want[1], -7.0)
+    stalled(lambda: call(out=out, hT=hT), monkeypatch)
+    assert (out[:2500, 0] == -7).all() and (hT[0, 0] == -7).all()
+    want[0][:2500, 0] = -7
+    want[1][0, 0] = -7
+    assert torch.equal(out, want[0]) and torch.equal(hT, want[1])
+    assert all(not (t == -7).all() for t in call())
