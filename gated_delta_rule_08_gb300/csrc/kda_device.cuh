@@ -30,6 +30,16 @@ __device__ __forceinline__ float4 f4_fma(float a, float4 b, float4 c) {
   return make_float4(fmaf(a, b.x, c.x), fmaf(a, b.y, c.y), fmaf(a, b.z, c.z), fmaf(a, b.w, c.w));
 }
 
+// What is left of a decay e^x when it is rounded to `hi`, so that hi + low is closer to it than an fp32 number can be.  A
+// state is decayed by the same factor again and again where x is constant: the factor's rounding would add up over
+// the 1 / |x| tokens that a state remembers.  e^x - 1 is known to a step of its own, smaller size, and hi - 1 is
+// exact for hi in [1/2, 2]; below that a state forgets within a token or two, and nothing adds up.
+__device__ __forceinline__ float decay_low(float x, float hi) {
+  return hi >= 0.5f && hi <= 2.f ? expm1f(x) - (hi - 1.f) : 0.f;
+}
+// s e^x + k v for a decay in two parts
+__device__ __forceinline__ float decay_add(float2 e, float s, float k, float v) { return fmaf(e.x, s, fmaf(k, v, e.y * s)); }
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);

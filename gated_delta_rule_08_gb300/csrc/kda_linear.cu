@@ -7,8 +7,11 @@
 // linear_recurrent_kernel: whole sequences of fp32 inputs, token by token (bf16: kda_linear_tc.cu), so that fp32
 // inputs are multiplied as fp32.  Value columns are independent of one another, so a CTA takes 16 of them for the
 // whole sequence and keeps its dk x 16 slice of the state in registers; a thread owns dk / 8 rows of one column.
-// Bound by the chain of tokens: ~95 ns a token at dk = 64 and ~130 ns at 128 (1024 tokens of one sequence: 96.2 and
-// 134 us); with every SM busy by the instructions (8 x 1024 tokens, H = 32, d = 128: 1.29 ms).
+// Decays come in two parts (decay_low), by a fifth warp that works a stage ahead: with e^g as one fp32 number the
+// states were off by 1.3e-5 at g = -2^-8 and by 2e-4 over 8192 tokens at -1e-5, with two by 2.9e-7 and 1.6e-6, which
+// is what rounding the state once a token leaves.
+// Bound by the chain of tokens: ~110 ns a token at dk = 64 and ~138 ns at 128 (1024 tokens of one sequence, d = 128:
+// 141 us; with single decays 134); with every SM busy by the instructions (8 x 1000 tokens, H = 32, d = 128: 1.12 ms).
 //
 // linear_step_kernel: one token per request on a pool of states, in place (section 13.9's pooled
 // layout).  It streams each state in and out once.
@@ -22,25 +25,43 @@ namespace {
 constexpr int kCols = 16;  // value columns of a CTA
 constexpr int kTile = 8;   // tokens of a stage
 constexpr int kRecStages = 6;  // the copies run five stages ahead: a token takes less time than a load
-constexpr int kRecThreads = 128;
+constexpr int kRecThreads = 128;  // and a warp that makes the decays
 
 template <int DK>
 struct RecStage {
-  float k[kTile][DK], q[kTile][DK], v[kTile][kCols], g[kTile];
+  float k[kTile][DK], q[kTile][DK], v[kTile][kCols];
 };
 
-// `bytes` (4 or 16) of global memory to shared memory without registers; zeros if not `in`
-template <int bytes>
+// 16 bytes of global memory to shared memory without registers; zeros if not `in`
 __device__ __forceinline__ void cp_async_zero(void* dst, const void* src, bool in) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// Two fp32 lanes an instruction, each rounded as the scalar operation.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 template <int DK, typename Tout>
-__global__ void __launch_bounds__(kRecThreads)
+__global__ void __launch_bounds__(kRecThreads + 32)
 linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                         int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* __restrict__ g,
                         int g_per_token, const float* h0, const int32_t* __restrict__ cu, Tout* __restrict__ out,
@@ -50,6 +71,7 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
   extern __shared__ __align__(16) uint8_t rec_smem[];
   RecStage<DK>* stages = reinterpret_cast<RecStage<DK>*>(rec_smem);
   __shared__ float so[kTile][kCols];
+  __shared__ float2 se[2][kTile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = dv / kCols;
   const int slice = blockIdx.x % slices, bh = blockIdx.x / slices, h = bh % H, b = bh / H;
@@ -63,13 +85,39 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
     t0 = cu[b];
     n = cu[b + 1] - cu[b];
   }
+  if (warp == kRecThreads / 32) {
+    // The decays of a stage, in two parts: made while the stage before is worked on, from values loaded while the
+    // one before that was.  Tokens past the sequence have none.
+    const float* pg = g + (g_per_token ? (t0 + lane) * H + h : h);
+    const int64_t g_step = g_per_token ? (int64_t)kTile * H : 0;
+    auto decays = [&](float x) {
+      const float e = expf(x);
+      return make_float2(e, decay_low(x, e));
+    };
+    float g_next = lane < kTile && lane < n ? *pg : 0.f;
+    int par = 0;
+#pragma unroll 1
+    for (int c = 0; c < n; c += kTile) {
+      const float x = g_next;
+      pg += g_step;
+      g_next = lane < kTile && c + kTile + lane < n ? *pg : 0.f;
+      if (lane < kTile) se[par][lane] = decays(x);
+      par ^= 1;
+      __syncthreads();
+      __syncthreads();
+    }
+    return;
+  }
   const int rg = lane & 7, col = warp * 4 + (lane >> 3);
   const int64_t soff = ((int64_t)b * H + h) * DK * dv + slice * kCols + col;
-  float s[NI][4];
+  uint64_t s[NI][2];  // pairs of rows
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = h0 ? h0[soff + (int64_t)(32 * i + 4 * rg + j) * dv] : 0.f;
+    for (int j = 0; j < 2; ++j) {
+      const float* at = h0 + soff + (int64_t)(32 * i + 4 * rg + 2 * j) * dv;
+      s[i][j] = h0 ? pair2(at[0], at[dv]) : 0;
+    }
 
   // This thread's pieces of a stage: a row of k and q every kRowStep tokens, a piece of v, a decay.  Tokens past
   // the sequence come as zeros with no decay (read from the sequence's first, of size 0).
@@ -78,8 +126,6 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
   const float* pk = k + (t0 + r0) * k_stride + h * DK + d0;
   const float* pq = q + (t0 + r0) * q_stride + h * DK + d0;
   const float* pv = v + (t0 + rv) * v_stride + (int64_t)h * dv + slice * kCols + dv0;
-  const float* pg = g + (g_per_token ? (t0 + tid) * H + h : h);
-  const int64_t g_step = g_per_token ? (int64_t)kTile * H : 0;
   int fetched = 0, put = 0;
   auto fetch = [&] {
     if (fetched < n) {
@@ -88,15 +134,13 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
       for (int i = 0; i < kRows; ++i) {
         const int r = r0 + i * kRowStep;
         const bool in = fetched + r < n;
-        cp_async_zero<16>(&st.k[r][d0], in ? pk + i * kRowStep * k_stride : k, in);
-        cp_async_zero<16>(&st.q[r][d0], in ? pq + i * kRowStep * q_stride : q, in);
+        cp_async_zero(&st.k[r][d0], in ? pk + i * kRowStep * k_stride : k, in);
+        cp_async_zero(&st.q[r][d0], in ? pq + i * kRowStep * q_stride : q, in);
       }
-      if (tid < kTile * kCols / 4) cp_async_zero<16>(&st.v[rv][dv0], fetched + rv < n ? pv : v, fetched + rv < n);
-      if (tid < kTile) cp_async_zero<4>(&st.g[tid], fetched + tid < n ? pg : g, fetched + tid < n);
+      if (tid < kTile * kCols / 4) cp_async_zero(&st.v[rv][dv0], fetched + rv < n ? pv : v, fetched + rv < n);
       pk += kTile * k_stride;
       pq += kTile * q_stride;
       pv += kTile * v_stride;
-      pg += g_step;
       fetched += kTile;
       put = put + 1 < kRecStages ? put + 1 : 0;
     }
@@ -105,7 +149,7 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
 #pragma unroll 1
   for (int i = 0; i < kRecStages - 1; ++i) fetch();
   Tout* po = out + ((t0 + tid / kCols) * H + h) * dv + slice * kCols + tid % kCols;
-  int get = 0;
+  int get = 0, par = 0;
 #pragma unroll 1
   for (int c = 0; c < n; c += kTile) {
     const int m = n - c < kTile ? n - c : kTile;
@@ -121,22 +165,20 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
       float acc[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float e = expf(st.g[t + u]), x = st.v[t + u][col];
-        float a0 = 0.f, a1 = 0.f;
+        const float2 e = se[par][t + u];
+        const float x = st.v[t + u][col];
+        const uint64_t e2 = pair2(e.x, e.x), low2 = pair2(e.y, e.y), x2 = pair2(x, x);
+        uint64_t a = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const float4 k4 = *reinterpret_cast<const float4*>(&st.k[t + u][32 * i + 4 * rg]);
-          const float4 q4 = *reinterpret_cast<const float4*>(&st.q[t + u][32 * i + 4 * rg]);
-          s[i][0] = fmaf(k4.x, x, e * s[i][0]);
-          s[i][1] = fmaf(k4.y, x, e * s[i][1]);
-          s[i][2] = fmaf(k4.z, x, e * s[i][2]);
-          s[i][3] = fmaf(k4.w, x, e * s[i][3]);
-          a0 = fmaf(q4.x, s[i][0], a0);
-          a1 = fmaf(q4.y, s[i][1], a1);
-          a0 = fmaf(q4.z, s[i][2], a0);
-          a1 = fmaf(q4.w, s[i][3], a1);
+          const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(&st.k[t + u][32 * i + 4 * rg]);
+          const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(&st.q[t + u][32 * i + 4 * rg]);
+          s[i][0] = fma2(e2, s[i][0], fma2(k4.x, x2, mul2(low2, s[i][0])));
+          s[i][1] = fma2(e2, s[i][1], fma2(k4.y, x2, mul2(low2, s[i][1])));
+          a = fma2(q4.x, s[i][0], a);
+          a = fma2(q4.y, s[i][1], a);
         }
-        acc[u] = a0 + a1;
+        acc[u] = split2(a).x + split2(a).y;
       }
       // sums over the eight row groups; lane rg keeps token t + (rg & 3)
 #pragma unroll
@@ -152,12 +194,17 @@ linear_recurrent_kernel(const float* __restrict__ q, const float* __restrict__ k
     static_assert(kTile * kCols == kRecThreads, "one output a thread");
     if (tid < m * kCols) *po = from_f32<Tout>(scale * (&so[0][0])[tid]);
     po += (int64_t)kTile * H * dv;
+    par ^= 1;
   }
   if (hT) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) hT[soff + (int64_t)(32 * i + 4 * rg + j) * dv] = s[i][j];
+      for (int j = 0; j < 2; ++j) {
+        float* at = hT + soff + (int64_t)(32 * i + 4 * rg + 2 * j) * dv;
+        at[0] = split2(s[i][j]).x;
+        at[dv] = split2(s[i][j]).y;
+      }
   }
 }
 
@@ -175,7 +222,7 @@ cudaError_t recurrent_typed(const LinearArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   auto* kernel = a.dk == 64 ? linear_recurrent_kernel<64, Tout> : linear_recurrent_kernel<128, Tout>;
   TraceScope ts("kda_linear_recurrent", st);
-  kernel<<<(unsigned)grid, kRecThreads, a.dk == 64 ? kRecStages * sizeof(RecStage<64>) : kSmem, st>>>(
+  kernel<<<(unsigned)grid, kRecThreads + 32, a.dk == 64 ? kRecStages * sizeof(RecStage<64>) : kSmem, st>>>(
       static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v), a.q_stride,
       a.k_stride, a.v_stride, a.g, a.g_per_token, a.h0, a.cu_seqlens, static_cast<Tout*>(a.out), a.hT, a.B, a.T, a.T_tot, a.H,
       a.dv, a.scale, a.err);
@@ -216,7 +263,10 @@ linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const T
 #pragma unroll
   for (int i = 0; i < RPG; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(S + (rg * RPG + i) * DV));
 
-  const float e = expf(g[g_per_token ? (int64_t)nh : h]);
+  const float log_decay = g[g_per_token ? (int64_t)nh : h];
+  float2 e;
+  e.x = expf(log_decay);
+  e.y = decay_low(log_decay, e.x);
   for (int i = tid; i < DK; i += kStepThreads) {
     sk[i] = to_f32(k[n * k_stride + h * DK + i]);
     sq[i] = to_f32(q[n * q_stride + h * DK + i]);
@@ -231,7 +281,8 @@ linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const T
 #pragma unroll
   for (int i = 0; i < RPG; ++i) {
     const float kk = sk[rg * RPG + i], qq = sq[rg * RPG + i];
-    s[i] = f4_fma(kk, x, make_float4(e * s[i].x, e * s[i].y, e * s[i].z, e * s[i].w));
+    s[i] = make_float4(decay_add(e, s[i].x, kk, x.x), decay_add(e, s[i].y, kk, x.y), decay_add(e, s[i].z, kk, x.z),
+                       decay_add(e, s[i].w, kk, x.w));
     __stcs(reinterpret_cast<float4*>(S + (rg * RPG + i) * DV), s[i]);
     acc = f4_fma(qq, s[i], acc);
   }
