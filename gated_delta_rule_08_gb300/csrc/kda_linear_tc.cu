@@ -65,8 +65,8 @@ struct Decay {
   float E[kC];    // scale e^{G_i} on the state before the chunk; 0 once it has been emptied
   float W[kC];    // w_j; 0 for tokens past the sequence (before: the log decays)
   int first[kC];  // the first token that reaches token i
-  float all;      // decay of the state over the whole chunk
-  int pad[3];
+  float all, low;  // decay of the state over the whole chunk, in two parts (decay_low)
+  int pad[2];
 };
 constexpr uint32_t kBar = kDecay + kRing * sizeof(Decay);
 constexpr uint32_t kSmem = kBar + 256 + 1024;
@@ -75,7 +75,7 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 // TMEM columns
 constexpr uint32_t kTmA = 0, kTmS = 64, kTm1 = 128, kTm2 = 192, kTmU = 256, kTmV = 384;  // V~^T: three parts of 32
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kEmpty = -150.f;
 constexpr float kNoSegment = -1.f;  // no decay: the segment's kernel has given up (a decay is 0 at least, or NaN)
 
@@ -107,7 +107,7 @@ struct Params {
   int nseg;
   int seg_len;       // chunks of a segment
   float* seg_state;  // [B H][nseg][dk dv]: MODE 1 writes U_seg, the merge turns it into the state before the segment
-  float* seg_decay;  // [B H][nseg]; kNoSegment where a segment, and in the last one's place where any, is missing
+  float2* seg_decay;  // [B H][nseg], in two parts; kNoSegment where a segment, and in the last one's place where any, is missing
 };
 
 // Sequence of a CTA, in shared memory, by all threads: the longest first, so that no long one starts
@@ -125,6 +125,12 @@ __device__ __forceinline__ int sequence_by_rank(const int32_t* __restrict__ cu, 
   }
   __syncthreads();
   return *slot;
+}
+
+// The decay 2^x, or that of an emptied state, in two parts: equal chunks and segments decay by equal factors.
+__device__ __forceinline__ float2 decay_parts(float x, bool emptied) {
+  const float e = emptied ? 0.f : exp2f(x);
+  return make_float2(e, decay_low(kLn2 * x, e));
 }
 
 // Decays of one chunk (one warp, tokens 2 lane and 2 lane + 1).  Returns log2 of the chunk's decay and
@@ -173,7 +179,11 @@ __device__ __forceinline__ float chunk_decay(Decay* d, float g0, float g1, int n
   d->first[i0] = l0 < 0 ? 0 : l0;
   d->first[i1] = l1 < 0 ? 0 : l1;
   emptied = final_last >= 0;
-  if (lane == 0) d->all = emptied ? 0.f : exp2f(total);
+  const float2 e = decay_parts(total, emptied);
+  if (lane == 0) {
+    d->all = e.x;
+    d->low = e.y;
+  }
   return total;
 }
 
@@ -354,7 +364,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       }
     }
     bool ok = true;
-    if (MODE == 0 && p.nseg > 1 && p.seg_decay[((int64_t)b * H + h) * p.nseg + last_seg] == kNoSegment) {
+    if (MODE == 0 && p.nseg > 1 && p.seg_decay[((int64_t)b * H + h) * p.nseg + last_seg].x == kNoSegment) {
       ok = false;  // the states of this (sequence, head) are not there: every role leaves by the abort flag
       *abort_flag = 1;
     }
@@ -381,7 +391,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (!ok) break;
       warp_arrive(&empty[c % kStages]);
       tc_fence_after();
-      const float all = decay[c % kRing].all;
+      const float all = decay[c % kRing].all, low = decay[c % kRing].low;
 #pragma unroll
       for (int i = 0; i < KC / 32; ++i) {
         float u[32];
@@ -393,7 +403,8 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float2 s = fma2(make_float2(all, all), make_float2(S[32 * i + j], S[32 * i + j + 1]), make_float2(u[j], u[j + 1]));
+          const float2 before = make_float2(S[32 * i + j], S[32 * i + j + 1]);
+          const float2 s = fma2(make_float2(all, all), before, fma2(make_float2(low, low), before, make_float2(u[j], u[j + 1])));
           S[32 * i + j] = s.x;
           S[32 * i + j + 1] = s.y;
         }
@@ -463,7 +474,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
         fetch_g(c + kAhead);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (MODE == 1 && lane == 0) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = any ? 0.f : exp2f(total + lost);
+      if (MODE == 1 && lane == 0) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = decay_parts(total + lost, any);
     } else if (warp == kMmaWarp) {
       // ======================== D_A and D_U
       {
@@ -673,7 +684,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
   drain_after_abort<kStages>(abort_flag, tid == kCopyWarp * 32, tid == kMmaWarp * 32 || tid == kMmaOutWarp * 32, full, issued,
                              bar_fin, p.err);
   // (by the thread that wrote the decay)
-  if (MODE == 1 && tid == kCopyWarp * 32 && *abort_flag) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg] = kNoSegment;
+  if (MODE == 1 && tid == kCopyWarp * 32 && *abort_flag) p.seg_decay[((int64_t)b * H + h) * p.nseg + seg].x = kNoSegment;
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
@@ -683,7 +694,7 @@ linear_chunk_kernel(const __grid_constant__ Maps maps, const Params p) {
 constexpr int kMergeThreads = 128;
 __global__ void __launch_bounds__(kMergeThreads)
 linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu, float* __restrict__ seg_state,
-                    float* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
+                    float2* __restrict__ seg_decay, int B, int64_t T, int64_t T_tot, int H, int nseg, int seg_len,
                     int elems, int parts) {
   griddep_launch_dependents();
   const bool ok = cu == nullptr || offsets_ok(cu, B, T_tot);
@@ -695,28 +706,28 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
   const int nchunks = (int)((len + kC - 1) / kC), last = nchunks > 0 ? (nchunks - 1) / seg_len : 0;
   float4 S = h0 ? *reinterpret_cast<const float4*>(h0 + (int64_t)bh * elems + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   float* p = seg_state + (int64_t)bh * nseg * elems + at;
-  float* e = seg_decay + (int64_t)bh * nseg;
+  float2* e = seg_decay + (int64_t)bh * nseg;
   bool missing = false;
   constexpr int kAhead = 4;  // loads under way at a time
   for (int i0 = 0; i0 < last; i0 += kAhead, p += (int64_t)kAhead * elems) {
     float4 u[kAhead];
-    float d[kAhead];
+    float2 d[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const bool in = i0 + i < last;
       u[i] = in ? *reinterpret_cast<const float4*>(p + (int64_t)i * elems) : make_float4(0.f, 0.f, 0.f, 0.f);
-      d[i] = in ? e[i0 + i] : 0.f;
-      missing |= d[i] == kNoSegment;
+      d[i] = in ? e[i0 + i] : make_float2(0.f, 0.f);
+      missing |= d[i].x == kNoSegment;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i0 + i < last) {
         *reinterpret_cast<float4*>(p + (int64_t)i * elems) = S;
-        S = f4_fma(d[i], S, u[i]);
+        S = f4_fma(d[i].x, S, f4_fma(d[i].y, S, u[i]));
       }
   }
   *reinterpret_cast<float4*>(seg_state + ((int64_t)bh * nseg + last) * elems + at) = S;
-  if (blockIdx.x % parts == 0 && threadIdx.x == 0) e[last] = missing ? kNoSegment : 0.f;
+  if (blockIdx.x % parts == 0 && threadIdx.x == 0) e[last].x = missing ? kNoSegment : 0.f;
 }
 
 // Segments, of n chunks at least so long that all of them, with one short one for each (sequence, head), make at most
@@ -825,7 +836,7 @@ size_t linear_tc_workspace(int B, int64_t T, int H, int dk, int dv) {
   for (int has_cu = 0; has_cu < 2; ++has_cu) {
     int nseg, seg_len;
     segments(B, T, has_cu ? T : (int64_t)B * T, has_cu != 0, H, sms, &nseg, &seg_len);
-    const size_t n = nseg > 1 ? (size_t)B * H * nseg * ((size_t)dk * dv + 1) * sizeof(float) : 0;
+    const size_t n = nseg > 1 ? (size_t)B * H * nseg * ((size_t)dk * dv + 2) * sizeof(float) : 0;
     if (n > most) most = n;
   }
   return align_up(most, 256);
@@ -841,7 +852,7 @@ cudaError_t linear_tc_launch(const LinearArgs& a, cudaStream_t st) {
   p.B = a.B; p.T = a.T; p.T_tot = a.T_tot; p.H = a.H; p.dv = a.dv; p.scale = a.scale; p.err = a.err;
   segments(a.B, a.T, a.T_tot, a.cu_seqlens != nullptr, a.H, sms, &p.nseg, &p.seg_len);
   p.seg_state = static_cast<float*>(a.workspace);
-  p.seg_decay = p.seg_state + (size_t)a.B * a.H * p.nseg * a.dk * a.dv;
+  p.seg_decay = reinterpret_cast<float2*>(p.seg_state + (size_t)a.B * a.H * p.nseg * a.dk * a.dv);
   Maps maps{};
   if (a.T_tot > 0 &&
       (!tensor_map_2d(&maps.q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.T_tot, (uint64_t)a.H * a.dk, a.q_stride * 2, kC, 64) ||

@@ -42,6 +42,21 @@ def test_fp32_sequences(T, dk, dv):
     check(hT[0], closed_form(k, v, g, h0[0]), T, 1, 4)
 
 
+@pytest.mark.parametrize("copies", [1, 20], ids=["cut", "uncut"])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+def test_bf16_sequences(dk, dv, copies):
+    """base: the weights of a chunk's tokens (two steps of the exponential, half a one of the product: 5 F32) and
+    the twelve accumulations of its product in the tensor core (a step each, at random: 2 sqrt(12) F32)."""
+    T, H = 8192, copies * len(RATES)
+    r = gen(T + dk + copies)
+    g = torch.tensor(copies * RATES, device="cuda")
+    q, k, v = randn(r, T, H, dk, dtype=BF), randn(r, T, H, dk, dtype=BF), randn(r, T, H, dv, dtype=BF)
+    h0 = randn(r, 1, H, dk, dv)
+    _, hT = kda.kda_linear_chunk_fwd(q, k, v, g, h0=h0)
+    n = len(RATES)
+    check(hT[0, :n], closed_form(k[:, :n], v[:, :n], g[:n], h0[0, :n]), T, 64, 12)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp32"])
 def test_tokens_one_by_one(dtype):
     T, H, dk, dv = 2048, len(RATES), 128, 64
