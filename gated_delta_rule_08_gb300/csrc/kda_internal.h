@@ -177,6 +177,9 @@ cudaError_t decode_launch(const DecodeArgs& a, cudaStream_t stream);
 // built for; false if a CUDA query failed.
 bool device_ready(unsigned int** err, bool* supported);
 
+// Tokens of a kda_linear_chunk_fwd call: the kernels' 32-bit token numbers run up to 512 past the last one.
+constexpr int64_t kMaxTokens = 0x7fffffff - 1023;
+
 // Linear attention with one decay per head: S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
 struct LinearArgs {
   const void* q;              // token rows at q_stride / k_stride / v_stride elements, heads dense inside a row

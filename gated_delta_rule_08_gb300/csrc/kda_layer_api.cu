@@ -16,6 +16,9 @@ bool dtype_ok(kda_dtype d) { return d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32; 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Sequences, tokens and heads of a linear attention call (32-bit token numbers and grids).
+bool counts_ok(int B, int64_t T_tot, int H) { return T_tot <= kMaxTokens && B <= 16384 && (int64_t)B * H <= 0x7fffffff / 64; }
+
 // Row strides of q, k, v (elements): rows may not overlap, and each must start on a 16-byte boundary.
 bool stride_ok(int64_t stride, int64_t row, kda_dtype d) {
   return stride >= row && stride < ((int64_t)1 << 32) && stride % (d == KDA_DTYPE_BF16 ? 8 : 4) == 0;
@@ -32,7 +35,7 @@ kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA
 }  // namespace
 
 KDA_API size_t kda_linear_chunk_fwd_workspace_size(int B, int64_t T, int H, int dk, int dv, kda_dtype dtype) {
-  if (B <= 0 || T < 0 || H <= 0 || !dims_ok(dk, dv) || !dtype_ok(dtype)) return 0;
+  if (B <= 0 || T < 0 || H <= 0 || !dims_ok(dk, dv) || !dtype_ok(dtype) || !counts_ok(B, T, H)) return 0;
   return 256 + (dtype == KDA_DTYPE_BF16 ? linear_tc_workspace(B, T, H, dk, dv) : 0);
 }
 
@@ -45,7 +48,7 @@ KDA_API kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void
   if (!dtype_ok(dtype) || !dtype_ok(out_dtype) || !dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
   if (!cu_seqlens && T > ((int64_t)1 << 40) / B) return KDA_ERR_UNSUPPORTED;
   const int64_t T_tot = cu_seqlens ? T : (int64_t)B * T;
-  if (T_tot > 0x7fffffff || B > 16384 || (int64_t)B * H > 0x7fffffff / 64) return KDA_ERR_UNSUPPORTED;  // 32-bit token coordinates
+  if (!counts_ok(B, T_tot, H)) return KDA_ERR_UNSUPPORTED;
   if (!stride_ok(q_stride, (int64_t)H * dk, dtype) || !stride_ok(k_stride, (int64_t)H * dk, dtype) ||
       !stride_ok(v_stride, (int64_t)H * dv, dtype))
     return KDA_ERR_INVALID_ARG;

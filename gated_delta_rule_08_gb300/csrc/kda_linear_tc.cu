@@ -834,6 +834,7 @@ size_t linear_tc_workspace(int B, int64_t T, int H, int dk, int dv) {
   if (device_sms(&sms) != cudaSuccess) return 0;
   size_t most = 0;  // with and without offsets (T is then one sequence's length)
   for (int has_cu = 0; has_cu < 2; ++has_cu) {
+    if (!has_cu && B * T > kMaxTokens) continue;  // not a call without offsets
     int nseg, seg_len;
     segments(B, T, has_cu ? T : (int64_t)B * T, has_cu != 0, H, sms, &nseg, &seg_len);
     const size_t n = nseg > 1 ? (size_t)B * H * nseg * ((size_t)dk * dv + 2) * sizeof(float) : 0;

@@ -290,7 +290,7 @@ kda_status kda_matmul_fp8(const void* a, const float* a_scale, const void* b, co
  *               KDA_DEVERR_BAD_SEQLENS, and nothing is written
  *   B         : at most 16384
  *   out       : [T_tot, H, dv] (out_dtype), dense; must not overlap an input
- *   T         : as for kda_chunk_fwd; T_tot below 2^31
+ *   T         : as for kda_chunk_fwd; T_tot at most 2^31 - 1024
  *   workspace : at least kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte aligned
  * q, k, v and the states have to be finite (a chunk's values meet in tensor-core products, where an
  * infinity times a masked zero is NaN). */
