@@ -112,6 +112,10 @@ int test_wait_timeout() {
   return strcmp(e, "stall") == 0 ? 2 : 1;
 }
 
+cudaError_t check_slots(const int32_t* slot, int N, int num_slots, unsigned int* err, cudaStream_t st) {
+  return launch_checks(nullptr, 0, nullptr, 0, slot, N, num_slots, err, st);
+}
+
 bool debug_checks() {
   const char* e = getenv("KDA_DEBUG_CHECKS");
   return e != nullptr && *e != '\0' && strcmp(e, "0") != 0;

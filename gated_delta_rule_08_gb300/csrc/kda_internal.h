@@ -44,6 +44,8 @@ int test_wait_timeout();
 // before the hot-path kernels, a check kernel tests the documented preconditions on the device
 // (g in (-5, 0], beta in [0, 1], distinct decode slots) and sets KDA_DEVERR_PRECONDITION.
 bool debug_checks();
+// The check of distinct slots alone.
+cudaError_t check_slots(const int32_t* slot, int N, int num_slots, unsigned int* err, cudaStream_t stream);
 
 // Epilogue arguments as the kernels see them (gate == nullptr: no epilogue).
 struct Epilogue {

@@ -96,7 +96,9 @@ KDA_API kda_status kda_linear_decode_step(const void* q, const void* k, const vo
   a.g = g; a.g_per_token = g_per_token != 0; a.state_pool = state_pool; a.slot_idx = slot_idx; a.out = out;
   a.N = N; a.H = H; a.dk = dk; a.dv = dv; a.num_slots = num_slots; a.scale = scale;
   a.bf16 = dtype == KDA_DTYPE_BF16; a.out_bf16 = out_dtype == KDA_DTYPE_BF16; a.err = err;
-  return done(linear_step_launch(a, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (debug_checks() && check_slots(slot_idx, N, num_slots, err, s) != cudaSuccess) return KDA_ERR_CUDA;
+  return done(linear_step_launch(a, s));
 }
 
 KDA_API kda_status kda_rmsnorm_quant(const void* x, const void* residual, const float* weight, void* residual_out,

@@ -41,7 +41,8 @@
  *   - Debugging: with the environment variable KDA_DEBUG_CHECKS set (any value but "" or "0";
  *     read at every call), kda_chunk_fwd*, kda_chunk_fwd_segment_map and kda_decode_* first run
  *     a check kernel over the inputs and set KDA_DEVERR_PRECONDITION when g is outside (-5, 0],
- *     beta outside [0, 1], or (decode) two requests name the same slot.  The check reads every
+ *     beta outside [0, 1], or (decode) two requests name the same slot; kda_linear_decode_step
+ *     looks for such slots too.  The check reads every
  *     g and beta once (decode: O(N^2) slot comparisons); it is off by default.
  *   - Testing: with the environment variable KDA_TEST_WAIT_TIMEOUT set (any value but "" or "0";
  *     read at every call) the prefill, kda_matmul_fp8 and kda_linear_chunk_fwd launch kernel variants
@@ -304,7 +305,7 @@ kda_status kda_linear_chunk_fwd(const void* q, const void* k, const void* v, con
 /* One token of linear attention for N requests on a pool of fp32 states, updated in place.
  *   q, k, v   : [N, H, dk] / [N, H, dv] (dtype) with row strides as in kda_linear_chunk_fwd
  *   g         : [N, H] if g_per_token, else [H], fp32
- *   state_pool, slot_idx : as for kda_decode_step (distinct slots; a bad index sets
+ *   state_pool, slot_idx : as for kda_decode_step (finite states, distinct slots; a bad index sets
  *               KDA_DEVERR_BAD_SLOT and leaves that request's rows and every slot untouched)
  *   out       : [N, H, dv] (out_dtype), dense */
 kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, const float* g, int g_per_token,
