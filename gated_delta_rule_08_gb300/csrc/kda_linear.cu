@@ -10,8 +10,9 @@
 // Decays come in two parts (decay_low), by a fifth warp that works a stage ahead: with e^g as one fp32 number the
 // states were off by 1.3e-5 at g = -2^-8 and by 2e-4 over 8192 tokens at -1e-5, with two by 2.9e-7 and 1.6e-6, which
 // is what rounding the state once a token leaves.
-// Bound by the chain of tokens: ~110 ns a token at dk = 64 and ~138 ns at 128 (1024 tokens of one sequence, d = 128:
-// 141 us; with single decays 134); with every SM busy by the instructions (8 x 1000 tokens, H = 32, d = 128: 1.12 ms).
+// Bound by the chain of tokens: ~110 ns a token at dk = 64 and ~138 ns at 128 (1024 tokens of one sequence: 112 and
+// 141 us; with single decays 96 and 134); with every SM busy by the instructions (8 x 1024 tokens, H = 32, d = 128:
+// 1.15 ms).
 //
 // linear_step_kernel: one token per request on a pool of states, in place (section 13.9's pooled
 // layout).  It streams each state in and out once.
@@ -235,7 +236,7 @@ constexpr int kStepThreads = 256;
 // CTA = (request, head).  A thread owns four columns of DK / NG consecutive rows, so a warp's state accesses are
 // whole 128-bit pieces of a row; the state stays in registers between load and store.
 //
-// Bound by the states' bytes, read once and written once: 256 requests x 32 heads of 128 x 128 take 157.6 us,
+// Bound by the states' bytes, read once and written once: 256 requests x 32 heads of 128 x 128 take 156 us,
 // 6.8 TB/s (the rate of a plain copy).  Few requests are bound by the latency of a load, a product and a store:
 // 32 states 2.9 us, 128 states 3.1 us.
 template <int DK, int DV, typename Tin, typename Tout>

@@ -30,8 +30,8 @@
 // compute every segment's own contribution U_seg to the state after it (no read-out), a merge kernel
 // folds them in order, and MODE 0 runs every segment from its state.
 //
-// Measured, bf16, H = 32, d = 128: 1 x 8192 tokens 128 us (segments 52, merge 8, last pass 78; of 272 MB, 2.1 TB/s),
-// 8 sequences of 512 to 8192 tokens 251 us (3.2 TB/s), where the longest's 128 chunks of 2 us follow one another.
+// Measured, bf16, H = 32, d = 128: 1 x 8192 tokens 127 us (segments 54, merge 8, last pass 78, which overlap; of 272 MB,
+// 2.1 TB/s), 8 sequences of 512 to 8192 tokens 246 us (3.3 TB/s), where the longest's 128 chunks of 2 us follow one another.
 // Bound by the instructions and the shared-memory traffic of a chunk, not by HBM: 32 MMAs at one in 120-150 clocks,
 // four schedulers at half their issue rate, two state products whose operands change between TMEM, registers
 // and shared memory.
@@ -731,10 +731,10 @@ linear_merge_kernel(const float* __restrict__ h0, const int32_t* __restrict__ cu
 }
 
 // Segments, of n chunks at least so long that all of them, with one short one for each (sequence, head), make at most
-// one CTA an SM (a second wave would cost as much as the first).  Measured, a pass over L chunks takes 2 L + 8 us and
-// the three launches of a cut one 3 n + 20 us, so a cut is taken where 3 n + 12 < 2 L.  Uncut against cut, us:
-//   1 x 640, H = 32: 28 / 32;  1 x 1024: 40 / 35;  1 x 2048: 69 / 48;  1 x 4096: 131 / 77;  2 x 4096: 132 / 165;
-//   1 x 4096, H = 8: 127 / 36.
+// one CTA an SM (a second wave would cost as much as the first).  Measured, a pass over L chunks takes 1.9 L + 6 us and
+// the three launches of a cut one 3 n + 19 us, so a cut is taken where 3 n + 12 < 2 L.  Uncut against cut, us:
+//   1 x 640, H = 32: 25 / 27;  1 x 1024: 36 / 31;  1 x 2048: 65 / 44;  1 x 4096: 127 / 73;  2 x 4096: 126 / 161;
+//   1 x 4096, H = 8: 123 / 32.  With d = 64: 20 / 21, 29 / 24, 52 / 34, 99 / 56, 100 / 126 and 99 / 23.
 // Lengths given by offsets are on the device, so half of all tokens stands for the longest of several sequences.
 constexpr int kMinSegChunks = 4;
 void segments(int B, int64_t T, int64_t T_tot, bool has_cu, int H, int sms, int* nseg, int* seg_len) {

@@ -16,9 +16,9 @@
 //    bytes, so the K blocks of a tile are split over the CTAs of a cluster, which add their partial
 //    sums through distributed shared memory in a fixed order.
 //
-// Measured: 8192 x 12288 x 4096 344 us, 2.4 PFLOP/s (900-960 clocks a block of K, of which the MMAs need 524: 48 KB a
-// block into each SM bound it); 64 x 12288 x 4096 15.4 us, 3.4 TB/s of weight;
-// 16 x 12288 x 4096 12.6 us, 4.1 TB/s.
+// Measured: 8192 x 12288 x 4096 342 to 370 us from run to run, 2.2 to 2.4 PFLOP/s (900-960 clocks a block of K, of
+// which the MMAs need 524: 48 KB a block into each SM bound it); 64 x 12288 x 4096 15.4 us, 3.3 TB/s of weight;
+// 16 x 12288 x 4096 12.6 us, 4.0 TB/s.
 #include "kda_device.cuh"
 #include "kda_internal.h"
 #include "kda_tc_common.cuh"
