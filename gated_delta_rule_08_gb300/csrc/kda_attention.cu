@@ -1,0 +1,385 @@
+// Attention over a paged cache for few rows a key head: single tokens, and small trees of drafted tokens.
+//
+//   out_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r},  s_rj = scale q_r . k_j,  m_r = max_j s_rj
+//
+// One pass over the keys with a running m and sum per row.  The weights are kept relative to a reference that follows
+// the running maximum only when that passes it by 2^8, so that the sums are rarely rescaled: every weight is then
+// at most 2^8, and nothing is lost, since sums and weights are floating point.
+//
+// A CTA has 16 rows of a request and key head (the rows of an m16n8k16 MMA; both products are MMAs, the weights go
+// from one to the other in registers) and its four warps take boxes of 16 keys in turn.  Each warp copies its own
+// boxes with TMA into a ring of its own, so that nothing but the end joins the warps; 104 KB a CTA and two
+// CTAs an SM keep some 190 KB under way, which is what HBM's latency asks for.  Legacy MMAs are enough here:
+// a box takes about 120 instructions and 32 MMAs of a scheduler, and its 8 KB some 350 clocks of an SM's share of HBM.
+//
+// Few requests leave SMs idle, so up to 16 CTAs, a cluster, share a tile's boxes; they join through distributed
+// shared memory, each a part of the output, and no second launch or workspace is needed.
+#include "kda_attention.cuh"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kRows = 16, kBox = 16, kBoxShift = 4;
+constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
+constexpr float kSlack = 8.f;
+
+template <int D>
+struct Layout {
+  static constexpr int kParts = D / 64;                    // 128-byte pieces of a token
+  static constexpr uint32_t kPart = kBox * 128;            // a piece of all 16 tokens
+  static constexpr uint32_t kStage = 2 * kParts * kPart;   // K, then V
+  static constexpr uint32_t kRing = kStages * kStage;      // of a warp; at the end its sums [16][D] fp32
+  static constexpr uint32_t kOut = kWarps * kRing;         // the CTA's sums
+  static constexpr uint32_t kSums = kOut + kRows * D * 4;  // [kWarps + 1][16] references, and sums of weights
+  static constexpr uint32_t kBar = kSums + (kWarps + 1) * kRows * 8;
+  static constexpr uint32_t kSmem = kBar + kWarps * kStages * 8 + 16 + 1024;
+  static_assert(kRows * D * 4 <= kRing, "a warp's sums take its ring's place");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = aligned_smem(smem_raw);
+  float* refs = reinterpret_cast<float*>(sm + L::kSums);  // [kWarps + 1][16]
+  float* sums = refs + (kWarps + 1) * kRows;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kWarps * kStages);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+
+  if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
+    if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
+    return;
+  }
+  Walk walk;
+  Tile t;
+  // (the CTAs of a cluster have the same tile, so they leave together)
+  if (!locate(p, kRows, blockIdx.x / split, walk, t) || t.rows == 0) return;
+  const int token0 = t.first / p.G, token1 = (t.first + t.rows + p.G - 1) / p.G;
+  const Span span = span_of(p, t, token0, token1, kBoxShift);
+  const int box0 = (int)((int64_t)span.boxes * rank / split), box1 = (int)((int64_t)span.boxes * (rank + 1) / split);
+
+  if (tid == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full[i], 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+
+  // Q as the MMA's A operand: rows g and g + 8 of the lane's quad
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  const int row0 = g, row1 = g + 8;
+  const bool live0 = row0 < t.rows, live1 = row1 < t.rows;
+  const int tok0 = (t.first + (live0 ? row0 : 0)) / p.G, tok1 = (t.first + (live1 ? row1 : 0)) / p.G;
+  uint32_t Q[D / 16][4];
+  {
+    const int h0 = t.head * p.G + (t.first + (live0 ? row0 : 0)) % p.G, h1 = t.head * p.G + (t.first + (live1 ? row1 : 0)) % p.G;
+    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok0) * p.q_stride + (int64_t)h0 * D + c2);
+    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok1) * p.q_stride + (int64_t)h1 * D + c2);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      Q[i][0] = live0 ? q0[8 * i] : 0u;
+      Q[i][1] = live1 ? q1[8 * i] : 0u;
+      Q[i][2] = live0 ? q0[8 * i + 4] : 0u;
+      Q[i][3] = live1 ? q1[8 * i + 4] : 0u;
+    }
+  }
+  const Row keys0 = row_keys(p, t, tok0), keys1 = row_keys(p, t, tok1);
+
+  float O[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) O[i][j] = 0.f;
+  float m0 = kLowest, m1 = kLowest, l0 = 0.f, l1 = 0.f;
+
+  uint8_t* ring = sm + warp * L::kRing;
+  uint64_t* bars = full + warp * kStages;
+  const int count = box1 > box0 + warp ? (box1 - box0 - warp + kWarps - 1) / kWarps : 0;  // boxes of this warp
+  const int32_t* table = p.tables + (int64_t)t.n * p.max_blocks;
+  // the blocks of boxes [32 i, 32 i + 32) of this warp, one a lane
+  auto block_ids = [&](int i) {
+    const int at = 32 * i + lane;
+    int id = 0;
+    if (at < count) {
+      id = table[box_key(span, box0 + warp + at * kWarps, kBoxShift) >> p.shift];
+      if ((unsigned)id >= (unsigned)p.num_blocks) {
+        atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+        id = p.num_blocks;  // reads as zeros
+      }
+    }
+    return id;
+  };
+  int ids = block_ids(0), next_ids = block_ids(1), ids_of = 0;
+  const bool copies = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
+  int issued = 0;
+  auto issue = [&]() {
+    if (issued >> 5 != ids_of) {
+      ids = next_ids;
+      ++ids_of;
+      next_ids = block_ids(ids_of + 1);
+    }
+    const int block = __shfl_sync(0xffffffffu, ids, issued & 31), s = issued % kStages;
+    const int token = box_key(span, box0 + warp + issued * kWarps, kBoxShift) & ((1 << p.shift) - 1);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[s], L::kStage);
+      uint8_t* st = ring + s * L::kStage;
+#pragma unroll
+      for (int i = 0; i < L::kParts; ++i) {
+        tma_load_box(st + i * L::kPart, &maps.k, 64 * i, token, t.head, block, &bars[s]);
+        tma_load_box(st + (L::kParts + i) * L::kPart, &maps.v, 64 * i, token, t.head, block, &bars[s]);
+      }
+    }
+    __syncwarp();
+    ++issued;
+  };
+  if (copies) {
+#pragma unroll 1
+    while (issued < count && issued < kStages) issue();
+  }
+
+  const uint32_t key_row = (uint32_t)(((lane >> 4) << 3) + (lane & 7)), k_chunk = (uint32_t)(lane >> 3) & 1u;
+  const uint32_t val_row = (uint32_t)(lane & 15), v_chunk = (uint32_t)lane >> 4;
+  bool ok = true;
+#pragma unroll 1
+  for (int it = 0; it < count; ++it) {
+    const int s = it % kStages;
+    ok = p.waits == kWaitsGiveUp ? warp_wait<true>(&bars[s], 0, abort_flag)
+                                 : warp_wait<false>(&bars[s], (uint32_t)((it / kStages) & 1), abort_flag);
+    if (!ok) break;
+    uint8_t* st = ring + s * L::kStage;
+    const uint32_t sk = smem_u32(st), sv = sk + L::kParts * L::kPart;
+    const int base = box_key(span, box0 + warp + it * kWarps, kBoxShift);
+    const bool whole = all_seen(p, span, base, kBox);
+    if (!whole) {
+      // values that no row sees may be anything, and meet weights of 0 in the product: cleared
+      const uint32_t used = used16(p, span, base);
+      if (used != 0xffffu) {
+        for (int i = lane; i < kBox * 8 * L::kParts; i += 32) {
+          const int r = i & 15, j = i >> 4;
+          if (!(used >> r & 1))
+            *reinterpret_cast<uint4*>(st + (L::kParts + (j >> 3)) * L::kPart + row_chunk(r, j & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    }
+    float S[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t j = 2 * i + k_chunk;
+      uint32_t b[4];
+      ldsm4(sk + (j >> 3) * L::kPart + key_row * 128u + (((j & 7u) ^ (key_row & 7u)) << 4), b);
+      mma16816(S[0], Q[i], b[0], b[1]);
+      mma16816(S[1], Q[i], b[2], b[3]);
+    }
+    if (!whole) {
+      const uint32_t see0 = seen16(p, t, keys0, base) >> c2, see1 = seen16(p, t, keys1, base) >> c2;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (!(see0 >> (8 * n + j) & 1)) S[n][j] = -INFINITY;
+          if (!(see1 >> (8 * n + j) & 1)) S[n][2 + j] = -INFINITY;
+        }
+    }
+    const float top0 = fmaxf(fmaxf(S[0][0], S[0][1]), fmaxf(S[1][0], S[1][1])) * p.c;
+    const float top1 = fmaxf(fmaxf(S[0][2], S[0][3]), fmaxf(S[1][2], S[1][3])) * p.c;
+    if (__any_sync(0xffffffffu, top0 > m0 + kSlack || top1 > m1 + kSlack)) {
+      float n0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, 1)), n1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+      n0 = fmaxf(m0, fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, 2)));
+      n1 = fmaxf(m1, fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, 2)));
+      const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        O[i][0] *= f0;
+        O[i][1] *= f0;
+        O[i][2] *= f1;
+        O[i][3] *= f1;
+      }
+    }
+    uint32_t P[4];
+    float w[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[n][j] = ex2(fmaf(S[n][j], p.c, j < 2 ? -m0 : -m1));
+    l0 += (w[0][0] + w[0][1]) + (w[1][0] + w[1][1]);
+    l1 += (w[0][2] + w[0][3]) + (w[1][2] + w[1][3]);
+    // to bf16, what the tensor cores take: half a step, 2^-8 at most, of each weight, at random in a sum of many
+    P[0] = pack_bf2(w[0][0], w[0][1]);
+    P[1] = pack_bf2(w[0][2], w[0][3]);
+    P[2] = pack_bf2(w[1][0], w[1][1]);
+    P[3] = pack_bf2(w[1][2], w[1][3]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint32_t j = 2 * i + v_chunk;
+      uint32_t b[4];
+      ldsm4_t(sv + (j >> 3) * L::kPart + val_row * 128u + (((j & 7u) ^ (val_row & 7u)) << 4), b);
+      mma16816(O[2 * i], P, b[0], b[1]);
+      mma16816(O[2 * i + 1], P, b[2], b[3]);
+    }
+    __syncwarp();  // all lanes have read the stage
+    if (copies && issued < count) issue();
+  }
+  if (!ok) {  // copies that are still under way land before the memory is given back
+    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      if (lane == 0) mbar_wait(&bars[i % kStages], (uint32_t)((i / kStages) & 1));
+    if (lane == 0) atomicOr(p.err, KDA_DEVERR_WAIT_TIMEOUT);
+    __syncwarp();
+  }
+
+  // join: the warps' sums, then the CTAs'
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+  float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    *reinterpret_cast<float2*>(mine + row0 * D + 8 * i + c2) = make_float2(O[i][0], O[i][1]);
+    *reinterpret_cast<float2*>(mine + row1 * D + 8 * i + c2) = make_float2(O[i][2], O[i][3]);
+  }
+  if ((lane & 3) == 0) {
+    refs[warp * kRows + row0] = m0;
+    refs[warp * kRows + row1] = m1;
+    sums[warp * kRows + row0] = l0;
+    sums[warp * kRows + row1] = l1;
+  }
+  __syncthreads();
+  float* joined = reinterpret_cast<float*>(sm + L::kOut);
+  constexpr int kEach = kRows * D / kThreads;  // values a thread joins: a piece of one row
+  {
+    const int r = tid * kEach / D, x = tid * kEach % D;
+    float m = kLowest, l = 0.f, f[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, refs[i * kRows + r]);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      f[i] = ex2(refs[i * kRows + r] - m);
+      l += f[i] * sums[i * kRows + r];
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; j += 4) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i)
+        a = f4_fma(f[i], *reinterpret_cast<const float4*>(sm + i * L::kRing + (r * D + x + j) * 4), a);
+      *reinterpret_cast<float4*>(joined + r * D + x + j) = a;
+    }
+    if (x == 0) {
+      refs[kWarps * kRows + r] = m;
+      sums[kWarps * kRows + r] = l;
+    }
+  }
+  if (split > 1) cluster_sync(); else __syncthreads();
+  // each CTA of the cluster writes its part of the rows' pairs of values
+  bool gone = *abort_flag != 0;
+  if (split > 1)
+    for (int i = 0; i < split; ++i) gone |= __float_as_int(ld_peer(peer(const_cast<const int*>(abort_flag), i))) != 0;
+  if (!gone) {
+    const int pairs = kRows * D / 2 / split;
+    for (int i = tid; i < pairs; i += kThreads) {
+      const int at = rank * pairs + i, r = at / (D / 2), x = at % (D / 2) * 2;
+      if (r >= t.rows) break;
+      float a, b, l;
+      if (split == 1) {
+        a = joined[r * D + x];
+        b = joined[r * D + x + 1];
+        l = sums[kWarps * kRows + r];
+      } else {
+        float m = kLowest;
+        a = b = l = 0.f;
+        for (int k = 0; k < split; ++k) m = fmaxf(m, ld_peer(peer(refs + kWarps * kRows + r, k)));
+        for (int k = 0; k < split; ++k) {
+          const float f = ex2(ld_peer(peer(refs + kWarps * kRows + r, k)) - m);
+          l = fmaf(f, ld_peer(peer(sums + kWarps * kRows + r, k)), l);
+          a = fmaf(f, ld_peer(peer(joined + r * D + x, k)), a);
+          b = fmaf(f, ld_peer(peer(joined + r * D + x + 1, k)), b);
+        }
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
+      const int tok = (t.first + r) / p.G, h = t.head * p.G + (t.first + r) % p.G;
+      *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(t.t0 + tok) * p.H + h) * D + x) = pack_bf2(a * inv, b * inv);
+    }
+  }
+  if (split > 1) cluster_sync();  // no CTA leaves while another reads its memory
+}
+
+// CTAs that share a tile: as many as there are SMs for (two CTAs each), 16 at most, and no fewer than 256 keys each.
+int split_of(int64_t tiles, int64_t keys, int sms) {
+  int split = 1;
+  while (split < 16 && tiles * split * 2 <= 2 * sms && keys >= 512 * split) split *= 2;
+  return split;
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
+  Maps maps;
+  if (!tensor_map_cache(&maps.k, a.k_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, kBox) ||
+      !tensor_map_cache(&maps.v, a.v_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, kBox))
+    return cudaErrorInvalidValue;
+  static DeviceOnce once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  static int sms[kMaxDevices];
+  cudaError_t e = once.run(dev, [dev] {
+    cudaError_t f = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return f;
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = most_tiles(a, kRows) * a.Hkv;
+  p.split = split_of(tiles, most_keys(a, kRows), sms[dev]);
+  TraceScope ts("kda_attention_rows", st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_rows_kernel<D>, maps, p);
+}
+
+}  // namespace
+
+cudaError_t attention_rows_launch(const AttentionArgs& a, cudaStream_t st) {
+  return a.d == 64 ? launch<64>(a, params_of(a), st) : launch<128>(a, params_of(a), st);
+}
+
+}  // namespace kda

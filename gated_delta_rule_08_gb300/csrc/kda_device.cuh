@@ -11,6 +11,7 @@
 #define KDA_DEVERR_BAD_COUNT 0x8u
 #define KDA_DEVERR_NONFINITE 0x10u
 #define KDA_DEVERR_PRECONDITION 0x20u
+#define KDA_DEVERR_NO_BLOCKS 0x40u
 
 namespace kda {
 

@@ -255,6 +255,69 @@ struct MatmulArgs {
 };
 cudaError_t matmul_fp8_launch(const MatmulArgs& a, cudaStream_t stream);
 
+// ---- an attention layer over a paged cache (kda_attention_api.cu dispatches to them).  block_size is 1 << shift.
+
+constexpr int kMaxTableRequests = 8192;  // their sums lie in shared memory
+struct BlockTablesArgs {
+  const int32_t* counts;
+  const int32_t* lengths;
+  int32_t* block_tables;
+  int32_t* free_ring;
+  const int32_t* free_state;
+  int32_t* new_lengths;     // may be lengths
+  int32_t* new_free_state;  // may be free_state
+  int32_t* slot_map;
+  int32_t* positions;
+  int32_t* cu_seqlens;
+  int N, max_blocks, num_blocks, shift;
+  int64_t T;
+  unsigned int* err;
+};
+cudaError_t block_tables_launch(const BlockTablesArgs& a, cudaStream_t stream);
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const double* inv_freq;
+  const int32_t* axis;  // may be null (0)
+  const int32_t* positions;
+  const int32_t* slot_map;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  int64_t block_stride, token_stride, head_stride;  // of the caches, in elements
+  int64_t T;
+  int H, Hkv, d, rot, axes, num_blocks, shift;
+  bool adjacent;  // pairs 2 i, 2 i + 1 (else i, i + rot / 2)
+  bool bf16;
+  unsigned int* err;
+};
+cudaError_t rope_append_launch(const RopeArgs& a, cudaStream_t stream);
+
+struct AttentionArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int64_t block_stride, token_stride, head_stride;  // of the caches, in elements
+  const int32_t* block_tables;
+  const int32_t* lengths;
+  const int32_t* cu_seqlens;   // null: one token of each request
+  const uint64_t* tree_mask;   // null: causal
+  int mask_words;
+  void* out;
+  int N;
+  int64_t T;
+  int H, Hkv, d, num_blocks, shift, max_blocks, window, sinks;
+  int64_t max_length;          // > 0
+  float scale;
+  unsigned int* err;
+  int waits;  // test_wait_timeout()
+};
+cudaError_t attention_rows_launch(const AttentionArgs& a, cudaStream_t stream);  // few rows (kda_attention.cu)
+
 // Kernel tracing (kda_trace_enable): brackets internal launches with CUDA events.
 bool trace_enabled();
 void trace_begin(const char* name, cudaStream_t s);

@@ -36,4 +36,30 @@ bool tensor_map_2d(CUtensorMap* map, const void* base, CUtensorMapDataType type,
          CUDA_SUCCESS;
 }
 
+bool tensor_map_cache(CUtensorMap* map, const void* base, uint64_t blocks, uint64_t tokens, uint64_t heads, uint64_t d,
+                      uint64_t block_stride, uint64_t token_stride, uint64_t head_stride, uint32_t box_tokens) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {d, tokens, heads, blocks};
+  const cuuint64_t strides[3] = {token_stride * 2, head_stride * 2, block_stride * 2};
+  const cuuint32_t box[4] = {64, box_tokens, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tensor_map_rows(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t d,
+                     uint64_t token_stride, uint32_t box_tokens, uint32_t box_heads) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {d, heads, tokens};
+  const cuuint64_t strides[2] = {d * 2, token_stride * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_tokens};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace kda

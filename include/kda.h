@@ -76,12 +76,13 @@ typedef enum {
 } kda_dtype;
 
 /* Bits of the device error word. */
-#define KDA_DEVERR_BAD_SLOT     0x1u  /* decode: slot_idx[n] outside [0, num_slots)        */
+#define KDA_DEVERR_BAD_SLOT     0x1u  /* a slot index outside its pool, a block outside its cache */
 #define KDA_DEVERR_BAD_SEQLENS  0x2u  /* prefill: cu_seqlens not non-decreasing in [0, T]  */
 #define KDA_DEVERR_WAIT_TIMEOUT 0x4u  /* a bounded device-side wait gave up                */
-#define KDA_DEVERR_BAD_COUNT    0x8u  /* decode_multi: ntok_per_req[n] outside [0, n_tok]   */
+#define KDA_DEVERR_BAD_COUNT    0x8u  /* a number of tokens outside what its call allows     */
 #define KDA_DEVERR_NONFINITE   0x10u /* tensor-core path wrote a non-finite out / state value */
 #define KDA_DEVERR_PRECONDITION 0x20u /* KDA_DEBUG_CHECKS: g, beta or slot_idx broke a precondition */
+#define KDA_DEVERR_NO_BLOCKS   0x40u  /* block_tables: fewer free blocks than the new tokens need */
 
 /* Optional fused epilogue (section 3.3, Eq. 6): RMSNorm over dv per (token, head), then
  * the sigmoid output gate.  The norm is taken on the fp32 read-out before rounding.
@@ -312,6 +313,106 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, c
                                   float* state_pool, const int32_t* slot_idx, void* out, int N, int H, int dk,
                                   int dv, int num_slots, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                                   float scale, kda_dtype dtype, kda_dtype out_dtype, void* stream);
+
+/* ---- An attention layer over a paged cache (serving), as models mix it with recurrent layers.  The cache is a pool
+ * of blocks of block_size tokens (16, 32, 64, 128 or 256), for keys and for values:
+ *   k_cache, v_cache : [num_blocks, block_size, Hkv, d] bf16.  The d values of a head are dense; blocks, tokens and
+ *                      heads lie cache_strides[0], [1] and [2] elements apart (both caches alike; multiples of 8),
+ *                      so a layout [num_blocks, Hkv, block_size, d] is one of strides
+ *   block_tables     : [N, max_blocks] int32 device; token p of request n lies in block block_tables[n][p / block_size]
+ *   d in {64, 128};  H a multiple of Hkv, H / Hkv at most 128 (KDA_ERR_UNSUPPORTED otherwise).
+ * A step runs kda_block_tables (once for all layers), then in each layer kda_rope_append and one of the three
+ * attentions, whose `lengths` are kda_block_tables' new lengths. */
+
+/* Block tables, slots and positions of a step, from the tokens that each request gains or loses.
+ *   counts       : [N] int32, tokens that request n gains (>= 0), or the number of its last tokens that it gives up (< 0;
+ *                  a request ends by giving up all)
+ *   lengths      : [N] int32, tokens of each request before the step;  new_lengths: [N] int32, after it; may be lengths
+ *   block_tables : [N, max_blocks] int32, updated in place: entries of blocks that new tokens need are written, all
+ *                  others are left as they are (those of blocks given back too)
+ *   free_ring    : [num_blocks] int32, the free blocks as a ring: entries head, head + 1, .. (modulo num_blocks).  Blocks
+ *                  are taken at the head, in order of the requests, and given back behind the last, likewise
+ *   free_state   : [2] int32, head and number of free blocks;  new_free_state: the same after the step; may be free_state
+ *   slot_map     : [T] int32, slots (block * block_size + place in it) of the new tokens, packed in order of the requests;
+ *                  -1 behind the last
+ *   positions    : [T] int32, their positions in their requests; 0 behind the last
+ *   cu_seqlens   : [N + 1] int32, where each request's new tokens begin
+ * Blocks given back in a step are not taken in the same one.  If a request's tokens would fall below 0 or pass
+ * max_blocks * block_size, or all new tokens pass T, or a state is impossible (KDA_DEVERR_BAD_COUNT), or free blocks do not
+ * suffice (KDA_DEVERR_NO_BLOCKS), the step does nothing: tables, ring, lengths and state stay or are copied, the
+ * slots are all -1 and the offsets 0.  A block of the tables or the ring outside [0, num_blocks) sets
+ * KDA_DEVERR_BAD_SLOT; its tokens get the slot -1.
+ * N at most 8192, T at most 2^30; N * max_blocks and num_blocks * block_size below 2^31.  slot_map and positions
+ * 16-byte aligned, the others 4.  No two arrays overlap but those named. */
+kda_status kda_block_tables(const int32_t* counts, const int32_t* lengths, int32_t* block_tables, int32_t* free_ring,
+                            const int32_t* free_state, int32_t* new_lengths, int32_t* new_free_state,
+                            int32_t* slot_map, int32_t* positions, int32_t* cu_seqlens, int N, int max_blocks,
+                            int num_blocks, int block_size, int64_t T, void* stream);
+
+/* Rotary positions with one or several axes, and the cache's write.  For pair i of a head's first rot values
+ *   angle = positions[axis[i]][t] * inv_freq[i],  (a, b) -> (a cos - b sin, b cos + a sin)
+ * the pair being values i and i + rot / 2, or 2 i and 2 i + 1 if interleaved; values from rot on are left.  The
+ * angle is reduced exactly (in 64-bit fixed point), so positions may be as far as int32 goes, and negative.
+ *   q, k, v   : [T, H, d], [T, Hkv, d], [T, Hkv, d] (dtype), a token's heads dense, tokens q_stride / k_stride /
+ *               v_stride elements apart (as in kda_linear_chunk_fwd)
+ *   inv_freq  : [rot / 2] fp64, radians for each position;  axis: [rot / 2] int32 in [0, axes), or NULL (all 0)
+ *   positions : [axes, T] int32
+ *   slot_map  : [T] int32, as from kda_block_tables: token t's keys and values go to slot slot_map[t].  A token with -1 is
+ *               skipped whole (its row of q_out too); other slots outside the cache set KDA_DEVERR_BAD_SLOT and are
+ *               skipped, as are the tokens of an axis outside [0, axes).  The slots are distinct
+ *   q_out     : [T, H, d] bf16, dense;  computed in fp32 and rounded once, as what goes to the cache is
+ *   rot       : a multiple of 16, at most d;  axes 1 to 4
+ * q, k, v, the caches and q_out 16-byte aligned, inv_freq 8, the others 4.  Nothing written may overlap an input. */
+kda_status kda_rope_append(const void* q, const void* k, const void* v, const double* inv_freq, const int32_t* axis,
+                           const int32_t* positions, const int32_t* slot_map, void* q_out, void* k_cache, void* v_cache,
+                           int64_t T, int H, int Hkv, int d, int rot, int axes, int interleaved, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, int num_blocks, int block_size,
+                           const int64_t* cache_strides, kda_dtype dtype, void* stream);
+
+/* Attention with a sliding window and sinks, for new tokens whose keys and values are in the cache already.  The token at
+ * position p of its request sees the keys j <= p with j > p - window or j < sinks:
+ *   out = sum_j softmax_j(scale q . k_j) v_j        (head h reads the cache's head h / (H / Hkv))
+ *   q            : [T, H, d] bf16, a token's heads dense, tokens q_stride elements apart
+ *   lengths      : [N] int32, tokens of request n in the cache, its new ones included
+ *   cu_seqlens   : [N + 1] int32, where each request's new tokens begin in q; they are its last ones.  Offsets that do not
+ *                  rise from 0 to at most T set KDA_DEVERR_BAD_SEQLENS, and nothing is written; a request of more new
+ *                  tokens than its length, or longer than max_blocks * block_size, sets it and is skipped.  Rows of
+ *                  out behind the last request are left as they were
+ *   window       : tokens a token sees, itself included; 0 means all.  sinks >= 0: first tokens that stay visible
+ *   max_length   : no request is longer (a hint for how the work is split; 0: as long as the tables allow)
+ *   out          : [T, H, d] bf16, dense; must not overlap an input
+ * Keys and values of tokens that a row sees have to be finite.  What lies in the cache elsewhere may be anything, and
+ * table entries of blocks that no new token sees are not read.  A block that is, outside [0, num_blocks),
+ * sets KDA_DEVERR_BAD_SLOT; the rows of its request are then undefined (nothing outside the cache is read).
+ * Scores, softmax and sums are fp32; the weights are rounded to bf16 for their product with the values. */
+kda_status kda_window_attention_fwd(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                    const int32_t* lengths, const int32_t* cu_seqlens, void* out, int N, int64_t T,
+                                    int H, int Hkv, int d, int64_t q_stride, int num_blocks, int block_size,
+                                    int max_blocks, const int64_t* cache_strides, int window, int sinks,
+                                    int64_t max_length, float scale, void* stream);
+
+/* The same for one new token of each request: q, out [N, H, d], request n's token being its last (position
+ * lengths[n] - 1).  A request of length 0 gets zeros; one below 0 or longer than its table sets KDA_DEVERR_BAD_SEQLENS and
+ * is skipped. */
+kda_status kda_window_attention_decode_step(const void* q, const void* k_cache, const void* v_cache,
+                                            const int32_t* block_tables, const int32_t* lengths, void* out, int N, int H,
+                                            int Hkv, int d, int64_t q_stride, int num_blocks, int block_size,
+                                            int max_blocks, const int64_t* cache_strides, int window, int sinks,
+                                            int64_t max_length, float scale, void* stream);
+
+/* Attention of drafted tokens that form a tree, over the cache: the verify step that goes with kda_decode_multi's.
+ * A request's drafted tokens lie in the cache as its last cu_seqlens[n + 1] - cu_seqlens[n] ones, behind `before` others.
+ *   tree_mask : [T, mask_words] 64-bit words: bit j % 64 of word j / 64 says that the token sees drafted token j of its
+ *               request (its ancestors and itself; the mask alone decides); a request drafts at most 64 * mask_words
+ *               tokens (KDA_DEVERR_BAD_COUNT, and it is skipped).  Bits past a request's drafted tokens are ignored
+ * A token whose mask names m drafted tokens stands at position before + m - 1 and sees, of the tokens before the drafted
+ * ones, what kda_window_attention_fwd shows it there.  A token that sees nothing gets zeros.
+ * mask_words 1 to 16; tree_mask 8-byte aligned.  All else as for kda_window_attention_fwd. */
+kda_status kda_tree_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                              const int32_t* lengths, const int32_t* cu_seqlens, const uint64_t* tree_mask, int mask_words,
+                              void* out, int N, int64_t T, int H, int Hkv, int d, int64_t q_stride, int num_blocks,
+                              int block_size, int max_blocks, const int64_t* cache_strides, int window, int sinks,
+                              int64_t max_length, float scale, void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's error word into
  * *flags (KDA_DEVERR_* bits).  Returns KDA_OK, or KDA_ERR_CUDA if the sync failed. */
