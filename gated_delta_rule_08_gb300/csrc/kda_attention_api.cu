@@ -39,6 +39,9 @@ kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA
 
 bool heads_ok(int H, int Hkv) { return H % Hkv == 0 && H / Hkv <= 128; }
 
+// Rows of a key head and request, in the mean (their numbers are on the device), from which on tiles of 128 rows pay.
+bool many_rows(const AttentionArgs& a) { return a.T * (a.H / a.Hkv) > (int64_t)32 * a.N; }
+
 kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, void* stream) {
   if (a.N < 0 || a.T < 0 || a.H <= 0 || a.Hkv <= 0 || a.num_blocks < 0 || a.max_blocks < 0 || a.window < 0 || a.sinks < 0 ||
       a.max_length < 0 || !(a.scale > 0.f) || isinf(a.scale))
@@ -64,7 +67,8 @@ kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, vo
   if (a.max_length == 0 || a.max_length > longest) a.max_length = longest;
   a.block_stride = strides[0]; a.token_stride = strides[1]; a.head_stride = strides[2];
   a.waits = test_wait_timeout();
-  return done(attention_rows_launch(a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(many_rows(a) ? attention_tc_launch(a, s) : attention_rows_launch(a, s));
 }
 
 }  // namespace

@@ -1,0 +1,633 @@
+// Attention over a paged cache for many rows a key head, on the tcgen05 tensor cores: prompts, and trees of drafted
+// tokens of more rows than a warp MMA has.
+//
+// The mathematics is that of kda_attention.cu.  A work item is 256 rows of a request and key head, in two halves of 128
+// (an MMA's rows: TMEM lanes), of whole tokens each.  For every tile of 128 keys
+//   S_h [128 x 128] = Q_h K^T      Q, K in shared memory
+//   P_h             = weights of S_h, bf16, written over S_h in TMEM
+//   O_h [128 x d]  += P_h V        A operand P in TMEM, V as it lies in the cache (MN-major)
+// The halves alternate: while one's four softmax warps work, the tensor cores multiply for the other.  A thread
+// has a row of its own, so that maxima and sums need no exchange.  PV of a tile is issued before the next QK of
+// its half: one commit tells a softmax warp that its scores are there and that O is at rest, so that it may rescale O
+// itself in the rare case that a row's maximum has passed its reference by 2^8 (no warps of their own for that).
+//
+// Keys and values come by TMA, a box for each block of the cache (or 128 tokens of it), into one ring of tiles, K and V
+// in turn.  A tile is made of boxes, not of 128 consecutive keys: the sinks' boxes and the window's lie in it side by
+// side, which saves a tile for the sinks and most of one for a window that starts inside one.  Only tiles with a key
+// that some row does not see look at masks.  Values that no row sees may be anything (unwritten memory, NaN) and meet
+// weights of 0: a warp of its own clears them before such a tile is multiplied.
+//
+// Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 MMAs, 10 clears.  A CTA an SM walks over items (prompts, the
+// requests' last tiles first, which have the most keys); few items: a cluster of CTAs shares the keys of one and
+// joins through distributed shared memory.
+#include "kda_attention.cuh"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 384;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
+constexpr int kHalf = 128, kKeys = 128;
+constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
+constexpr float kSlack = 8.f;
+constexpr uint32_t kTmS = 0, kTmO = 256;      // TMEM columns: S (and P) of the halves, O of the halves
+
+template <int D>
+struct Layout {
+  static constexpr int kParts = D / 64;
+  static constexpr uint32_t kPart = kKeys * 128;             // 64 values of 128 rows
+  static constexpr uint32_t kTile = kParts * kPart;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
+  static constexpr uint32_t kBar = kRing + kStages * kTile;
+  static constexpr uint32_t kSmem = kBar + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+  static_assert((4 * kStages + 16) * 8 <= 512, "barriers");
+  static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
+};
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rd, ra, rb;\n"
+      " mov.b64 {%0, %1}, rd;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int x, int head, int token, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool hold(const Params& p, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return p.waits == kWaitsGiveUp ? warp_wait<true>(bar, parity, abort_flag) : warp_wait<false>(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool poll(const Params& p, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return p.waits == kWaitsGiveUp ? warp_spin<true>(bar, parity, abort_flag) : warp_spin<false>(bar, parity, abort_flag);
+}
+
+struct QMap {
+  CUtensorMap q;
+};
+
+// An item as every role sees it.
+struct Item {
+  Tile t;
+  Span span;       // of both halves: the boxes
+  int tile0, tile1;  // this CTA's tiles
+};
+
+// The first key of 16-key group g of tile j, or -1 past the last box.
+__device__ __forceinline__ int group_key(const Span& s, int j, int g, int box_shift) {
+  const int key = j * kKeys + g * 16, box = key >> box_shift;
+  return box < s.boxes ? box_key(s, box, box_shift) + (key & ((1 << box_shift) - 1)) : -1;
+}
+// Bit i: some row of `half` sees a key of group i of tile j; all rows see all of it; every key of it is one that some row
+// of the item sees (one warp together).
+struct Groups {
+  uint32_t some, all;
+};
+__device__ __forceinline__ Groups groups_of(const Params& p, const Span& boxes, const Span& half, int j, int box_shift) {
+  const int lane = threadIdx.x & 31;
+  bool some = false, all = false;
+  if (lane < 8) {
+    const int base = group_key(boxes, j, lane, box_shift);
+    if (base >= 0) {
+      some = used16(p, half, base) != 0;
+      all = all_seen(p, half, base, 16);
+    }
+  }
+  return {__ballot_sync(0xffffffffu, some), __ballot_sync(0xffffffffu, all)};
+}
+// Which groups of tile j hold keys that no row of the item sees (one warp together).
+__device__ __forceinline__ uint32_t unclean(const Params& p, const Span& s, int j, int box_shift) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  if (lane < 8) {
+    const int base = group_key(s, j, lane, box_shift);
+    bad = base < 0 || used16(p, s, base) != 0xffffu;
+  }
+  return __ballot_sync(0xffffffffu, bad);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = aligned_smem(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* q_full = empty + L::kStages;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;   // [2] scores there, O at rest
+  uint64_t* p_ready = q_full + 4;  // [2] weights written
+  uint64_t* o_done = q_full + 6;   // [2] the item's products complete, all tiles read
+  uint64_t* cleared = q_full + 8;  // a tile's values cleared
+  uint64_t* unclear = q_full + 9;  // ... have landed
+  uint64_t* bar_fin = q_full + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 11);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* refs = reinterpret_cast<float*>(sm);  // of 256 rows, in Q's place once the item's products are done (split)
+  float* sums = refs + 256;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+  const int G = p.G, span_tokens = kHalf / G, half_rows = span_tokens * G;  // of a half
+  if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
+    if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
+    return;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_full[h], 1);
+      mbar_init(&p_ready[h], 4);
+      mbar_init(&o_done[h], 1);
+    }
+    mbar_init(cleared, 1);
+    mbar_init(unclear, 1);
+    mbar_init(bar_fin, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Items of this CTA: every role walks them by itself.
+  Walk walk;
+  int64_t at = split > 1 ? blockIdx.x / split : blockIdx.x;
+  const int64_t step = split > 1 ? (int64_t)1 << 40 : gridDim.x;
+  auto next = [&](Item& it) {
+    while (true) {
+      if (!locate(p, 2 * half_rows, at, walk, it.t)) return false;
+      at += step;
+      if (it.t.rows > 0) break;
+    }
+    const int a = it.t.first / G;
+    it.span = span_of(p, it.t, a, a + it.t.rows / G, box_shift);
+    const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
+    it.tile0 = (int)((int64_t)tiles * rank / split);
+    it.tile1 = (int)((int64_t)tiles * (rank + 1) / split);
+    return true;
+  };
+  auto half_span = [&](const Item& it, int h) {
+    const int a = it.t.first / G + h * span_tokens, b = min(a + span_tokens, it.t.first / G + it.t.rows / G);
+    return span_of(p, it.t, a, b, box_shift);
+  };
+  bool ok = true;
+  int64_t issued = 0, q_issued = 0;  // copies started (copy warp)
+  Item it;
+
+  if (warp < 8) {
+    // ======================== softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int h = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t ts = tmem_lane(tmem, warp) + kTmS + 128 * h, to = tmem_lane(tmem, warp) + kTmO + 128 * h;
+    uint32_t seen = 0, items = 0;  // scores and items so far: the barriers' phases
+    while (ok && next(it)) {
+      const int rows = min(half_rows, it.t.rows - h * half_rows);
+      const bool live = row < rows;
+      const int r = it.t.first + h * half_rows + (live ? row : 0);  // in the request
+      float m = kLowest, l = 0.f;
+      bool any = false;
+      if (rows > 0) {
+        const Span span = half_span(it, h);
+        const Row keys = row_keys(p, it.t, r / G);
+#pragma unroll 1
+        for (int j = it.tile0; j < it.tile1; ++j) {
+          // tiles of consecutive keys that all rows see need no look at the groups
+          const int v0 = (j * kKeys) >> box_shift, v1 = ((j + 1) * kKeys) >> box_shift;
+          bool whole = v0 >= it.span.sink_boxes && v1 <= it.span.boxes && all_seen(p, span, box_key(it.span, v0, box_shift), kKeys);
+          if (!whole) {
+            const Groups g = groups_of(p, it.span, span, j, box_shift);
+            if (g.some == 0) continue;
+            whole = g.all == 0xffu;
+          }
+          ok = hold(p, &s_full[h], seen & 1, abort_flag);
+          if (!ok) break;
+          ++seen;
+          tc_fence_after();
+          float s[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_landed(s[i]);
+          if (!whole) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const int base = group_key(it.span, j, g, box_shift);
+              const uint32_t see = base < 0 ? 0u : seen16(p, it.t, keys, base);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!(see >> e & 1)) s[g / 2][g % 2 * 16 + e] = -INFINITY;
+            }
+          }
+          float top4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a = s[i][0], b = s[i][1];
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) {
+              a = fmaxf(a, s[i][e]);
+              b = fmaxf(b, s[i][e + 1]);
+            }
+            top4[i] = fmaxf(a, b);
+          }
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.c;
+          if (__any_sync(0xffffffffu, live && top > m + kSlack)) {
+            const float n = fmaxf(m, top), f = ex2(m - n);
+            m = n;
+            l *= f;
+            if (any) {
+#pragma unroll 1
+              for (int i = 0; i < D; i += 32) {
+                float o[32];
+                tmem_ld32(to + i, o);
+                tmem_landed(o);
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                tmem_st32u(to + i, w);
+              }
+            }
+          }
+          any = true;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(-m, -m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 x = fma2(make_float2(s[i][2 * e], s[i][2 * e + 1]), c2, m2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum[e & 1] = add2(sum[e & 1], x);
+              // to bf16, what the tensor cores take: half a step, 2^-8 at most, of each weight, at random in a sum of many
+              w[e] = pack_bf2(x.x, x.y);
+            }
+            tmem_st16u(ts + 16 * i, w);
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          l += both.x + both.y;
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&p_ready[h]);
+        }
+      }
+      if (!ok) break;
+      ok = hold(p, &o_done[h], items & 1, abort_flag);
+      if (!ok) break;
+      ++items;
+      tc_fence_after();
+      if (split > 1) {
+        // sums into the ring (all its tiles have been read), pieces of 16 bytes permuted by the row
+        const int rr = h * kHalf + row;
+        uint8_t* dst = sm + L::kRing + (uint32_t)rr * (D * 4);
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          if (any) {
+            tmem_ld32(to + i, o);
+            tmem_landed(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + (((i + e) / 4 ^ (rr & (D / 4 - 1))) << 4)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        refs[rr] = m;
+        sums[rr] = l;
+        break;  // one item
+      }
+      if (rows > 0) {
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
+        __nv_bfloat16* dst = p.out + ((int64_t)(it.t.t0 + r / G) * p.H + it.t.head * G + r % G) * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float o[32];
+          if (any) {
+            tmem_ld32(to + i, o);
+            tmem_landed(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + i + e) =
+                  make_uint4(pack_bf2(o[e] * inv, o[e + 1] * inv), pack_bf2(o[e + 2] * inv, o[e + 3] * inv),
+                             pack_bf2(o[e + 4] * inv, o[e + 5] * inv), pack_bf2(o[e + 6] * inv, o[e + 7] * inv));
+          }
+          __syncwarp();
+        }
+        tc_fence_before();  // O is read before the next item's weights are told
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kCopyWarp) {
+      // ======================== copies
+      while (ok && next(it)) {
+        const int halves = it.t.rows > half_rows ? 2 : 1;
+        if (q_issued > 0) ok = hold(p, q_empty, (uint32_t)((q_issued - 1) & 1), abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(halves * L::kParts * half_rows * 128));
+          for (int h = 0; h < halves; ++h)
+            for (int i = 0; i < L::kParts; ++i)
+              tma_load_rows(sm + h * L::kTile + i * L::kPart, &qmap.q, 64 * i, it.t.head * G,
+                            it.t.t0 + it.t.first / G + h * span_tokens, q_full);
+        }
+        __syncwarp();
+        ++q_issued;
+        const int32_t* table = p.tables + (int64_t)it.t.n * p.max_blocks;
+        const int per = kKeys >> box_shift;  // boxes of a tile, at most 8
+        // a lane has a box of four tiles at a time
+        auto block_ids = [&](int j) {
+          const int box = j * per + lane;
+          int id = 0;
+          if (lane < 4 * per && box < it.span.boxes && box < it.tile1 * per) {
+            id = table[box_key(it.span, box, box_shift) >> p.shift];
+            if ((unsigned)id >= (unsigned)p.num_blocks) {
+              atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+              id = p.num_blocks;  // reads as zeros
+            }
+          }
+          return id;
+        };
+        int ids = block_ids(it.tile0), next_ids = block_ids(it.tile0 + 4);
+#pragma unroll 1
+        for (int j = it.tile0; j < it.tile1 && ok; ++j) {
+          const int in4 = (j - it.tile0) & 3;
+          if (in4 == 0 && j > it.tile0) {
+            ids = next_ids;
+            next_ids = block_ids(j + 4);
+          }
+          const int mine = j * per + lane;  // box of this lane
+          const int block = __shfl_sync(0xffffffffu, ids, (in4 * per + lane) & 31);
+          const int boxes = min(per, it.span.boxes - j * per);
+          const int token = box_key(it.span, mine, box_shift) & ((1 << p.shift) - 1);
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const int s = (int)(issued % L::kStages);
+            if (issued >= L::kStages) ok = hold(p, &empty[s], (uint32_t)((issued / L::kStages - 1) & 1), abort_flag);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)boxes * (uint32_t)(L::kParts * 128) << box_shift);
+            __syncwarp();
+            if (lane < boxes) {
+              uint8_t* dst = sm + L::kRing + s * L::kTile + ((uint32_t)lane << box_shift) * 128u;
+#pragma unroll
+              for (int i = 0; i < L::kParts; ++i)
+                tma_load_box(dst + i * L::kPart, kv ? &maps.v : &maps.k, 64 * i, token, it.t.head, block, &full[s]);
+            }
+            __syncwarp();
+            ++issued;
+          }
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ======================== MMAs
+      const bool leader = lane == 0;
+      constexpr uint32_t id_s = idesc_bf16_f32(128, kKeys, false, false), id_o = idesc_bf16_f32(128, D, false, true);
+      const uint64_t d_q = smem_desc_sw128(smem_u32(sm), 16, 1024);
+      uint32_t used = 0, weights[2] = {0, 0}, clears = 0, q_used = 0;
+      const bool works = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
+      while (works && ok && next(it)) {
+        const int halves = it.t.rows > half_rows ? 2 : 1;
+        Span span[2];
+        span[0] = half_span(it, 0);
+        if (halves == 2) span[1] = half_span(it, 1); else span[1] = span[0];
+        ok = poll(p, q_full, q_used & 1, abort_flag);
+        if (!ok) break;
+        ++q_used;
+        bool pending[2] = {false, false}, begun[2] = {false, false}, clean = true;
+#pragma unroll 1
+        for (int j = it.tile0; j <= it.tile1 && ok; ++j) {
+          const bool more = j < it.tile1;
+          const int sk = (int)(used % L::kStages), sv = (int)((used - 1) % L::kStages);  // K of tile j, V of the one before
+          if (more) ok = poll(p, &full[sk], (used / L::kStages) & 1, abort_flag);
+          if (!ok) break;
+          const uint64_t d_k = smem_desc_sw128(smem_u32(sm + L::kRing + sk * L::kTile), 16, 1024);
+          const uint64_t d_v = smem_desc_sw128(smem_u32(sm + L::kRing + sv * L::kTile), L::kPart, 1024);
+          bool v_there = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h >= halves) continue;
+            if (pending[h]) {
+              if (!v_there) {
+                ok = clean ? poll(p, &full[sv], ((used - 1) / L::kStages) & 1, abort_flag) : poll(p, cleared, clears & 1, abort_flag);
+                v_there = true;
+              }
+              ok = ok && poll(p, &p_ready[h], weights[h] & 1, abort_flag);
+              if (!ok) break;
+              ++weights[h];
+              tc_fence_after();
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                mma_bf16_ts_by(leader, tmem + kTmO + 128 * h, tmem + kTmS + 128 * h + 8 * i, desc_add(d_v, i * 2048), id_o,
+                               begun[h] || i > 0);
+              begun[h] = true;
+              pending[h] = false;
+            }
+            if (more && groups_of(p, it.span, span[h], j, box_shift).some != 0) {
+              tc_fence_after();
+#pragma unroll
+              for (int b = 0; b < L::kParts; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  mma_bf16_ss_by(leader, tmem + kTmS + 128 * h, desc_add(d_q, h * L::kTile + b * L::kPart + i * 32),
+                                 desc_add(d_k, b * L::kPart + i * 32), id_s, b + i > 0);
+              mma_commit_by(leader, &s_full[h]);
+              pending[h] = true;
+            }
+          }
+          if (!ok) break;
+          if (j > it.tile0) {
+            if (!clean) {
+              if (!v_there) ok = poll(p, cleared, clears & 1, abort_flag);
+              if (!ok) break;
+              ++clears;
+            } else if (!v_there) {
+              ok = poll(p, &full[sv], ((used - 1) / L::kStages) & 1, abort_flag);
+            }
+            mma_commit_by(leader, &empty[sv]);
+          }
+          if (more) {
+            mma_commit_by(leader, &empty[sk]);
+            clean = unclean(p, it.span, j, box_shift) == 0;
+            if (!clean) {
+              ok = poll(p, &full[(used + 1) % L::kStages], ((used + 1) / L::kStages) & 1, abort_flag);
+              if (!ok) break;
+              warp_arrive(unclear);
+            }
+            used += 2;
+          }
+        }
+        if (!ok) break;
+        mma_commit_by(leader, q_empty);
+        mma_commit_by(leader, &o_done[0]);
+        mma_commit_by(leader, &o_done[1]);
+        if (split > 1) break;
+      }
+    } else if (warp == kClearWarp) {
+      // ======================== values that no row sees
+      // (told of a tile's arrival by the MMA warp, which follows the ring; a wait that skips phases would mistake them)
+      uint32_t used = 0, tiles = 0;
+      while (ok && next(it)) {
+#pragma unroll 1
+        for (int j = it.tile0; j < it.tile1 && ok; ++j, used += 2) {
+          const uint32_t bad = unclean(p, it.span, j, box_shift);
+          if (bad == 0) continue;
+          const int s = (int)((used + 1) % L::kStages);
+          ok = hold(p, unclear, tiles & 1, abort_flag);
+          if (!ok) break;
+          ++tiles;
+          uint8_t* st = sm + L::kRing + s * L::kTile;
+          for (int g = 0; g < 8; ++g) {
+            if (!(bad >> g & 1)) continue;
+            const int base = group_key(it.span, j, g, box_shift);
+            const uint32_t keep = base < 0 ? 0u : used16(p, it.span, base);
+            for (int i = lane; i < 16 * 8 * L::kParts; i += 32) {
+              const int r = i & 15, c = i >> 4;
+              if (!(keep >> r & 1))
+                *reinterpret_cast<uint4*>(st + (c >> 3) * L::kPart + row_chunk(16 * g + r, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+          warp_arrive(cleared);
+        }
+        if (split > 1) break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // copies and MMAs that may still be under way are waited for, with a limit
+    if (tid == kCopyWarp * 32) {
+      if (q_issued > 0) mbar_wait(q_full, (uint32_t)((q_issued - 1) & 1));
+      for (int64_t i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
+        mbar_wait(&full[i % L::kStages], (uint32_t)((i / L::kStages) & 1));
+      atomicOr(p.err, KDA_DEVERR_WAIT_TIMEOUT);
+    }
+    if (tid == kMmaWarp * 32) {
+      mma_commit(bar_fin);
+      mbar_wait(bar_fin, 0);
+    }
+    __syncthreads();
+  }
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (split == 1) return;
+
+  // the cluster's CTAs join: each a part of the rows
+  cluster_sync();
+  bool gone = false;
+  for (int i = 0; i < split; ++i) gone |= __float_as_int(ld_peer(peer(const_cast<const int*>(abort_flag), i))) != 0;
+  walk = Walk{};
+  at = blockIdx.x / split;
+  if (!gone && next(it)) {
+    constexpr int kPieces = D / 8;  // a thread's eight values
+    const int each = 256 / split;
+    for (int i = tid; i < each * kPieces; i += kThreads) {
+      const int rr = rank * each + i / kPieces, x = i % kPieces * 8;
+      const int h = rr / kHalf, row = rr % kHalf, q = h * half_rows + row;
+      if (row >= half_rows || q >= it.t.rows) continue;
+      float m = kLowest, l = 0.f;
+      for (int k = 0; k < split; ++k) m = fmaxf(m, ld_peer(peer(refs + rr, k)));
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      const uint8_t* src = sm + L::kRing + (uint32_t)rr * (D * 4);
+      for (int k = 0; k < split; ++k) {
+        const float f = ex2(ld_peer(peer(refs + rr, k)) - m);
+        l = fmaf(f, ld_peer(peer(sums + rr, k)), l);
+        a = f4_fma(f, ld_peer4(peer(src + ((x / 4 ^ (rr & (D / 4 - 1))) << 4), k)), a);
+        b = f4_fma(f, ld_peer4(peer(src + (((x / 4 + 1) ^ (rr & (D / 4 - 1))) << 4), k)), b);
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int r = it.t.first + q;
+      *reinterpret_cast<uint4*>(p.out + ((int64_t)(it.t.t0 + r / G) * p.H + it.t.head * G + r % G) * D + x) =
+          make_uint4(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv), pack_bf2(b.x * inv, b.y * inv),
+                     pack_bf2(b.z * inv, b.w * inv));
+    }
+  }
+  cluster_sync();  // no CTA leaves while another reads its memory
+}
+
+// CTAs that share an item's keys: as many as there are SMs for, 16 at most, and no fewer than four tiles each.
+int split_of(int64_t items, int64_t keys, int sms) {
+  int split = 1;
+  while (split < 16 && items * split * 2 <= sms && keys >= (int64_t)split * 2 * 4 * kKeys) split *= 2;
+  return split;
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
+  static DeviceOnce once;
+  static int sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const cudaError_t e = once.run(dev, [dev] {
+    cudaError_t f = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return f;
+  });
+  if (e != cudaSuccess) return e;
+  const int box_shift = a.shift < 7 ? a.shift : 7, tokens = kHalf / p.G;
+  Maps maps;
+  QMap qmap;
+  if (!tensor_map_cache(&maps.k, a.k_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, 1u << box_shift) ||
+      !tensor_map_cache(&maps.v, a.v_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, 1u << box_shift) ||
+      !tensor_map_rows(&qmap.q, a.q, a.T, a.H, D, a.q_stride, (uint32_t)tokens, (uint32_t)p.G))
+    return cudaErrorInvalidValue;
+  const int64_t items = most_tiles(a, 2 * tokens * p.G) * a.Hkv;
+  p.split = split_of(items, most_keys(a, 2 * tokens), sms[dev]);
+  TraceScope ts("kda_attention_tc", st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.split > 1 ? items * p.split : items < sms[dev] ? items : sms[dev]));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<D>, maps, qmap, p, box_shift);
+}
+
+}  // namespace
+
+cudaError_t attention_tc_launch(const AttentionArgs& a, cudaStream_t st) {
+  return a.d == 64 ? launch<64>(a, params_of(a), st) : launch<128>(a, params_of(a), st);
+}
+
+}  // namespace kda

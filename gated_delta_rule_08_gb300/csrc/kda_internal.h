@@ -317,6 +317,7 @@ struct AttentionArgs {
   int waits;  // test_wait_timeout()
 };
 cudaError_t attention_rows_launch(const AttentionArgs& a, cudaStream_t stream);  // few rows (kda_attention.cu)
+cudaError_t attention_tc_launch(const AttentionArgs& a, cudaStream_t stream);    // many rows (kda_attention_tc.cu)
 
 // Kernel tracing (kda_trace_enable): brackets internal launches with CUDA events.
 bool trace_enabled();
