@@ -17,7 +17,7 @@
 // that some row does not see look at masks.  Values that no row sees may be anything (unwritten memory, NaN) and meet
 // weights of 0: a warp of its own clears them before such a tile is multiplied.
 //
-// Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 MMAs, 10 clears.  A CTA an SM walks over items (prompts, the
+// Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 and 10 the halves' MMAs, 11 clears.  A CTA an SM walks over items (prompts, the
 // requests' last tiles first, which have the most keys); few items: a cluster of CTAs shares the keys of one and
 // joins through distributed shared memory.
 #include "kda_attention.cuh"
@@ -28,7 +28,7 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 384;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 11;  // (MMAs: two warps)
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr int kHalf = 128, kKeys = 128;
@@ -46,7 +46,7 @@ struct Layout {
   static constexpr uint32_t kBar = kRing + kStages * kTile;
   static constexpr uint32_t kSmem = kBar + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
-  static_assert((4 * kStages + 16) * 8 <= 512, "barriers");
+  static_assert((2 * kStages + 20) * 8 <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
 };
 
@@ -70,12 +70,39 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t a) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ bool hold(const Params& p, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return p.waits == kWaitsGiveUp ? warp_wait<true>(bar, parity, abort_flag) : warp_wait<false>(bar, parity, abort_flag);
-}
-__device__ __forceinline__ bool poll(const Params& p, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return p.waits == kWaitsGiveUp ? warp_spin<true>(bar, parity, abort_flag) : warp_spin<false>(bar, parity, abort_flag);
-}
+// Waits of a whole warp (branches are on votes, so that it stays together), with a limit of about a second, or none at
+// all in the variant that gives up.  hold() leaves the waiting to the hardware; poll() is for the MMA warp, which all
+// others wait for (a suspended warp comes back some hundreds of clocks late).  Both are kept small: they are inlined many
+// times, and the warps' loops share an instruction cache.
+struct Waiter {
+  volatile int* abort_flag;
+  bool give_up;
+  __device__ __forceinline__ bool hold(uint64_t* bar, uint32_t parity) const {
+    const uint32_t tries = give_up ? 0u : kPausedTries;
+#pragma unroll 1
+    for (uint32_t i = 0; i < tries; ++i) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+      pause_after(i);
+    }
+    *abort_flag = 1;
+    return false;
+  }
+  __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) const {
+    const uint32_t tries = give_up ? 0u : kPolls;
+#pragma unroll 1
+    for (uint32_t i = 0; i < tries; ++i) {
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+      if (i >= kQuickPolls) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+        __nanosleep(1000);
+      }
+    }
+    *abort_flag = 1;
+    return false;
+  }
+  static constexpr uint32_t kQuickPolls = 16384, kPolls = kQuickPolls + 700000;
+};
 
 struct QMap {
   CUtensorMap q;
@@ -121,6 +148,22 @@ __device__ __forceinline__ uint32_t unclean(const Params& p, const Span& s, int 
   return __ballot_sync(0xffffffffu, bad);
 }
 
+// The tiles, if any, that hold 128 consecutive keys of which every row of the span sees all.
+struct Plain {
+  int first, end;
+};
+__device__ __forceinline__ Plain plain_tiles(const Span& boxes, const Span& rows, int box_shift) {
+  // tile j's first key, from the first after the sinks' boxes on
+  const int64_t shift = ((int64_t)boxes.first_box - boxes.sink_boxes) << box_shift;
+  int64_t first = (((int64_t)boxes.sink_boxes << box_shift) + kKeys - 1) / kKeys;
+  const int64_t seen = (rows.all_lo - shift + kKeys - 1) / kKeys;
+  if (seen > first) first = seen;
+  const int64_t end = ((int64_t)rows.all_hi + 1 - shift) / kKeys;
+  return {(int)first, (int)(end > first ? end : first)};
+}
+// a value that is the same in all lanes, as one that the compiler knows to be
+__device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
@@ -132,12 +175,13 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   uint64_t* q_full = empty + L::kStages;
   uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_full + 2;   // [2] scores there, O at rest
-  uint64_t* p_ready = q_full + 4;  // [2] weights written
-  uint64_t* o_done = q_full + 6;   // [2] the item's products complete, all tiles read
+  uint64_t* p_ready = q_full + 14;  // [2][2] weights of half the keys written
+  uint64_t* o_done = q_full + 6;   // [2] the item's products complete (split: both halves')
   uint64_t* cleared = q_full + 8;  // a tile's values cleared
   uint64_t* unclear = q_full + 9;  // ... have landed
-  uint64_t* bar_fin = q_full + 10;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 11);
+  uint64_t* turn = q_full + 10;    // [2] the half's turn at the tensor cores
+  uint64_t* bar_fin = q_full + 12;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* refs = reinterpret_cast<float*>(sm);  // of 256 rows, in Q's place once the item's products are done (split)
   float* sums = refs + 256;
@@ -156,18 +200,20 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&s_full[h], 1);
-      mbar_init(&p_ready[h], 4);
-      mbar_init(&o_done[h], 1);
+      mbar_init(&p_ready[2 * h], 4);
+      mbar_init(&p_ready[2 * h + 1], 4);
+      mbar_init(&turn[h], 1);
+      mbar_init(&o_done[h], split > 1 ? 2 : 1);
     }
     mbar_init(cleared, 1);
     mbar_init(unclear, 1);
-    mbar_init(bar_fin, 1);
+    mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -197,6 +243,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     const int a = it.t.first / G + h * span_tokens, b = min(a + span_tokens, it.t.first / G + it.t.rows / G);
     return span_of(p, it.t, a, b, box_shift);
   };
+  const Waiter w{abort_flag, p.waits == kWaitsGiveUp};
   bool ok = true;
   int64_t issued = 0, q_issued = 0;  // copies started (copy warp)
   Item it;
@@ -216,47 +263,52 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       if (rows > 0) {
         const Span span = half_span(it, h);
         const Row keys = row_keys(p, it.t, r / G);
+        const Plain plain = plain_tiles(it.span, span, box_shift);
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1; ++j) {
-          // tiles of consecutive keys that all rows see need no look at the groups
-          const int v0 = (j * kKeys) >> box_shift, v1 = ((j + 1) * kKeys) >> box_shift;
-          bool whole = v0 >= it.span.sink_boxes && v1 <= it.span.boxes && all_seen(p, span, box_key(it.span, v0, box_shift), kKeys);
+          bool whole = j >= plain.first && j < plain.end;
           if (!whole) {
             const Groups g = groups_of(p, it.span, span, j, box_shift);
             if (g.some == 0) continue;
             whole = g.all == 0xffu;
           }
-          ok = hold(p, &s_full[h], seen & 1, abort_flag);
+          ok = w.hold(&s_full[h], seen & 1);
           if (!ok) break;
           ++seen;
           tc_fence_after();
+          if (!whole) {  // what the row does not see, out of S
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              uint32_t see = 0;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const int base = group_key(it.span, j, 2 * i + g, box_shift);
+                if (base >= 0) see |= seen16(p, it.t, keys, base) << (16 * g);
+              }
+              float s[32];
+              tmem_ld32(ts + 32 * i, s);
+              tmem_landed(s);
+              uint32_t u[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? __float_as_uint(s[e]) : 0xff800000u;  // -infinity
+              tmem_st32u(ts + 32 * i, u);
+            }
+            tmem_wait_st();
+          }
           float s[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_landed(s[i]);
-          if (!whole) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const int base = group_key(it.span, j, g, box_shift);
-              const uint32_t see = base < 0 ? 0u : seen16(p, it.t, keys, base);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!(see >> e & 1)) s[g / 2][g % 2 * 16 + e] = -INFINITY;
-            }
-          }
-          float top4[4];
+          float t[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float a = s[i][0], b = s[i][1];
+            t[i] = s[i][0];
 #pragma unroll
-            for (int e = 2; e < 32; e += 2) {
-              a = fmaxf(a, s[i][e]);
-              b = fmaxf(b, s[i][e + 1]);
-            }
-            top4[i] = fmaxf(a, b);
+            for (int e = 1; e < 31; e += 2) t[i] = fmaxf(t[i], fmaxf(s[i][e], s[i][e + 1]));
+            t[i] = fmaxf(t[i], s[i][31]);
           }
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * p.c;
+          const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.c;
           if (__any_sync(0xffffffffu, live && top > m + kSlack)) {
             const float n = fmaxf(m, top), f = ex2(m - n);
             m = n;
@@ -267,10 +319,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
                 float o[32];
                 tmem_ld32(to + i, o);
                 tmem_landed(o);
-                uint32_t w[32];
+                uint32_t u[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-                tmem_st32u(to + i, w);
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                tmem_st32u(to + i, u);
               }
             }
           }
@@ -279,7 +331,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           const float2 c2 = make_float2(p.c, p.c), m2 = make_float2(-m, -m);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t w[16];
+            uint32_t u[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 x = fma2(make_float2(s[i][2 * e], s[i][2 * e + 1]), c2, m2);
@@ -287,19 +339,24 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
               x.y = ex2(x.y);
               sum[e & 1] = add2(sum[e & 1], x);
               // to bf16, what the tensor cores take: half a step, 2^-8 at most, of each weight, at random in a sum of many
-              w[e] = pack_bf2(x.x, x.y);
+              u[e] = pack_bf2(x.x, x.y);
             }
-            tmem_st16u(ts + 16 * i, w);
+            tmem_st16u(ts + 16 * i, u);
+            if (i == 1) {  // the first half of the keys can be multiplied
+              tmem_wait_st();
+              tc_fence_before();
+              warp_arrive(&p_ready[2 * h]);
+            }
           }
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
           tmem_wait_st();
           tc_fence_before();
-          warp_arrive(&p_ready[h]);
+          warp_arrive(&p_ready[2 * h + 1]);
         }
       }
       if (!ok) break;
-      ok = hold(p, &o_done[h], items & 1, abort_flag);
+      ok = w.hold(&o_done[h], items & 1);
       if (!ok) break;
       ++items;
       tc_fence_after();
@@ -356,7 +413,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       // ======================== copies
       while (ok && next(it)) {
         const int halves = it.t.rows > half_rows ? 2 : 1;
-        if (q_issued > 0) ok = hold(p, q_empty, (uint32_t)((q_issued - 1) & 1), abort_flag);
+        if (q_issued > 0) ok = w.hold(q_empty, (uint32_t)((q_issued - 1) & 1));
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full, (uint32_t)(halves * L::kParts * half_rows * 128));
@@ -397,7 +454,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             const int s = (int)(issued % L::kStages);
-            if (issued >= L::kStages) ok = hold(p, &empty[s], (uint32_t)((issued / L::kStages - 1) & 1), abort_flag);
+            if (issued >= L::kStages) ok = w.hold(&empty[s], (uint32_t)((issued / L::kStages - 1) & 1));
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)boxes * (uint32_t)(L::kParts * 128) << box_shift);
             __syncwarp();
@@ -412,89 +469,114 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           }
         }
       }
-    } else if (warp == kMmaWarp) {
-      // ======================== MMAs
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      // ======================== MMAs, a warp for each half
+      // What the loops go by passes through votes and reductions, which the compiler knows to be the same in all lanes:
+      // descriptors are then formed in uniform registers (from vector registers an MMA takes 100 clocks to issue).
       const bool leader = lane == 0;
+      const int h = warp == kMmaWarp ? 0 : 1;
       constexpr uint32_t id_s = idesc_bf16_f32(128, kKeys, false, false), id_o = idesc_bf16_f32(128, D, false, true);
-      const uint64_t d_q = smem_desc_sw128(smem_u32(sm), 16, 1024);
-      uint32_t used = 0, weights[2] = {0, 0}, clears = 0, q_used = 0;
+      const uint64_t d_q = smem_desc_sw128(smem_u32(sm + h * L::kTile), 16, 1024);
+      const uint64_t d_k = smem_desc_sw128(smem_u32(sm + L::kRing), 16, 1024);
+      const uint64_t d_v = smem_desc_sw128(smem_u32(sm + L::kRing), L::kPart, 1024);
+      const uint32_t t_s = tmem + kTmS + 128 * h, t_o = tmem + kTmO + 128 * h;
       const bool works = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
-      while (works && ok && next(it)) {
-        const int halves = it.t.rows > half_rows ? 2 : 1;
-        Span span[2];
-        span[0] = half_span(it, 0);
-        if (halves == 2) span[1] = half_span(it, 1); else span[1] = span[0];
-        ok = poll(p, q_full, q_used & 1, abort_flag);
-        if (!ok) break;
-        ++q_used;
-        bool pending[2] = {false, false}, begun[2] = {false, false}, clean = true;
+      int stage = 0;  // of the next tile in the ring, and its phase
+      uint32_t phase = 0, weights = 0, clears = 0, q_used = 0, turns = h ^ 1;  // (half 0 has the first turn)
+      while (works && ok && __any_sync(0xffffffffu, next(it))) {
+        const int tile0 = same(it.tile0), tile1 = same(it.tile1);
+        const bool rows = same(it.t.rows) > h * half_rows;
+        const Plain plain = plain_tiles(it.span, it.span, box_shift);
+        const int plain0 = same(plain.first), plain1 = same(plain.end);
+        const Span span = rows ? half_span(it, h) : it.span;
+        ok = w.poll(q_full, q_used & 1);
+        q_used ^= 1;
+        bool pending = false, begun = false, clean = true;  // weights to come, O begun, V as it came
+        int v_stage = 0;
+        uint32_t v_phase = 0;
 #pragma unroll 1
-        for (int j = it.tile0; j <= it.tile1 && ok; ++j) {
-          const bool more = j < it.tile1;
-          const int sk = (int)(used % L::kStages), sv = (int)((used - 1) % L::kStages);  // K of tile j, V of the one before
-          if (more) ok = poll(p, &full[sk], (used / L::kStages) & 1, abort_flag);
+        for (int j = tile0; j <= tile1; ++j) {
           if (!ok) break;
-          const uint64_t d_k = smem_desc_sw128(smem_u32(sm + L::kRing + sk * L::kTile), 16, 1024);
-          const uint64_t d_v = smem_desc_sw128(smem_u32(sm + L::kRing + sv * L::kTile), L::kPart, 1024);
-          bool v_there = false;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h >= halves) continue;
-            if (pending[h]) {
-              if (!v_there) {
-                ok = clean ? poll(p, &full[sv], ((used - 1) / L::kStages) & 1, abort_flag) : poll(p, cleared, clears & 1, abort_flag);
-                v_there = true;
-              }
-              ok = ok && poll(p, &p_ready[h], weights[h] & 1, abort_flag);
-              if (!ok) break;
-              ++weights[h];
-              tc_fence_after();
-#pragma unroll
-              for (int i = 0; i < kKeys / 16; ++i)
-                mma_bf16_ts_by(leader, tmem + kTmO + 128 * h, tmem + kTmS + 128 * h + 8 * i, desc_add(d_v, i * 2048), id_o,
-                               begun[h] || i > 0);
-              begun[h] = true;
-              pending[h] = false;
-            }
-            if (more && groups_of(p, it.span, span[h], j, box_shift).some != 0) {
-              tc_fence_after();
-#pragma unroll
-              for (int b = 0; b < L::kParts; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  mma_bf16_ss_by(leader, tmem + kTmS + 128 * h, desc_add(d_q, h * L::kTile + b * L::kPart + i * 32),
-                                 desc_add(d_k, b * L::kPart + i * 32), id_s, b + i > 0);
-              mma_commit_by(leader, &s_full[h]);
-              pending[h] = true;
-            }
-          }
-          if (!ok) break;
-          if (j > it.tile0) {
-            if (!clean) {
-              if (!v_there) ok = poll(p, cleared, clears & 1, abort_flag);
-              if (!ok) break;
-              ++clears;
-            } else if (!v_there) {
-              ok = poll(p, &full[sv], ((used - 1) / L::kStages) & 1, abort_flag);
-            }
-            mma_commit_by(leader, &empty[sv]);
-          }
+          const bool more = j < tile1;
+          bool active = false, next_clean = true;
           if (more) {
-            mma_commit_by(leader, &empty[sk]);
-            clean = unclean(p, it.span, j, box_shift) == 0;
-            if (!clean) {
-              ok = poll(p, &full[(used + 1) % L::kStages], ((used + 1) / L::kStages) & 1, abort_flag);
+            active = rows;
+            if (j < plain0 || j >= plain1) {
+              active = rows && groups_of(p, it.span, span, j, box_shift).some != 0;
+              next_clean = unclean(p, it.span, j, box_shift) == 0;
+            }
+            ok = w.poll(&full[stage], phase);
+            if (!ok) break;
+          }
+          if (j > tile0) {
+            ok = clean ? w.poll(&full[v_stage], v_phase) : w.poll(cleared, clears);
+            if (!ok) break;
+            clears ^= clean ? 0 : 1;
+          }
+          ok = w.poll(&turn[h], turns);
+          if (!ok) break;
+          turns ^= 1;
+          if (pending) {
+            const uint64_t at = desc_add(d_v, v_stage * L::kTile);
+            ok = w.poll(&p_ready[2 * h], weights);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < kKeys / 32; ++i)
+              mma_bf16_ts_by(leader, t_o, t_s + 8 * i, desc_add(at, i * 2048), id_o, i > 0 || begun);
+            ok = w.poll(&p_ready[2 * h + 1], weights);
+            if (!ok) break;
+            weights ^= 1;
+            tc_fence_after();
+#pragma unroll
+            for (int i = kKeys / 32; i < kKeys / 16; ++i)
+              mma_bf16_ts_by(leader, t_o, t_s + 8 * i, desc_add(at, i * 2048), id_o, true);
+            begun = true;
+          }
+          const uint64_t at = desc_add(d_k, stage * L::kTile);
+          if (active) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              mma_bf16_ss_by(leader, t_s, desc_add(d_q, (i >> 2) * L::kPart + (i & 3) * 32),
+                             desc_add(at, (i >> 2) * L::kPart + (i & 3) * 32), id_s, i > 0);
+          }
+          warp_arrive(&turn[h ^ 1]);  // with MMAs still to issue: the turn takes some 200 clocks to pass
+          if (active) {
+#pragma unroll
+            for (int i = D / 32; i < D / 16; ++i)
+              mma_bf16_ss_by(leader, t_s, desc_add(d_q, (i >> 2) * L::kPart + (i & 3) * 32),
+                             desc_add(at, (i >> 2) * L::kPart + (i & 3) * 32), id_s, true);
+            mma_commit_by(leader, &s_full[h]);
+          }
+          if (j > tile0) mma_commit_by(leader, &empty[v_stage]);
+          pending = active;
+          clean = next_clean;
+          if (more) {
+            mma_commit_by(leader, &empty[stage]);
+            if (++stage == L::kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+            v_stage = stage;
+            v_phase = phase;
+            if (++stage == L::kStages) {
+              stage = 0;
+              phase ^= 1;
+            }
+            if (!clean && h == 0) {
+              ok = w.poll(&full[v_stage], v_phase);
               if (!ok) break;
               warp_arrive(unclear);
             }
-            used += 2;
           }
         }
         if (!ok) break;
         mma_commit_by(leader, q_empty);
-        mma_commit_by(leader, &o_done[0]);
-        mma_commit_by(leader, &o_done[1]);
-        if (split > 1) break;
+        mma_commit_by(leader, &o_done[h]);
+        if (split > 1) {
+          mma_commit_by(leader, &o_done[h ^ 1]);
+          break;
+        }
       }
     } else if (warp == kClearWarp) {
       // ======================== values that no row sees
@@ -506,7 +588,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           const uint32_t bad = unclean(p, it.span, j, box_shift);
           if (bad == 0) continue;
           const int s = (int)((used + 1) % L::kStages);
-          ok = hold(p, unclear, tiles & 1, abort_flag);
+          ok = w.hold(unclear, tiles & 1);
           if (!ok) break;
           ++tiles;
           uint8_t* st = sm + L::kRing + s * L::kTile;
@@ -537,7 +619,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         mbar_wait(&full[i % L::kStages], (uint32_t)((i / L::kStages) & 1));
       atomicOr(p.err, KDA_DEVERR_WAIT_TIMEOUT);
     }
-    if (tid == kMmaWarp * 32) {
+    if (tid == kMmaWarp * 32 || tid == (kMmaWarp + 1) * 32) {
       mma_commit(bar_fin);
       mbar_wait(bar_fin, 0);
     }
