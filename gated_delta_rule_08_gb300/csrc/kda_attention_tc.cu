@@ -534,18 +534,12 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
             begun = true;
           }
           const uint64_t at = desc_add(d_k, stage * L::kTile);
+          warp_arrive(&turn[h ^ 1]);  // with MMAs still to issue: the turn takes some 500 clocks to pass
           if (active) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
+            for (int i = 0; i < D / 16; ++i)
               mma_bf16_ss_by(leader, t_s, desc_add(d_q, (i >> 2) * L::kPart + (i & 3) * 32),
                              desc_add(at, (i >> 2) * L::kPart + (i & 3) * 32), id_s, i > 0);
-          }
-          warp_arrive(&turn[h ^ 1]);  // with MMAs still to issue: the turn takes some 200 clocks to pass
-          if (active) {
-#pragma unroll
-            for (int i = D / 32; i < D / 16; ++i)
-              mma_bf16_ss_by(leader, t_s, desc_add(d_q, (i >> 2) * L::kPart + (i & 3) * 32),
-                             desc_add(at, (i >> 2) * L::kPart + (i & 3) * 32), id_s, true);
             mma_commit_by(leader, &s_full[h]);
           }
           if (j > tile0) mma_commit_by(leader, &empty[v_stage]);
