@@ -79,8 +79,8 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   Walk walk;
   Tile t;
   // (the CTAs of a cluster have the same tile, so they leave together)
-  if (!locate(p, kRows, blockIdx.x / split, walk, t) || t.rows == 0) return;
-  const int token0 = t.first / p.G, token1 = (t.first + t.rows + p.G - 1) / p.G;
+  if (!locate(p, kRows, Divisor{1, 4, kRows}, blockIdx.x / split, walk, t) || t.rows == 0) return;
+  const int token0 = p.by_G.div(t.first), token1 = p.by_G.div(t.first + t.rows + p.G - 1);
   const Span span = span_of(p, t, token0, token1, kBoxShift);
   const int box0 = (int)((int64_t)span.boxes * rank / split), box1 = (int)((int64_t)span.boxes * (rank + 1) / split);
 
@@ -95,10 +95,11 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   const int row0 = g, row1 = g + 8;
   const bool live0 = row0 < t.rows, live1 = row1 < t.rows;
-  const int tok0 = (t.first + (live0 ? row0 : 0)) / p.G, tok1 = (t.first + (live1 ? row1 : 0)) / p.G;
+  const int r0 = t.first + (live0 ? row0 : 0), r1 = t.first + (live1 ? row1 : 0);
+  const int tok0 = p.by_G.div(r0), tok1 = p.by_G.div(r1);
   uint32_t Q[D / 16][4];
   {
-    const int h0 = t.head * p.G + (t.first + (live0 ? row0 : 0)) % p.G, h1 = t.head * p.G + (t.first + (live1 ? row1 : 0)) % p.G;
+    const int h0 = t.head * p.G + p.by_G.mod(r0), h1 = t.head * p.G + p.by_G.mod(r1);
     const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok0) * p.q_stride + (int64_t)h0 * D + c2);
     const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok1) * p.q_stride + (int64_t)h1 * D + c2);
 #pragma unroll
@@ -328,7 +329,7 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
-      const int tok = (t.first + r) / p.G, h = t.head * p.G + (t.first + r) % p.G;
+      const int tok = p.by_G.div(t.first + r), h = t.head * p.G + p.by_G.mod(t.first + r);
       *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(t.t0 + tok) * p.H + h) * D + x) = pack_bf2(a * inv, b * inv);
     }
   }
@@ -360,6 +361,7 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   const int64_t tiles = most_tiles(a, kRows) * a.Hkv;
+  p.by_each = divisor((p.G + kRows - 1) / kRows);
   p.split = split_of(tiles, most_keys(a, kRows), sms[dev]);
   TraceScope ts("kda_attention_rows", st);
   cudaLaunchConfig_t cfg{};

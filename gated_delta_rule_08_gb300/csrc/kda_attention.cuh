@@ -17,6 +17,18 @@ using namespace tcx;
 struct Maps {
   CUtensorMap k, v;
 };
+// n / d for 0 <= n < 2^31 by a multiplication (d fixed by the launch): with 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1
+// it is (n + floor(n m / 2^32)) / 2^s, and the sum stays below 2^32.
+struct Divisor {
+  uint32_t m, s, d;
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+  __device__ __forceinline__ int mod(int n) const { return n - div(n) * (int)d; }
+};
+inline Divisor divisor(int d) {
+  uint32_t s = 0;
+  while ((1u << s) < (uint32_t)d) ++s;
+  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - (uint64_t)d)) / (uint64_t)d + 1), s, (uint32_t)d};
+}
 struct Params {
   const __nv_bfloat16* q;
   int64_t q_stride;
@@ -28,7 +40,11 @@ struct Params {
   __nv_bfloat16* out;
   int N;
   int64_t T;
-  int H, Hkv, G, shift, max_blocks, num_blocks, window, sinks;
+  int H, Hkv, G;
+  Divisor by_G, by_Hkv, by_each;  // by_each: tiles of a request of one token
+  int half_rows;             // rows of half an item, and of an item (kda_attention_tc.cu)
+  Divisor by_item;
+  int shift, max_blocks, num_blocks, window, sinks;
   float c;                   // scale log2(e): scores are kept in log2
   unsigned int* err;
   int waits;                 // enum Waits
@@ -85,34 +101,32 @@ struct Tile {
 // Walks the tiles of all requests in order, `per` rows a tile: item = (tile, key head).  A warp calls it
 // with rising items; `base` and `tiles` keep its place.
 struct Walk {
-  int base = 0;         // request of lane 0
-  int64_t tiles = 0;    // tiles of the requests before it
+  int base = 0;     // request of lane 0
+  int tiles = 0;    // tiles of the requests before it
 };
-__device__ __forceinline__ bool locate(const Params& p, int per, int64_t item, Walk& w, Tile& t) {
+__device__ __forceinline__ bool locate(const Params& p, int per, Divisor by_per, int item, Walk& w, Tile& t) {
   const int lane = threadIdx.x & 31;
-  const int64_t tile = item / p.Hkv;
-  t.head = (int)(item - tile * p.Hkv);
-  int64_t k;
+  const int tile = p.by_Hkv.div(item);
+  t.head = item - tile * p.Hkv;
+  int k;
   if (p.cu == nullptr) {
-    const int each = (p.G + per - 1) / per;
-    if (tile >= (int64_t)p.N * each) return false;
-    t.n = (int)(tile / each);
+    t.n = p.by_each.div(tile);
+    if (t.n >= p.N) return false;
     t.t0 = t.n;
     t.tokens = 1;
-    k = tile % each;
+    k = tile - t.n * (int)p.by_each.d;
   } else {
     while (true) {
       if (w.base >= p.N) return false;
       const int n = w.base + lane;
       const int a = n < p.N ? p.cu[n] : 0, b = n < p.N ? p.cu[n + 1] : 0;
-      const int64_t mine = ((int64_t)(b - a) * p.G + per - 1) / per;
-      int64_t sum = mine;
+      int sum = by_per.div((b - a) * p.G + per - 1);  // (T H and a tile's rows are below 2^31 together)
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, (long long)sum, o);
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
       }
-      const int64_t all = __shfl_sync(0xffffffffu, (long long)sum, 31);
+      const int all = __shfl_sync(0xffffffffu, sum, 31);
       if (tile < w.tiles + all) {
         const unsigned over = __ballot_sync(0xffffffffu, w.tiles + sum > tile);
         const int src = __ffs(over) - 1;
@@ -120,7 +134,7 @@ __device__ __forceinline__ bool locate(const Params& p, int per, int64_t item, W
         t.t0 = __shfl_sync(0xffffffffu, a, src);
         t.tokens = __shfl_sync(0xffffffffu, b - a, src);
         // a request's last tile first: it sees the most keys
-        k = __shfl_sync(0xffffffffu, (long long)(w.tiles + sum), src) - 1 - tile;
+        k = __shfl_sync(0xffffffffu, w.tiles + sum, src) - 1 - tile;
         break;
       }
       w.tiles += all;
@@ -129,7 +143,7 @@ __device__ __forceinline__ bool locate(const Params& p, int per, int64_t item, W
   }
   t.len = p.lengths[t.n];
   t.before = t.len - t.tokens;
-  t.first = (int)k * per;  // T H is below 2^31
+  t.first = k * per;
   t.rows = min(t.tokens * p.G - t.first, per);
   bool bad = t.len < 0 || (int64_t)t.len > ((int64_t)p.max_blocks << p.shift);
   if (p.cu == nullptr) {
@@ -270,7 +284,7 @@ inline Params params_of(const AttentionArgs& a) {
   p.cu = a.cu_seqlens; p.mask = a.tree_mask; p.mask_words = a.mask_words; p.out = static_cast<__nv_bfloat16*>(a.out);
   p.N = a.N; p.T = a.T; p.H = a.H; p.Hkv = a.Hkv; p.G = a.H / a.Hkv; p.shift = a.shift; p.max_blocks = a.max_blocks;
   p.num_blocks = a.num_blocks; p.window = a.window; p.sinks = a.sinks; p.c = a.scale * 1.4426950408889634f; p.err = a.err;
-  p.waits = a.waits; p.split = 1;
+  p.waits = a.waits; p.split = 1; p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv);
   return p;
 }
 // Keys that a tile sees at most, as far as the host knows.

@@ -48,7 +48,7 @@ kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, vo
     return KDA_ERR_INVALID_ARG;
   a.shift = block_shift(block_size);
   if (a.shift < 0 || (a.d != 64 && a.d != 128) || !heads_ok(a.H, a.Hkv)) return KDA_ERR_UNSUPPORTED;
-  if (a.N > (1 << 20) || a.T > 0x7fffffff / a.H || (int64_t)a.N * a.H > 0x7fffffff / 64 ||
+  if (a.N > (1 << 20) || a.T > (0x7fffffff - 512) / a.H || (int64_t)a.N * a.H > 0x7fffffff / 64 ||
       (int64_t)a.num_blocks << a.shift > 0x7fffffff || (int64_t)a.N * a.max_blocks > 0x7fffffff)
     return KDA_ERR_UNSUPPORTED;
   if (!strides || !strides_ok(strides, a.d)) return KDA_ERR_INVALID_ARG;

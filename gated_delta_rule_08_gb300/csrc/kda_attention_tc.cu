@@ -41,10 +41,11 @@ struct Layout {
   static constexpr int kParts = D / 64;
   static constexpr uint32_t kPart = kKeys * 128;             // 64 values of 128 rows
   static constexpr uint32_t kTile = kParts * kPart;
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStages = D == 128 ? 4 : 8;           // K and V of two tiles (of four)
   static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
   static constexpr uint32_t kBar = kRing + kStages * kTile;
-  static constexpr uint32_t kSmem = kBar + 512 + 1024;
+  static constexpr uint32_t kOut = kBar + 512;               // 4 KB a softmax warp: 64 values of its 32 rows
+  static constexpr uint32_t kSmem = kOut + 8 * 4096 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert((2 * kStages + 20) * 8 <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
@@ -64,6 +65,10 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_rows(const CUtensorMap* map, int x, int head, int token) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(head), "r"(token)
+               : "memory");
 }
 __device__ __forceinline__ float4 ld_peer4(uint32_t a) {
   float4 v;
@@ -120,32 +125,41 @@ __device__ __forceinline__ int group_key(const Span& s, int j, int g, int box_sh
   const int key = j * kKeys + g * 16, box = key >> box_shift;
   return box < s.boxes ? box_key(s, box, box_shift) + (key & ((1 << box_shift) - 1)) : -1;
 }
-// Bit i: some row of `half` sees a key of group i of tile j; all rows see all of it; every key of it is one that some row
-// of the item sees (one warp together).
-struct Groups {
-  uint32_t some, all;
-};
-__device__ __forceinline__ Groups groups_of(const Params& p, const Span& boxes, const Span& half, int j, int box_shift) {
-  const int lane = threadIdx.x & 31;
-  bool some = false, all = false;
-  if (lane < 8) {
-    const int base = group_key(boxes, j, lane, box_shift);
-    if (base >= 0) {
-      some = used16(p, half, base) != 0;
-      all = all_seen(p, half, base, 16);
+// Keys by their place in the item's tiles: the sinks' boxes come first, as they lie in the cache; from then on the place
+// of a key is the key less this.
+__device__ __forceinline__ int place_shift(const Span& s, int box_shift) { return (s.first_box - s.sink_boxes) << box_shift; }
+// Whether some row of `rows` may see a key of tile j (a span's keys from lo to hi, and the sinks up to hi).
+__device__ __forceinline__ bool tile_seen(const Params& p, const Span& boxes, const Span& rows, int j, int box_shift) {
+  const int shift = place_shift(boxes, box_shift), first = j * kKeys;
+  return (first < rows.hi + 1 - shift && first + kKeys > rows.lo - shift) || first < min(p.sinks, rows.hi + 1);
+}
+// Whether tile j may hold keys that no row of the item sees.
+__device__ __forceinline__ bool unclean(const Span& s, int j, int box_shift) {
+  const int shift = place_shift(s, box_shift), first = j * kKeys;
+  return first < s.lo - shift || first + kKeys > s.hi + 1 - shift;
+}
+// Bits [a, b) of 32.
+__device__ __forceinline__ uint32_t bits(int a, int b) {
+  const uint32_t below_a = a <= 0 ? 0u : a >= 32 ? ~0u : (1u << a) - 1u, below_b = b <= 0 ? 0u : b >= 32 ? ~0u : (1u << b) - 1u;
+  return below_b & ~below_a;
+}
+// Which keys of tile j a row sees, a bit each.
+__device__ __forceinline__ uint4 row_mask(const Params& p, const Tile& t, const Span& s, const Row& r, int j, int box_shift) {
+  const int shift = place_shift(s, box_shift), first = j * kKeys;
+  const int sinks = min(p.sinks, r.hi + 1) - first, lo = r.lo - shift - first, hi = r.hi + 1 - shift - first;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bits(lo - 32 * i, hi - 32 * i) | bits(0, sinks - 32 * i);
+  if (r.mask && first + kKeys > t.before - shift) {
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      const int key = group_key(s, j, g, box_shift);
+      const uint32_t see = key < 0 ? 0u : seen16(p, t, r, key) << (16 * (g & 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] |= i == g / 2 ? see : 0u;
     }
   }
-  return {__ballot_sync(0xffffffffu, some), __ballot_sync(0xffffffffu, all)};
-}
-// Which groups of tile j hold keys that no row of the item sees (one warp together).
-__device__ __forceinline__ uint32_t unclean(const Params& p, const Span& s, int j, int box_shift) {
-  const int lane = threadIdx.x & 31;
-  bool bad = false;
-  if (lane < 8) {
-    const int base = group_key(s, j, lane, box_shift);
-    bad = base < 0 || used16(p, s, base) != 0xffffu;
-  }
-  return __ballot_sync(0xffffffffu, bad);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The tiles, if any, that hold 128 consecutive keys of which every row of the span sees all.
@@ -154,12 +168,9 @@ struct Plain {
 };
 __device__ __forceinline__ Plain plain_tiles(const Span& boxes, const Span& rows, int box_shift) {
   // tile j's first key, from the first after the sinks' boxes on
-  const int64_t shift = ((int64_t)boxes.first_box - boxes.sink_boxes) << box_shift;
-  int64_t first = (((int64_t)boxes.sink_boxes << box_shift) + kKeys - 1) / kKeys;
-  const int64_t seen = (rows.all_lo - shift + kKeys - 1) / kKeys;
-  if (seen > first) first = seen;
-  const int64_t end = ((int64_t)rows.all_hi + 1 - shift) / kKeys;
-  return {(int)first, (int)(end > first ? end : first)};
+  const int shift = place_shift(boxes, box_shift);
+  const int first = max((boxes.sink_boxes << box_shift) + kKeys - 1, rows.all_lo - shift + kKeys - 1) / kKeys;
+  return {first, max(first, (rows.all_hi + 1 - shift) / kKeys)};
 }
 // a value that is the same in all lanes, as one that the compiler knows to be
 __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
@@ -188,7 +199,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
-  const int G = p.G, span_tokens = kHalf / G, half_rows = span_tokens * G;  // of a half
+  const int G = p.G, half_rows = p.half_rows, span_tokens = p.by_G.div(half_rows);  // of a half
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
@@ -224,23 +235,23 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 
   // Items of this CTA: every role walks them by itself.
   Walk walk;
-  int64_t at = split > 1 ? blockIdx.x / split : blockIdx.x;
-  const int64_t step = split > 1 ? (int64_t)1 << 40 : gridDim.x;
+  int at = split > 1 ? blockIdx.x / split : blockIdx.x;
+  const int step = split > 1 ? 0x40000000 : gridDim.x;
   auto next = [&](Item& it) {
     while (true) {
-      if (!locate(p, 2 * half_rows, at, walk, it.t)) return false;
-      at += step;
+      if (at < 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
+      at += step;  // (a second one of a split item's passes 2^31 or the last item)
       if (it.t.rows > 0) break;
     }
-    const int a = it.t.first / G;
-    it.span = span_of(p, it.t, a, a + it.t.rows / G, box_shift);
+    const int a = p.by_G.div(it.t.first);
+    it.span = span_of(p, it.t, a, a + p.by_G.div(it.t.rows), box_shift);
     const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
-    it.tile0 = (int)((int64_t)tiles * rank / split);
-    it.tile1 = (int)((int64_t)tiles * (rank + 1) / split);
+    it.tile0 = split > 1 ? (int)((int64_t)tiles * rank / split) : 0;
+    it.tile1 = split > 1 ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
     return true;
   };
   auto half_span = [&](const Item& it, int h) {
-    const int a = it.t.first / G + h * span_tokens, b = min(a + span_tokens, it.t.first / G + it.t.rows / G);
+    const int first = p.by_G.div(it.t.first), a = first + h * span_tokens, b = min(a + span_tokens, first + p.by_G.div(it.t.rows));
     return span_of(p, it.t, a, b, box_shift);
   };
   const Waiter w{abort_flag, p.waits == kWaitsGiveUp};
@@ -254,7 +265,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     const int h = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t ts = tmem_lane(tmem, warp) + kTmS + 128 * h, to = tmem_lane(tmem, warp) + kTmO + 128 * h;
     uint32_t seen = 0, items = 0;  // scores and items so far: the barriers' phases
-    while (ok && next(it)) {
+    Item coming;  // looked up before the wait for an item's last products
+    bool more = next(coming);
+    while (ok && more) {
+      it = coming;
       const int rows = min(half_rows, it.t.rows - h * half_rows);
       const bool live = row < rows;
       const int r = it.t.first + h * half_rows + (live ? row : 0);  // in the request
@@ -262,44 +276,30 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       bool any = false;
       if (rows > 0) {
         const Span span = half_span(it, h);
-        const Row keys = row_keys(p, it.t, r / G);
+        const Row keys = row_keys(p, it.t, p.by_G.div(r));
         const Plain plain = plain_tiles(it.span, span, box_shift);
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1; ++j) {
-          bool whole = j >= plain.first && j < plain.end;
-          if (!whole) {
-            const Groups g = groups_of(p, it.span, span, j, box_shift);
-            if (g.some == 0) continue;
-            whole = g.all == 0xffu;
-          }
+          const bool whole = j >= plain.first && j < plain.end;
+          if (!whole && !tile_seen(p, it.span, span, j, box_shift)) continue;
           ok = w.hold(&s_full[h], seen & 1);
           if (!ok) break;
           ++seen;
           tc_fence_after();
-          if (!whole) {  // what the row does not see, out of S
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              uint32_t see = 0;
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const int base = group_key(it.span, j, 2 * i + g, box_shift);
-                if (base >= 0) see |= seen16(p, it.t, keys, base) << (16 * g);
-              }
-              float s[32];
-              tmem_ld32(ts + 32 * i, s);
-              tmem_landed(s);
-              uint32_t u[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) u[e] = see >> e & 1 ? __float_as_uint(s[e]) : 0xff800000u;  // -infinity
-              tmem_st32u(ts + 32 * i, u);
-            }
-            tmem_wait_st();
-          }
           float s[4][32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s[i]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_landed(s[i]);
+          if (!whole) {
+            const uint4 see = row_mask(p, it.t, it.span, keys, j, box_shift);
+            const uint32_t words[4] = {see.x, see.y, see.z, see.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(words[i] >> e & 1)) s[i][e] = -INFINITY;
+          }
           float t[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -356,6 +356,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
       }
       if (!ok) break;
+      more = next(coming);
       ok = w.hold(&o_done[h], items & 1);
       if (!ok) break;
       ++items;
@@ -383,25 +384,41 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         break;  // one item
       }
       if (rows > 0) {
+        // by way of shared memory, so that whole lines are written: 64 values of the warp's rows at a time
         const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
-        __nv_bfloat16* dst = p.out + ((int64_t)(it.t.t0 + r / G) * p.H + it.t.head * G + r % G) * D;
-#pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          float o[32];
+        uint8_t* stage = sm + L::kOut + warp * 4096;
+        // rows 4 k + lane / 8 of the warp, and where they go
+        const int row8 = (warp & 3) * 32 + lane / 8;
+        __nv_bfloat16* dst[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int q = it.t.first + h * half_rows + row8 + 4 * k, tok = p.by_G.div(q);
+          dst[k] = p.out + ((int64_t)(it.t.t0 + tok) * p.H + (it.t.head * G + q - tok * G)) * D + lane % 8 * 8;
+        }
+#pragma unroll
+        for (int i = 0; i < L::kParts; ++i) {
+          float o[2][32];
           if (any) {
-            tmem_ld32(to + i, o);
-            tmem_landed(o);
+            tmem_ld32(to + 64 * i, o[0]);
+            tmem_ld32(to + 64 * i + 32, o[1]);
+            tmem_landed(o[0]);
+            tmem_landed(o[1]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0.f;
           }
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + i + e) =
-                  make_uint4(pack_bf2(o[e] * inv, o[e + 1] * inv), pack_bf2(o[e + 2] * inv, o[e + 3] * inv),
-                             pack_bf2(o[e + 4] * inv, o[e + 5] * inv), pack_bf2(o[e + 6] * inv, o[e + 7] * inv));
+          for (int k = 0; k < 8; ++k) {
+            const float* x = &o[k / 4][k % 4 * 8];
+            *reinterpret_cast<uint4*>(stage + row_chunk(lane, k)) =
+                make_uint4(pack_bf2(x[0] * inv, x[1] * inv), pack_bf2(x[2] * inv, x[3] * inv), pack_bf2(x[4] * inv, x[5] * inv),
+                           pack_bf2(x[6] * inv, x[7] * inv));
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (row8 + 4 * k < rows)
+              *reinterpret_cast<uint4*>(dst[k] + 64 * i) = *reinterpret_cast<const uint4*>(stage + row_chunk(4 * k + lane / 8, lane & 7));
           __syncwarp();
         }
         tc_fence_before();  // O is read before the next item's weights are told
@@ -411,19 +428,32 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
       // ======================== copies
-      while (ok && next(it)) {
-        const int halves = it.t.rows > half_rows ? 2 : 1;
-        if (q_issued > 0) ok = w.hold(q_empty, (uint32_t)((q_issued - 1) & 1));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full, (uint32_t)(halves * L::kParts * half_rows * 128));
-          for (int h = 0; h < halves; ++h)
-            for (int i = 0; i < L::kParts; ++i)
-              tma_load_rows(sm + h * L::kTile + i * L::kPart, &qmap.q, 64 * i, it.t.head * G,
-                            it.t.t0 + it.t.first / G + h * span_tokens, q_full);
+      Item coming;
+      bool have = next(coming);
+      while (ok && have) {
+        it = coming;
+        have = next(coming);
+        if (have && lane < 2 * L::kParts) {  // the next item's queries towards L2: every CTA wants its own at about the same time
+          const int h = lane / L::kParts;
+          if (h * half_rows < coming.t.rows)
+            tma_prefetch_rows(&qmap.q, 64 * (lane % L::kParts), coming.t.head * G, coming.t.t0 + p.by_G.div(coming.t.first) + h * span_tokens);
         }
         __syncwarp();
-        ++q_issued;
+        auto copy_q = [&]() {
+          if (q_issued > 0) ok = w.hold(q_empty, (uint32_t)((q_issued - 1) & 1));
+          if (!ok) return;
+          if (lane == 0) {
+            const int halves = it.t.rows > half_rows ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, (uint32_t)(halves * L::kParts * half_rows * 128));
+            for (int h = 0; h < halves; ++h)
+              for (int i = 0; i < L::kParts; ++i)
+                tma_load_rows(sm + h * L::kTile + i * L::kPart, &qmap.q, 64 * i, it.t.head * G,
+                              it.t.t0 + p.by_G.div(it.t.first) + h * span_tokens, q_full);
+          }
+          __syncwarp();
+          ++q_issued;
+        };
+        if (it.tile0 == it.tile1) copy_q();
         const int32_t* table = p.tables + (int64_t)it.t.n * p.max_blocks;
         const int per = kKeys >> box_shift;  // boxes of a tile, at most 8
         // a lane has a box of four tiles at a time
@@ -453,6 +483,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           const int token = box_key(it.span, mine, box_shift) & ((1 << p.shift) - 1);
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
+            if (kv == 1 && j == it.tile0) {  // the first keys have not waited for the item before to leave Q
+              copy_q();
+              if (!ok) break;
+            }
             const int s = (int)(issued % L::kStages);
             if (issued >= L::kStages) ok = w.hold(&empty[s], (uint32_t)((issued / L::kStages - 1) & 1));
             if (!ok) break;
@@ -483,7 +517,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       const bool works = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
       int stage = 0;  // of the next tile in the ring, and its phase
       uint32_t phase = 0, weights = 0, clears = 0, q_used = 0, turns = h ^ 1;  // (half 0 has the first turn)
-      while (works && ok && __any_sync(0xffffffffu, next(it))) {
+      Item coming;  // looked up before the wait for an item's last weights
+      bool have = __any_sync(0xffffffffu, next(coming));
+      while (works && ok && have) {
+        it = coming;
         const int tile0 = same(it.tile0), tile1 = same(it.tile1);
         const bool rows = same(it.t.rows) > h * half_rows;
         const Plain plain = plain_tiles(it.span, it.span, box_shift);
@@ -491,7 +528,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         const Span span = rows ? half_span(it, h) : it.span;
         ok = w.poll(q_full, q_used & 1);
         q_used ^= 1;
-        bool pending = false, begun = false, clean = true;  // weights to come, O begun, V as it came
+        bool pending = false, begun = false, clean = true, left = false;  // weights to come, O begun, V as it came, Q given up
         int v_stage = 0;
         uint32_t v_phase = 0;
 #pragma unroll 1
@@ -502,11 +539,13 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           if (more) {
             active = rows;
             if (j < plain0 || j >= plain1) {
-              active = rows && groups_of(p, it.span, span, j, box_shift).some != 0;
-              next_clean = unclean(p, it.span, j, box_shift) == 0;
+              active = rows && __any_sync(0xffffffffu, tile_seen(p, it.span, span, j, box_shift));
+              next_clean = !__any_sync(0xffffffffu, unclean(it.span, j, box_shift));
             }
             ok = w.poll(&full[stage], phase);
             if (!ok) break;
+          } else {
+            have = __any_sync(0xffffffffu, next(coming));
           }
           if (j > tile0) {
             ok = clean ? w.poll(&full[v_stage], v_phase) : w.poll(cleared, clears);
@@ -542,6 +581,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
                              desc_add(at, (i >> 2) * L::kPart + (i & 3) * 32), id_s, i > 0);
             mma_commit_by(leader, &s_full[h]);
           }
+          if (j + 1 >= tile1 && !left) {  // Q has been read
+            mma_commit_by(leader, q_empty);
+            left = true;
+          }
           if (j > tile0) mma_commit_by(leader, &empty[v_stage]);
           pending = active;
           clean = next_clean;
@@ -565,7 +608,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           }
         }
         if (!ok) break;
-        mma_commit_by(leader, q_empty);
         mma_commit_by(leader, &o_done[h]);
         if (split > 1) {
           mma_commit_by(leader, &o_done[h ^ 1]);
@@ -579,17 +621,16 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       while (ok && next(it)) {
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1 && ok; ++j, used += 2) {
-          const uint32_t bad = unclean(p, it.span, j, box_shift);
-          if (bad == 0) continue;
+          if (!unclean(it.span, j, box_shift)) continue;
           const int s = (int)((used + 1) % L::kStages);
           ok = w.hold(unclear, tiles & 1);
           if (!ok) break;
           ++tiles;
           uint8_t* st = sm + L::kRing + s * L::kTile;
           for (int g = 0; g < 8; ++g) {
-            if (!(bad >> g & 1)) continue;
             const int base = group_key(it.span, j, g, box_shift);
             const uint32_t keep = base < 0 ? 0u : used16(p, it.span, base);
+            if (keep == 0xffffu) continue;
             for (int i = lane; i < 16 * 8 * L::kParts; i += 32) {
               const int r = i & 15, c = i >> 4;
               if (!(keep >> r & 1))
@@ -648,7 +689,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int r = it.t.first + q;
-      *reinterpret_cast<uint4*>(p.out + ((int64_t)(it.t.t0 + r / G) * p.H + it.t.head * G + r % G) * D + x) =
+      *reinterpret_cast<uint4*>(p.out + ((int64_t)(it.t.t0 + p.by_G.div(r)) * p.H + it.t.head * G + p.by_G.mod(r)) * D + x) =
           make_uint4(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv), pack_bf2(b.x * inv, b.y * inv),
                      pack_bf2(b.z * inv, b.w * inv));
     }
@@ -677,6 +718,9 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   const int box_shift = a.shift < 7 ? a.shift : 7, tokens = kHalf / p.G;
+  p.half_rows = tokens * p.G;
+  p.by_item = divisor(2 * p.half_rows);
+  p.by_each = divisor((p.G + 2 * p.half_rows - 1) / (2 * p.half_rows));
   Maps maps;
   QMap qmap;
   if (!tensor_map_cache(&maps.k, a.k_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, 1u << box_shift) ||
