@@ -24,6 +24,8 @@ using namespace attn;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kRows = 16, kBox = 16, kBoxShift = 4;
+constexpr int kMaxSplit = 16;
+constexpr float kGone = -1.f;                // for a sum of weights: the CTA has given up
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
 constexpr float kSlack = 8.f;
 
@@ -32,12 +34,14 @@ struct Layout {
   static constexpr int kParts = D / 64;                    // 128-byte pieces of a token
   static constexpr uint32_t kPart = kBox * 128;            // a piece of all 16 tokens
   static constexpr uint32_t kStage = 2 * kParts * kPart;   // K, then V
-  static constexpr uint32_t kRing = kStages * kStage;      // of a warp; at the end its sums [16][D] fp32
-  static constexpr uint32_t kOut = kWarps * kRing;         // the CTA's sums
-  static constexpr uint32_t kSums = kOut + kRows * D * 4;  // [kWarps + 1][16] references, and sums of weights
-  static constexpr uint32_t kBar = kSums + (kWarps + 1) * kRows * 8;
+  static constexpr uint32_t kRing = kStages * kStage;      // of a warp; at the end its sums [16][kPitch] fp32
+  static constexpr int kPitch = D + 8;                     // (the rows of a quad's store in banks of their own)
+  static constexpr uint32_t kIn = kWarps * kRing;          // [split][16 D / split]: this CTA's part of every CTA's sums
+  static constexpr uint32_t kSums = kIn + kRows * D * 4;   // [kWarps][16] references and sums of weights of the warps,
+  static constexpr uint32_t kAll = kSums + kWarps * kRows * 8;  // [kMaxSplit][16] of the CTAs
+  static constexpr uint32_t kBar = kAll + kMaxSplit * kRows * 8;
   static constexpr uint32_t kSmem = kBar + kWarps * kStages * 8 + 16 + 1024;
-  static_assert(kRows * D * 4 <= kRing, "a warp's sums take its ring's place");
+  static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums take its ring's place");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -65,52 +69,32 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
-  float* refs = reinterpret_cast<float*>(sm + L::kSums);  // [kWarps + 1][16]
-  float* sums = refs + (kWarps + 1) * kRows;
+  float2* sums = reinterpret_cast<float2*>(sm + L::kSums);  // reference, sum of weights
+  float2* all = reinterpret_cast<float2*>(sm + L::kAll);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kWarps * kStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
 
+  // (the CTAs of a cluster have the same tile, so they leave together)
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
   }
   Walk walk;
   Tile t;
-  // (the CTAs of a cluster have the same tile, so they leave together)
   if (!locate(p, kRows, Divisor{1, 4, kRows}, blockIdx.x / split, walk, t) || t.rows == 0) return;
-  const int token0 = p.by_G.div(t.first), token1 = p.by_G.div(t.first + t.rows + p.G - 1);
-  const Span span = span_of(p, t, token0, token1, kBoxShift);
-  const int box0 = (int)((int64_t)span.boxes * rank / split), box1 = (int)((int64_t)span.boxes * (rank + 1) / split);
-
+  if (split > 1) cluster_arrive();  // this CTA has begun: others may write to its memory
   if (tid == 0) {
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full[i], 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
   __syncthreads();
-
-  // Q as the MMA's A operand: rows g and g + 8 of the lane's quad
-  const int g = lane >> 2, c2 = (lane & 3) * 2;
-  const int row0 = g, row1 = g + 8;
-  const bool live0 = row0 < t.rows, live1 = row1 < t.rows;
-  const int r0 = t.first + (live0 ? row0 : 0), r1 = t.first + (live1 ? row1 : 0);
-  const int tok0 = p.by_G.div(r0), tok1 = p.by_G.div(r1);
-  uint32_t Q[D / 16][4];
-  {
-    const int h0 = t.head * p.G + p.by_G.mod(r0), h1 = t.head * p.G + p.by_G.mod(r1);
-    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok0) * p.q_stride + (int64_t)h0 * D + c2);
-    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok1) * p.q_stride + (int64_t)h1 * D + c2);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      Q[i][0] = live0 ? q0[8 * i] : 0u;
-      Q[i][1] = live1 ? q1[8 * i] : 0u;
-      Q[i][2] = live0 ? q0[8 * i + 4] : 0u;
-      Q[i][3] = live1 ? q1[8 * i + 4] : 0u;
-    }
-  }
-  const Row keys0 = row_keys(p, t, tok0), keys1 = row_keys(p, t, tok1);
+  const int token0 = p.by_G.div(t.first), token1 = p.by_G.div(t.first + t.rows + p.G - 1);
+  const Span span = span_of(p, t, token0, token1, kBoxShift);
+  const int box0 = split > 1 ? (int)((int64_t)span.boxes * rank / split) : 0;
+  const int box1 = split > 1 ? (int)((int64_t)span.boxes * (rank + 1) / split) : span.boxes;
 
   float O[D / 8][4];
 #pragma unroll
@@ -163,6 +147,27 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll 1
     while (issued < count && issued < kStages) issue();
   }
+
+  // Q as the MMA's A operand: rows g and g + 8 of the lane's quad
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  const int row0 = g, row1 = g + 8;
+  const bool live0 = row0 < t.rows, live1 = row1 < t.rows;
+  const int r0 = t.first + (live0 ? row0 : 0), r1 = t.first + (live1 ? row1 : 0);
+  const int tok0 = p.by_G.div(r0), tok1 = p.by_G.div(r1);
+  uint32_t Q[D / 16][4];
+  {
+    const int h0 = t.head * p.G + p.by_G.mod(r0), h1 = t.head * p.G + p.by_G.mod(r1);
+    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok0) * p.q_stride + (int64_t)h0 * D + c2);
+    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(p.q + (int64_t)(t.t0 + tok1) * p.q_stride + (int64_t)h1 * D + c2);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      Q[i][0] = live0 ? q0[8 * i] : 0u;
+      Q[i][1] = live1 ? q1[8 * i] : 0u;
+      Q[i][2] = live0 ? q0[8 * i + 4] : 0u;
+      Q[i][3] = live1 ? q1[8 * i + 4] : 0u;
+    }
+  }
+  const Row keys0 = row_keys(p, t, tok0), keys1 = row_keys(p, t, tok1);
 
   const uint32_t key_row = (uint32_t)(((lane >> 4) << 3) + (lane & 7)), k_chunk = (uint32_t)(lane >> 3) & 1u;
   const uint32_t val_row = (uint32_t)(lane & 15), v_chunk = (uint32_t)lane >> 4;
@@ -267,79 +272,79 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
-    *reinterpret_cast<float2*>(mine + row0 * D + 8 * i + c2) = make_float2(O[i][0], O[i][1]);
-    *reinterpret_cast<float2*>(mine + row1 * D + 8 * i + c2) = make_float2(O[i][2], O[i][3]);
+    *reinterpret_cast<float2*>(mine + row0 * L::kPitch + 8 * i + c2) = make_float2(O[i][0], O[i][1]);
+    *reinterpret_cast<float2*>(mine + row1 * L::kPitch + 8 * i + c2) = make_float2(O[i][2], O[i][3]);
   }
   if ((lane & 3) == 0) {
-    refs[warp * kRows + row0] = m0;
-    refs[warp * kRows + row1] = m1;
-    sums[warp * kRows + row0] = l0;
-    sums[warp * kRows + row1] = l1;
+    sums[warp * kRows + row0] = make_float2(m0, l0);
+    sums[warp * kRows + row1] = make_float2(m1, l1);
   }
   __syncthreads();
-  float* joined = reinterpret_cast<float*>(sm + L::kOut);
-  constexpr int kEach = kRows * D / kThreads;  // values a thread joins: a piece of one row
-  {
-    const int r = tid * kEach / D, x = tid * kEach % D;
-    float m = kLowest, l = 0.f, f[kWarps];
+  const bool gone = *abort_flag != 0;
+  if (split > 1) cluster_wait();  // every CTA of the cluster has begun
+  constexpr int kPieces = kRows * D / 4;  // of four values
+  const int part = split == 1 ? kPieces : kPieces / split;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, refs[i * kRows + r]);
+  for (int k = 0; k < kPieces / kThreads; ++k) {
+    const int at = tid + k * kThreads, r = at / (D / 4), x = at % (D / 4) * 4;
+    float m = kLowest, l = 0.f;
+    float2 s[kWarps];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-      f[i] = ex2(refs[i * kRows + r] - m);
-      l += f[i] * sums[i * kRows + r];
+      s[i] = sums[i * kRows + r];
+      m = fmaxf(m, s[i].x);
     }
 #pragma unroll
-    for (int j = 0; j < kEach; j += 4) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i)
-        a = f4_fma(f[i], *reinterpret_cast<const float4*>(sm + i * L::kRing + (r * D + x + j) * 4), a);
-      *reinterpret_cast<float4*>(joined + r * D + x + j) = a;
+    for (int i = 0; i < kWarps; ++i) {
+      const float f = ex2(s[i].x - m);
+      l = fmaf(f, s[i].y, l);
+      a = f4_fma(f, *reinterpret_cast<const float4*>(sm + i * L::kRing + (r * L::kPitch + x) * 4), a);
     }
-    if (x == 0) {
-      refs[kWarps * kRows + r] = m;
-      sums[kWarps * kRows + r] = l;
-    }
-  }
-  if (split > 1) cluster_sync(); else __syncthreads();
-  // each CTA of the cluster writes its part of the rows' pairs of values
-  bool gone = *abort_flag != 0;
-  if (split > 1)
-    for (int i = 0; i < split; ++i) gone |= __float_as_int(ld_peer(peer(const_cast<const int*>(abort_flag), i))) != 0;
-  if (!gone) {
-    const int pairs = kRows * D / 2 / split;
-    for (int i = tid; i < pairs; i += kThreads) {
-      const int at = rank * pairs + i, r = at / (D / 2), x = at % (D / 2) * 2;
-      if (r >= t.rows) break;
-      float a, b, l;
-      if (split == 1) {
-        a = joined[r * D + x];
-        b = joined[r * D + x + 1];
-        l = sums[kWarps * kRows + r];
-      } else {
-        float m = kLowest;
-        a = b = l = 0.f;
-        for (int k = 0; k < split; ++k) m = fmaxf(m, ld_peer(peer(refs + kWarps * kRows + r, k)));
-        for (int k = 0; k < split; ++k) {
-          const float f = ex2(ld_peer(peer(refs + kWarps * kRows + r, k)) - m);
-          l = fmaf(f, ld_peer(peer(sums + kWarps * kRows + r, k)), l);
-          a = fmaf(f, ld_peer(peer(joined + r * D + x, k)), a);
-          b = fmaf(f, ld_peer(peer(joined + r * D + x + 1, k)), b);
-        }
-      }
-      const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
-      const int tok = p.by_G.div(t.first + r), h = t.head * p.G + p.by_G.mod(t.first + r);
-      *reinterpret_cast<uint32_t*>(p.out + ((int64_t)(t.t0 + tok) * p.H + h) * D + x) = pack_bf2(a * inv, b * inv);
+    if (gone) l = kGone;
+    if (split == 1) {
+      *reinterpret_cast<float4*>(sm + L::kIn + at * 16) = a;
+      if (x == 0) all[r] = make_float2(m, l);
+    } else {
+      const int to = at / part;  // the CTA that writes these values; and everyone wants the sums
+      st_peer4(peer(sm + L::kIn + (rank * part + at - to * part) * 16, to), a);
+      if (x / 4 < split) st_peer2(peer(all + rank * kRows + r, x / 4), make_float2(m, l));
     }
   }
-  if (split > 1) cluster_sync();  // no CTA leaves while another reads its memory
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  // this CTA's part of the rows (nobody writes to its memory any more, and it reads no one else's)
+  for (int i = tid; i < part; i += kThreads) {
+    const int at = rank * part + i, r = at / (D / 4), x = at % (D / 4) * 4;
+    float m = kLowest, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool lost = false;
+#pragma unroll 4
+    for (int k = 0; k < split; ++k) m = fmaxf(m, all[k * kRows + r].x);
+#pragma unroll 4
+    for (int k = 0; k < split; ++k) {
+      const float2 s = all[k * kRows + r];
+      const float f = ex2(s.x - m);
+      lost |= s.y == kGone;
+      l = fmaf(f, s.y, l);
+      a = f4_fma(f, *reinterpret_cast<const float4*>(sm + L::kIn + (k * part + i) * 16), a);
+    }
+    if (r >= t.rows || lost) continue;
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
+    const int tok = p.by_G.div(t.first + r), h = t.head * p.G + p.by_G.mod(t.first + r);
+    *reinterpret_cast<uint2*>(p.out + ((int64_t)(t.t0 + tok) * p.H + h) * D + x) =
+        make_uint2(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv));
+  }
 }
 
 // CTAs that share a tile: as many as there are SMs for (two CTAs each), 16 at most, and no fewer than 256 keys each.
 int split_of(int64_t tiles, int64_t keys, int sms) {
   int split = 1;
-  while (split < 16 && tiles * split * 2 <= 2 * sms && keys >= 512 * split) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= 2 * sms && keys >= 512 * split) split *= 2;
   return split;
 }
 
@@ -352,17 +357,17 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   static DeviceOnce once;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  static int sms[kMaxDevices];
-  cudaError_t e = once.run(dev, [dev] {
-    cudaError_t f = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  cudaError_t e = once.run(dev, [] {
+    cudaError_t f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
     if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return f;
   });
   if (e != cudaSuccess) return e;
   const int64_t tiles = most_tiles(a, kRows) * a.Hkv;
   p.by_each = divisor((p.G + kRows - 1) / kRows);
-  p.split = split_of(tiles, most_keys(a, kRows), sms[dev]);
+  p.split = split_of(tiles, most_keys(a, kRows), sms);
   TraceScope ts("kda_attention_rows", st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * p.split));

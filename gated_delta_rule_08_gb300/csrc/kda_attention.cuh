@@ -68,8 +68,11 @@ __device__ __forceinline__ void tma_load_box(void* dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(token), "r"(head), "r"(block), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // the same shared address in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer(const void* p, int rank) {
@@ -77,10 +80,23 @@ __device__ __forceinline__ uint32_t peer(const void* p, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ float ld_peer(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+// Loads and stores there.  (Between the cluster's barriers, which the compiler moves no memory access over; the loads
+// themselves may overlap.)
+__device__ __forceinline__ float2 ld_peer2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
   return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void st_peer2(uint32_t a, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_peer4(uint32_t a, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 // Whether the offsets rise from 0 to at most T (all threads of the CTA).
@@ -286,6 +302,15 @@ inline Params params_of(const AttentionArgs& a) {
   p.num_blocks = a.num_blocks; p.window = a.window; p.sinks = a.sinks; p.c = a.scale * 1.4426950408889634f; p.err = a.err;
   p.waits = a.waits; p.split = 1; p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv);
   return p;
+}
+// SMs of the current device; 0 if a query fails.
+inline int device_sms() {
+  static DeviceOnce once;
+  static int sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (once.run(dev, [dev] { return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); }) != cudaSuccess) return 0;
+  return sms[dev];
 }
 // Keys that a tile sees at most, as far as the host knows.
 inline int64_t most_keys(const AttentionArgs& a, int64_t tokens) {

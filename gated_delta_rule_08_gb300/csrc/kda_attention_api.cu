@@ -39,8 +39,12 @@ kda_status done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA
 
 bool heads_ok(int H, int Hkv) { return H % Hkv == 0 && H / Hkv <= 128; }
 
-// Rows of a key head and request, in the mean (their numbers are on the device), from which on tiles of 128 rows pay.
-bool many_rows(const AttentionArgs& a) { return a.T * (a.H / a.Hkv) > (int64_t)32 * a.N; }
+// Rows of a key head and request, in the mean (their numbers are on the device), from which on tiles of 128 rows pay:
+// more than one tile of 16, each of which reads the keys again; or more than four where they would leave SMs idle.
+bool many_rows(const AttentionArgs& a) {
+  const int64_t rows = a.T * (a.H / a.Hkv);
+  return rows > (int64_t)(a.N * a.Hkv <= 32 ? 64 : 16) * a.N;
+}
 
 kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, void* stream) {
   if (a.N < 0 || a.T < 0 || a.H <= 0 || a.Hkv <= 0 || a.num_blocks < 0 || a.max_blocks < 0 || a.window < 0 || a.sinks < 0 ||

@@ -34,18 +34,19 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register
 constexpr int kHalf = 128, kKeys = 128;
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
 constexpr float kSlack = 8.f;
+constexpr float kGone = -1.f;                 // for a sum of weights: the CTA has given up
 constexpr uint32_t kTmS = 0, kTmO = 256;      // TMEM columns: S (and P) of the halves, O of the halves
 
-template <int D>
+template <int D, bool SPLIT>
 struct Layout {
   static constexpr int kParts = D / 64;
   static constexpr uint32_t kPart = kKeys * 128;             // 64 values of 128 rows
   static constexpr uint32_t kTile = kParts * kPart;
-  static constexpr int kStages = D == 128 ? 4 : 8;           // K and V of two tiles (of four)
+  static constexpr int kStages = (SPLIT ? 5 : 4) * (2 / kParts);
   static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
   static constexpr uint32_t kBar = kRing + kStages * kTile;
-  static constexpr uint32_t kOut = kBar + 512;               // 4 KB a softmax warp: 64 values of its 32 rows
-  static constexpr uint32_t kSmem = kOut + 8 * 4096 + 1024;
+  static constexpr uint32_t kOut = kBar + 512;               // 4 KB a softmax warp: 64 values of its 32 rows (not SPLIT)
+  static constexpr uint32_t kSmem = kOut + (SPLIT ? 0 : 8 * 4096) + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert((2 * kStages + 20) * 8 <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
@@ -70,10 +71,10 @@ __device__ __forceinline__ void tma_prefetch_rows(const CUtensorMap* map, int x,
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(head), "r"(token)
                : "memory");
 }
-__device__ __forceinline__ float4 ld_peer4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void tma_prefetch_box(const CUtensorMap* map, int x, int token, int head, int block) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(token), "r"(head),
+               "r"(block)
+               : "memory");
 }
 // Waits of a whole warp (branches are on votes, so that it stays together), with a limit of about a second, or none at
 // all in the variant that gives up.  hold() leaves the waiting to the hardware; poll() is for the MMA warp, which all
@@ -175,10 +176,11 @@ __device__ __forceinline__ Plain plain_tiles(const Span& boxes, const Span& rows
 // a value that is the same in all lanes, as one that the compiler knows to be
 __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-template <int D>
+// SPLIT: an item a cluster, whose p.split CTAs share its keys; else a CTA walks over items.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
-  using L = Layout<D>;
+  using L = Layout<D, SPLIT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
@@ -194,11 +196,11 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   uint64_t* bar_fin = q_full + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* refs = reinterpret_cast<float*>(sm);  // of 256 rows, in Q's place once the item's products are done (split)
-  float* sums = refs + 256;
+  // reference and sum of weights of 256 rows, in Q's place once the item's products are done (SPLIT)
+  float2* sums = reinterpret_cast<float2*>(sm);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+  const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)(blockIdx.x % split) : 0;
   const int G = p.G, half_rows = p.half_rows, span_tokens = p.by_G.div(half_rows);  // of a half
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
@@ -220,7 +222,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       mbar_init(&p_ready[2 * h], 4);
       mbar_init(&p_ready[2 * h + 1], 4);
       mbar_init(&turn[h], 1);
-      mbar_init(&o_done[h], split > 1 ? 2 : 1);
+      mbar_init(&o_done[h], SPLIT ? 2 : 1);
     }
     mbar_init(cleared, 1);
     mbar_init(unclear, 1);
@@ -235,8 +237,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 
   // Items of this CTA: every role walks them by itself.
   Walk walk;
-  int at = split > 1 ? blockIdx.x / split : blockIdx.x;
-  const int step = split > 1 ? 0x40000000 : gridDim.x;
+  int at = SPLIT ? blockIdx.x / split : blockIdx.x;
+  const int step = SPLIT ? 0x40000000 : gridDim.x;
   auto next = [&](Item& it) {
     while (true) {
       if (at < 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
@@ -246,8 +248,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     const int a = p.by_G.div(it.t.first);
     it.span = span_of(p, it.t, a, a + p.by_G.div(it.t.rows), box_shift);
     const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
-    it.tile0 = split > 1 ? (int)((int64_t)tiles * rank / split) : 0;
-    it.tile1 = split > 1 ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
+    it.tile0 = SPLIT ? (int)((int64_t)tiles * rank / split) : 0;
+    it.tile1 = SPLIT ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
     return true;
   };
   auto half_span = [&](const Item& it, int h) {
@@ -361,7 +363,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       if (!ok) break;
       ++items;
       tc_fence_after();
-      if (split > 1) {
+      if (SPLIT) {
         // sums into the ring (all its tiles have been read), pieces of 16 bytes permuted by the row
         const int rr = h * kHalf + row;
         uint8_t* dst = sm + L::kRing + (uint32_t)rr * (D * 4);
@@ -379,8 +381,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(dst + (((i + e) / 4 ^ (rr & (D / 4 - 1))) << 4)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
-        refs[rr] = m;
-        sums[rr] = l;
+        sums[rr] = make_float2(m, l);
         break;  // one item
       }
       if (rows > 0) {
@@ -432,13 +433,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       bool have = next(coming);
       while (ok && have) {
         it = coming;
-        have = next(coming);
-        if (have && lane < 2 * L::kParts) {  // the next item's queries towards L2: every CTA wants its own at about the same time
-          const int h = lane / L::kParts;
-          if (h * half_rows < coming.t.rows)
-            tma_prefetch_rows(&qmap.q, 64 * (lane % L::kParts), coming.t.head * G, coming.t.t0 + p.by_G.div(coming.t.first) + h * span_tokens);
-        }
-        __syncwarp();
         auto copy_q = [&]() {
           if (q_issued > 0) ok = w.hold(q_empty, (uint32_t)((q_issued - 1) & 1));
           if (!ok) return;
@@ -453,7 +447,29 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           __syncwarp();
           ++q_issued;
         };
-        if (it.tile0 == it.tile1) copy_q();
+        auto look_ahead = [&]() {
+          have = next(coming);
+          if (!have) return;
+          // Towards L2, as all CTAs come to their next items at about the same time: its queries, and its last keys and
+          // values (of a prompt: those that no item before it has read).
+          const int part = lane % L::kParts, i = lane / L::kParts;
+          if (i < 2 && i * half_rows < coming.t.rows)
+            tma_prefetch_rows(&qmap.q, 64 * part, coming.t.head * G, coming.t.t0 + p.by_G.div(coming.t.first) + i * span_tokens);
+          const int box = coming.span.boxes - 1 - i;
+          if (i < kKeys >> box_shift && box >= 0) {
+            const int key = box_key(coming.span, box, box_shift);
+            const int id = p.tables[(int64_t)coming.t.n * p.max_blocks + (key >> p.shift)];
+            if ((unsigned)id < (unsigned)p.num_blocks) {
+              tma_prefetch_box(&maps.k, 64 * part, key & ((1 << p.shift) - 1), coming.t.head, id);
+              tma_prefetch_box(&maps.v, 64 * part, key & ((1 << p.shift) - 1), coming.t.head, id);
+            }
+          }
+          __syncwarp();
+        };
+        if (it.tile0 == it.tile1) {
+          copy_q();
+          look_ahead();
+        }
         const int32_t* table = p.tables + (int64_t)it.t.n * p.max_blocks;
         const int per = kKeys >> box_shift;  // boxes of a tile, at most 8
         // a lane has a box of four tiles at a time
@@ -501,6 +517,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
             __syncwarp();
             ++issued;
           }
+          if (ok && j == it.tile0) look_ahead();
         }
       }
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -609,7 +626,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
         if (!ok) break;
         mma_commit_by(leader, &o_done[h]);
-        if (split > 1) {
+        if (SPLIT) {
           mma_commit_by(leader, &o_done[h ^ 1]);
           break;
         }
@@ -640,7 +657,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           fence_proxy_async_smem();
           warp_arrive(cleared);
         }
-        if (split > 1) break;
+        if (SPLIT) break;
       }
     }
   }
@@ -662,15 +679,15 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   }
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-  if (split == 1) return;
+  if (!SPLIT) return;
 
   // the cluster's CTAs join: each a part of the rows
-  cluster_sync();
-  bool gone = false;
-  for (int i = 0; i < split; ++i) gone |= __float_as_int(ld_peer(peer(const_cast<const int*>(abort_flag), i))) != 0;
+  if (*abort_flag && tid < 256) sums[tid] = make_float2(kLowest, kGone);
   walk = Walk{};
   at = blockIdx.x / split;
-  if (!gone && next(it)) {
+  const bool there = next(it);
+  cluster_sync();
+  if (there) {
     constexpr int kPieces = D / 8;  // a thread's eight values
     const int each = 256 / split;
     for (int i = tid; i < each * kPieces; i += kThreads) {
@@ -678,15 +695,23 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       const int h = rr / kHalf, row = rr % kHalf, q = h * half_rows + row;
       if (row >= half_rows || q >= it.t.rows) continue;
       float m = kLowest, l = 0.f;
-      for (int k = 0; k < split; ++k) m = fmaxf(m, ld_peer(peer(refs + rr, k)));
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       const uint8_t* src = sm + L::kRing + (uint32_t)rr * (D * 4);
-      for (int k = 0; k < split; ++k) {
-        const float f = ex2(ld_peer(peer(refs + rr, k)) - m);
-        l = fmaf(f, ld_peer(peer(sums + rr, k)), l);
-        a = f4_fma(f, ld_peer4(peer(src + ((x / 4 ^ (rr & (D / 4 - 1))) << 4), k)), a);
-        b = f4_fma(f, ld_peer4(peer(src + (((x / 4 + 1) ^ (rr & (D / 4 - 1))) << 4), k)), b);
+      const uint32_t pa = (uint32_t)(x / 4 ^ (rr & (D / 4 - 1))) << 4, pb = (uint32_t)((x / 4 + 1) ^ (rr & (D / 4 - 1))) << 4;
+      bool lost = false;
+#pragma unroll 1
+      for (int k = 0; k < split; k += 2) {  // two CTAs' parts under way at a time
+        const float2 s0 = ld_peer2(peer(sums + rr, k)), s1 = ld_peer2(peer(sums + rr, min(k + 1, split - 1)));
+        const float4 a0 = ld_peer4(peer(src + pa, k)), b0 = ld_peer4(peer(src + pb, k));
+        const float4 a1 = ld_peer4(peer(src + pa, min(k + 1, split - 1))), b1 = ld_peer4(peer(src + pb, min(k + 1, split - 1)));
+        lost |= s0.y == kGone || s1.y == kGone;
+        const float n = fmaxf(m, fmaxf(s0.x, s1.x)), f = ex2(m - n), f0 = ex2(s0.x - n), f1 = k + 1 < split ? ex2(s1.x - n) : 0.f;
+        m = n;
+        l = fmaf(f, l, fmaf(f0, s0.y, f1 * s1.y));
+        a = f4_fma(f0, a0, f4_fma(f1, a1, make_float4(f * a.x, f * a.y, f * a.z, f * a.w)));
+        b = f4_fma(f0, b0, f4_fma(f1, b1, make_float4(f * b.x, f * b.y, f * b.z, f * b.w)));
       }
+      if (lost) continue;
       const float inv = l != 0.f ? 1.f / l : 0.f;
       const int r = it.t.first + q;
       *reinterpret_cast<uint4*>(p.out + ((int64_t)(it.t.t0 + p.by_G.div(r)) * p.H + it.t.head * G + p.by_G.mod(r)) * D + x) =
@@ -697,26 +722,45 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   cluster_sync();  // no CTA leaves while another reads its memory
 }
 
-// CTAs that share an item's keys: as many as there are SMs for, 16 at most, and no fewer than four tiles each.
+// CTAs that share an item's keys: where items leave SMs idle, as many as there are SMs for, with two tiles each at least;
+// else (trees: lengths differ from request to request) so many that none has more than kMostKeys.
+constexpr int kMostKeys = 4096;
 int split_of(int64_t items, int64_t keys, int sms) {
   int split = 1;
-  while (split < 16 && items * split * 2 <= sms && keys >= (int64_t)split * 2 * 4 * kKeys) split *= 2;
+  while (split < 8 && keys > (int64_t)split * (items * split * 2 <= sms ? 2 * kKeys : kMostKeys)) split *= 2;
   return split;
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch_one(const Maps& maps, const QMap& qmap, const Params& p, int box_shift, unsigned grid, cudaStream_t st) {
+  static DeviceOnce once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const cudaError_t e = once.run(dev, [] {
+    cudaError_t f = cudaFuncSetAttribute(attention_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D, SPLIT>::kSmem);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return f;
+  });
+  if (e != cudaSuccess) return e;
+  TraceScope ts("kda_attention_tc", st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Layout<D, SPLIT>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<D, SPLIT>, maps, qmap, p, box_shift);
 }
 
 template <int D>
 cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
-  static DeviceOnce once;
-  static int sms[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  const cudaError_t e = once.run(dev, [dev] {
-    cudaError_t f = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
-    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return f;
-  });
-  if (e != cudaSuccess) return e;
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   const int box_shift = a.shift < 7 ? a.shift : 7, tokens = kHalf / p.G;
   p.half_rows = tokens * p.G;
   p.by_item = divisor(2 * p.half_rows);
@@ -727,21 +771,10 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
       !tensor_map_cache(&maps.v, a.v_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, 1u << box_shift) ||
       !tensor_map_rows(&qmap.q, a.q, a.T, a.H, D, a.q_stride, (uint32_t)tokens, (uint32_t)p.G))
     return cudaErrorInvalidValue;
-  const int64_t items = most_tiles(a, 2 * tokens * p.G) * a.Hkv;
-  p.split = split_of(items, most_keys(a, 2 * tokens), sms[dev]);
-  TraceScope ts("kda_attention_tc", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.split > 1 ? items * p.split : items < sms[dev] ? items : sms[dev]));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<D>, maps, qmap, p, box_shift);
+  const int64_t items = most_tiles(a, 2 * p.half_rows) * a.Hkv;
+  if (a.tree_mask == nullptr && items > sms / 2) return launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)(items < sms ? items : sms), st);
+  p.split = split_of(items, most_keys(a, 2 * tokens), sms);
+  return launch_one<D, true>(maps, qmap, p, box_shift, (unsigned)(items * p.split), st);
 }
 
 }  // namespace
