@@ -760,16 +760,20 @@ def _caches(k_cache, v_cache, index: int):
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, Hkv, d]")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    strides, d = k_cache.stride(), shape[3]
+    bf16 = torch.bfloat16
+    if not (k_cache.dtype is bf16 and v_cache.dtype is bf16 and k_cache.get_device() == index == v_cache.get_device()):
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            if t.dtype is not bf16:
+                raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    strides = k_cache.stride()
     if strides[3] != 1 or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same strides, and dense heads")
+    blocks, size, heads, d = shape
     # (the stride of a dimension of one says nothing)
-    return shape, _CacheStrides(*(strides[i] if shape[i] != 1 else max(d, 8) for i in range(3)))
+    return shape, _CacheStrides(strides[0] if blocks != 1 else d, strides[1] if size != 1 else d,
+                                strides[2] if heads != 1 else d)
 
 
 def kda_rope_append(q, k, v, inv_freq, positions, slot_map, k_cache, v_cache, *, axis=None, interleaved: bool = False,

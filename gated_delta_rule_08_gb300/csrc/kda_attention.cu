@@ -74,16 +74,19 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kWarps * kStages);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = p.split, rank = split > 1 ? (int)(blockIdx.x % split) : 0;
+  const int rank = p.split > 1 ? (int)(blockIdx.x % p.split) : 0;
 
-  // (the CTAs of a cluster have the same tile, so they leave together)
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
   }
   Walk walk;
   Tile t;
-  if (!locate(p, kRows, Divisor{1, 4, kRows}, blockIdx.x / split, walk, t) || t.rows == 0) return;
+  if (!locate(p, kRows, Divisor{1, 4, kRows}, blockIdx.x / p.split, walk, t) || t.rows == 0) return;
+  const int token0 = p.by_G.div(t.first), token1 = p.by_G.div(t.first + t.rows + p.G - 1);
+  const Span span = span_of(p, t, token0, token1, kBoxShift);
+  const int split = parts_of(p, span.boxes);
+  if (rank >= split) return;
   if (split > 1) cluster_arrive();  // this CTA has begun: others may write to its memory
   if (tid == 0) {
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full[i], 1);
@@ -91,8 +94,6 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
     mbar_fence_init();
   }
   __syncthreads();
-  const int token0 = p.by_G.div(t.first), token1 = p.by_G.div(t.first + t.rows + p.G - 1);
-  const Span span = span_of(p, t, token0, token1, kBoxShift);
   const int box0 = split > 1 ? (int)((int64_t)span.boxes * rank / split) : 0;
   const int box1 = split > 1 ? (int)((int64_t)span.boxes * (rank + 1) / split) : span.boxes;
 
@@ -341,11 +342,17 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   }
 }
 
-// CTAs that share a tile: as many as there are SMs for (two CTAs each), 16 at most, and no fewer than 256 keys each.
-int split_of(int64_t tiles, int64_t keys, int sms) {
-  int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= 2 * sms && keys >= 512 * split) split *= 2;
-  return split;
+// CTAs that may share a tile's keys, and the boxes for each at least: few tiles leave SMs idle, and are cut down to 256
+// keys; many are cut to about kMostKeys, so that no long request is left over at the end, as far as CTAs that find nothing
+// to do (of the others) remain cheap.
+constexpr int kMostKeys = 2048, kMostCtas = 4096;
+void split_of(int64_t tiles, int64_t keys, int sms, int* split, int* least) {
+  *split = 1;
+  while (*split < kMaxSplit && tiles * *split * 2 <= 2 * sms && keys > 256 * *split) *split *= 2;
+  *least = 256 / kBox;
+  if (tiles * 4 <= 2 * sms) return;
+  *least = kMostKeys / kBox;
+  while (*split < kMaxSplit && tiles * *split * 2 <= kMostCtas && keys > kMostKeys * *split) *split *= 2;
 }
 
 template <int D>
@@ -367,7 +374,7 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = most_tiles(a, kRows) * a.Hkv;
   p.by_each = divisor((p.G + kRows - 1) / kRows);
-  p.split = split_of(tiles, most_keys(a, kRows), sms);
+  split_of(tiles, most_keys(a, kRows), sms, &p.split, &p.least);
   TraceScope ts("kda_attention_rows", st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * p.split));

@@ -48,7 +48,8 @@ struct Params {
   float c;                   // scale log2(e): scores are kept in log2
   unsigned int* err;
   int waits;                 // enum Waits
-  int split;                 // CTAs (a cluster) that share a tile's keys
+  int split;                 // CTAs (a cluster) that may share a tile's keys: those past parts_of() leave at once
+  int least;                 // boxes (tc: tiles) for each of them at least
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -97,6 +98,13 @@ __device__ __forceinline__ void st_peer2(uint32_t a, float2 v) {
 }
 __device__ __forceinline__ void st_peer4(uint32_t a, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// Into how many parts (CTAs) a tile's keys are cut: a power of two that the host bounds and the request's length decides.
+__device__ __forceinline__ int parts_of(const Params& p, int boxes) {
+  int parts = 1;
+  while (parts < p.split && boxes > parts * p.least) parts *= 2;
+  return parts;
 }
 
 // Whether the offsets rise from 0 to at most T (all threads of the CTA).
@@ -302,15 +310,6 @@ inline Params params_of(const AttentionArgs& a) {
   p.num_blocks = a.num_blocks; p.window = a.window; p.sinks = a.sinks; p.c = a.scale * 1.4426950408889634f; p.err = a.err;
   p.waits = a.waits; p.split = 1; p.by_G = divisor(p.G); p.by_Hkv = divisor(p.Hkv);
   return p;
-}
-// SMs of the current device; 0 if a query fails.
-inline int device_sms() {
-  static DeviceOnce once;
-  static int sms[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (once.run(dev, [dev] { return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); }) != cudaSuccess) return 0;
-  return sms[dev];
 }
 // Keys that a tile sees at most, as far as the host knows.
 inline int64_t most_keys(const AttentionArgs& a, int64_t tokens) {

@@ -200,12 +200,34 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   float2* sums = reinterpret_cast<float2*>(sm);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = SPLIT ? p.split : 1, rank = SPLIT ? (int)(blockIdx.x % split) : 0;
+  const int rank = SPLIT ? (int)(blockIdx.x % p.split) : 0;
+  int split = 1;
   const int G = p.G, half_rows = p.half_rows, span_tokens = p.by_G.div(half_rows);  // of a half
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
   }
+  // Items of this CTA: every role walks them by itself, one ahead.
+  Walk walk;
+  int at = SPLIT ? blockIdx.x / p.split : blockIdx.x;
+  const int step = SPLIT ? 0x40000000 : gridDim.x;
+  auto next = [&](Item& it) {
+    while (true) {
+      if (at < 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
+      at += step;  // (a second one of a split item's passes 2^31 or the last item)
+      if (it.t.rows > 0) break;
+    }
+    const int a = p.by_G.div(it.t.first);
+    it.span = span_of(p, it.t, a, a + p.by_G.div(it.t.rows), box_shift);
+    const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
+    if (SPLIT) split = parts_of(p, tiles);
+    it.tile0 = SPLIT ? (int)((int64_t)tiles * rank / split) : 0;
+    it.tile1 = SPLIT ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
+    return true;
+  };
+  Item coming;
+  bool have = next(coming);
+  if (SPLIT && (!have || rank >= split)) return;
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -235,23 +257,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Items of this CTA: every role walks them by itself.
-  Walk walk;
-  int at = SPLIT ? blockIdx.x / split : blockIdx.x;
-  const int step = SPLIT ? 0x40000000 : gridDim.x;
-  auto next = [&](Item& it) {
-    while (true) {
-      if (at < 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
-      at += step;  // (a second one of a split item's passes 2^31 or the last item)
-      if (it.t.rows > 0) break;
-    }
-    const int a = p.by_G.div(it.t.first);
-    it.span = span_of(p, it.t, a, a + p.by_G.div(it.t.rows), box_shift);
-    const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
-    it.tile0 = SPLIT ? (int)((int64_t)tiles * rank / split) : 0;
-    it.tile1 = SPLIT ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
-    return true;
-  };
   auto half_span = [&](const Item& it, int h) {
     const int first = p.by_G.div(it.t.first), a = first + h * span_tokens, b = min(a + span_tokens, first + p.by_G.div(it.t.rows));
     return span_of(p, it.t, a, b, box_shift);
@@ -267,9 +272,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     const int h = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t ts = tmem_lane(tmem, warp) + kTmS + 128 * h, to = tmem_lane(tmem, warp) + kTmO + 128 * h;
     uint32_t seen = 0, items = 0;  // scores and items so far: the barriers' phases
-    Item coming;  // looked up before the wait for an item's last products
-    bool more = next(coming);
-    while (ok && more) {
+    while (ok && have) {
       it = coming;
       const int rows = min(half_rows, it.t.rows - h * half_rows);
       const bool live = row < rows;
@@ -358,7 +361,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
       }
       if (!ok) break;
-      more = next(coming);
+      have = next(coming);  // before the wait for the item's last products
       ok = w.hold(&o_done[h], items & 1);
       if (!ok) break;
       ++items;
@@ -429,8 +432,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
       // ======================== copies
-      Item coming;
-      bool have = next(coming);
       while (ok && have) {
         it = coming;
         auto copy_q = [&]() {
@@ -534,8 +535,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       const bool works = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
       int stage = 0;  // of the next tile in the ring, and its phase
       uint32_t phase = 0, weights = 0, clears = 0, q_used = 0, turns = h ^ 1;  // (half 0 has the first turn)
-      Item coming;  // looked up before the wait for an item's last weights
-      bool have = __any_sync(0xffffffffu, next(coming));
+      have = __any_sync(0xffffffffu, have);
       while (works && ok && have) {
         it = coming;
         const int tile0 = same(it.tile0), tile1 = same(it.tile1);
@@ -635,7 +635,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       // ======================== values that no row sees
       // (told of a tile's arrival by the MMA warp, which follows the ring; a wait that skips phases would mistake them)
       uint32_t used = 0, tiles = 0;
-      while (ok && next(it)) {
+      for (; ok && have; have = next(coming)) {
+        it = coming;
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1 && ok; ++j, used += 2) {
           if (!unclean(it.span, j, box_shift)) continue;
@@ -684,16 +685,17 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   // the cluster's CTAs join: each a part of the rows
   if (*abort_flag && tid < 256) sums[tid] = make_float2(kLowest, kGone);
   walk = Walk{};
-  at = blockIdx.x / split;
-  const bool there = next(it);
+  at = blockIdx.x / p.split;
+  next(coming);
   cluster_sync();
-  if (there) {
+  {
+    const Tile& t = coming.t;
     constexpr int kPieces = D / 8;  // a thread's eight values
     const int each = 256 / split;
     for (int i = tid; i < each * kPieces; i += kThreads) {
       const int rr = rank * each + i / kPieces, x = i % kPieces * 8;
       const int h = rr / kHalf, row = rr % kHalf, q = h * half_rows + row;
-      if (row >= half_rows || q >= it.t.rows) continue;
+      if (row >= half_rows || q >= t.rows) continue;
       float m = kLowest, l = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       const uint8_t* src = sm + L::kRing + (uint32_t)rr * (D * 4);
@@ -713,8 +715,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       }
       if (lost) continue;
       const float inv = l != 0.f ? 1.f / l : 0.f;
-      const int r = it.t.first + q;
-      *reinterpret_cast<uint4*>(p.out + ((int64_t)(it.t.t0 + p.by_G.div(r)) * p.H + it.t.head * G + p.by_G.mod(r)) * D + x) =
+      const int r = t.first + q;
+      *reinterpret_cast<uint4*>(p.out + ((int64_t)(t.t0 + p.by_G.div(r)) * p.H + t.head * G + p.by_G.mod(r)) * D + x) =
           make_uint4(pack_bf2(a.x * inv, a.y * inv), pack_bf2(a.z * inv, a.w * inv), pack_bf2(b.x * inv, b.y * inv),
                      pack_bf2(b.z * inv, b.w * inv));
     }
@@ -722,13 +724,16 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   cluster_sync();  // no CTA leaves while another reads its memory
 }
 
-// CTAs that share an item's keys: where items leave SMs idle, as many as there are SMs for, with two tiles each at least;
-// else (trees: lengths differ from request to request) so many that none has more than kMostKeys.
-constexpr int kMostKeys = 4096;
-int split_of(int64_t items, int64_t keys, int sms) {
-  int split = 1;
-  while (split < 8 && keys > (int64_t)split * (items * split * 2 <= sms ? 2 * kKeys : kMostKeys)) split *= 2;
-  return split;
+// CTAs that may share an item's keys, and the tiles for each at least: where items leave SMs idle, as many as there are SMs
+// for, with two tiles each; else (trees: lengths differ from request to request) a few, with kMostTiles each.
+constexpr int kMaxSplit = 8, kMostTiles = 32, kMostCtas = 1024;
+void split_of(int64_t items, int64_t keys, int sms, int* split, int* least) {
+  *split = 1;
+  *least = 2;
+  while (*split < kMaxSplit && items * *split * 2 <= sms && keys > *split * 2 * kKeys) *split *= 2;
+  if (items * 2 <= sms) return;
+  *least = kMostTiles;
+  while (*split < kMaxSplit && items * *split * 2 <= kMostCtas && keys > *split * kMostTiles * kKeys) *split *= 2;
 }
 
 template <int D, bool SPLIT>
@@ -773,7 +778,7 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   const int64_t items = most_tiles(a, 2 * p.half_rows) * a.Hkv;
   if (a.tree_mask == nullptr && items > sms / 2) return launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)(items < sms ? items : sms), st);
-  p.split = split_of(items, most_keys(a, 2 * tokens), sms);
+  split_of(items, most_keys(a, 2 * tokens), sms, &p.split, &p.least);
   return launch_one<D, true>(maps, qmap, p, box_shift, (unsigned)(items * p.split), st);
 }
 

@@ -30,6 +30,16 @@ struct DeviceOnce {
   }
 };
 
+// SMs of the current device; 0 if a query fails.
+inline int device_sms() {
+  static DeviceOnce once;
+  static int sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (once.run(dev, [dev] { return cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev); }) != cudaSuccess) return 0;
+  return sms[dev];
+}
+
 // The tensor-core kernels' bounded waits on work of their own CTA (mbarrier phases of copies, MMAs
 // and hand-overs between warps) give up after about a second.  With the environment variable
 // KDA_TEST_WAIT_TIMEOUT set (any value but "" or "0"; read at every call) the launches use kernel

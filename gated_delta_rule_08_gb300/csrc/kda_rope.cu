@@ -7,10 +7,11 @@
 // itself.  Its top 32 bits, as a signed fraction of a turn, go to sincospi.  That is exact to 2^-32 of a turn for every
 // 32-bit position (F's own rounding, 2^-53 of it, adds at most |pos f| 2^-53).
 //
-// A unit of work is 16 values of one head of one token (two pieces of 16 bytes in bf16): eight pairs, or 16 values
-// to copy.  A block holds the cosines and sines of its tokens in shared memory, for all their heads; each thread
-// loads several units before it needs the first cosine.  Few tokens: a block has one, and its heads are spread
-// over several blocks, which all make the 64 cosines (a quarter of a microsecond) rather than wait for one another.
+// A warp has a token (for few tokens a part of its heads), each lane a unit of 16 values of a head (two pieces of 16
+// bytes in bf16): eight pairs, or 16 values to copy, the same ones in every head.  A lane makes the cosines and sines of
+// two pairs, gets those of its own eight from other lanes, and goes through the heads with them in registers; loads of
+// four heads are under way before it needs them, and no warp waits for another.  A lane's two frequencies are turned
+// into fixed point once, as a warp walks over tokens.
 //
 // Bound by HBM for many tokens: every value read once and written once.
 #include "kda_device.cuh"
@@ -19,26 +20,47 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 3;  // units a thread has under way
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kAhead = 4;  // heads a lane has under way
 
-struct Values {
-  float x[16];
-};
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 16 values of a lane, as they come
+template <typename T>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const __nv_bfloat16* a, const __nv_bfloat16* b) {
+    lo = __ldcs(reinterpret_cast<const uint4*>(a));
+    hi = __ldcs(reinterpret_cast<const uint4*>(b));
   }
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+  __device__ __forceinline__ void wide(float (&x)[16]) const {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Piece<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* a, const float* b) {
+    v[0] = __ldcs(reinterpret_cast<const float4*>(a));
+    v[1] = __ldcs(reinterpret_cast<const float4*>(a) + 1);
+    v[2] = __ldcs(reinterpret_cast<const float4*>(b));
+    v[3] = __ldcs(reinterpret_cast<const float4*>(b) + 1);
+  }
+  __device__ __forceinline__ void wide(float (&x)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = v[i].x;
+      x[4 * i + 1] = v[i].y;
+      x[4 * i + 2] = v[i].z;
+      x[4 * i + 3] = v[i].w;
+    }
+  }
+};
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&t);
@@ -46,125 +68,122 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
-
-// A unit's two pieces: eight values at `lo` and at `hi` of its head, and its first pair (-1: values to copy).
-struct Unit {
-  int lo, hi, pair;
-};
-template <bool ADJ>
-__device__ __forceinline__ Unit unit_of(int u, int rot, bool rotated) {
-  if (!rotated || 16 * u >= rot) return {16 * u, 16 * u + 8, -1};
-  return ADJ ? Unit{16 * u, 16 * u + 8, 8 * u} : Unit{8 * u, rot / 2 + 8 * u, 8 * u};
+// f / (2 pi) in 64-bit fixed point, without its whole turns
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  double turns = f * 0.15915494309189535;
+  turns -= floor(turns);
+  return turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
 }
 
-// TOK tokens a block; blockIdx.y: its part of their units
-template <typename Tin, int TOK, bool ADJ>
+template <typename Tin, bool ADJ>
 __global__ void __launch_bounds__(kThreads)
-rope_append_kernel(const RopeArgs p) {
-  __shared__ float cs[TOK][64], sn[TOK][64];
-  __shared__ int slots[TOK];
-  const int tid = threadIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.x * TOK;
-  const int per_head = p.d / 16, heads = p.H + 2 * p.Hkv, units = per_head * heads;
-  const int part = (units * TOK + gridDim.y - 1) / gridDim.y;  // units of this block
-  const int first = blockIdx.y * part, last = min(first + part, units * TOK);
+rope_append_kernel(const RopeArgs p, const int parts) {
+  const int lane = threadIdx.x & 31;
+  const int per_head = p.d / 16, at_once = 32 / per_head;  // lanes of a head, heads of a warp
+  const int u = lane % per_head, head0 = lane / per_head;
+  const int heads = p.H + 2 * p.Hkv, pairs = p.rot / 2;
+  // the lane's two pieces of a head, and its first pair
+  const bool turned = 16 * u < p.rot;
+  const int lo = turned && !ADJ ? 8 * u : 16 * u, hi = turned && !ADJ ? pairs + 8 * u : 16 * u + 8;
+  const int from = turned ? 4 * u : 0;  // the lane with the first two of its pairs, 8 u and 8 u + 1
 
-  Values v[kAhead];
-  // Every thread passes the barrier below, so the loads before it need no more than their own bounds.
-  auto fetch = [&](int at, Values& x) {
-    const int tok = at / units, r = at - tok * units, head = r / per_head, u = r - head * per_head;
-    const int64_t t = t0 + tok;
-    if (at >= last || t >= p.T) return;
-    const Unit w = unit_of<ADJ>(u, p.rot, head < p.H + p.Hkv);
-    const Tin* src = head < p.H ? static_cast<const Tin*>(p.q) + t * p.q_stride + (int64_t)head * p.d
-                     : head < p.H + p.Hkv ? static_cast<const Tin*>(p.k) + t * p.k_stride + (int64_t)(head - p.H) * p.d
-                                          : static_cast<const Tin*>(p.v) + t * p.v_stride + (int64_t)(head - p.H - p.Hkv) * p.d;
-    load8(src + w.lo, x.x);
-    load8(src + w.hi, x.x + 8);
-  };
+  uint64_t F[2] = {0, 0};
+  int axis[2] = {0, 0};
+  bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(first + tid + i * kThreads, v[i]);
-
-  const int pairs = p.rot / 2;
-  if (tid < TOK) {
-    const int64_t t = t0 + tid;
-    int s = t < p.T ? p.slot_map[t] : -1;
-    if (s < -1 || (int64_t)s >= (int64_t)p.num_blocks << p.shift) {
-      atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-      s = -1;
-    }
-    slots[tid] = s;
+  for (int i = 0; i < 2; ++i) {
+    const int j = 2 * lane + i;
+    if (j >= pairs) continue;
+    F[i] = turns_of(p.inv_freq[j]);
+    axis[i] = p.axis ? p.axis[j] : 0;
+    bad |= (unsigned)axis[i] >= (unsigned)p.axes;
   }
-  __syncthreads();
-  for (int i = tid; i < TOK * pairs; i += kThreads) {
-    const int tok = i / pairs, j = i - tok * pairs;
-    const int64_t t = t0 + tok;
-    if (t >= p.T) break;
-    const int a = p.axis ? p.axis[j] : 0;
-    if ((unsigned)a >= (unsigned)p.axes) {
-      atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-      slots[tok] = -1;
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+    return;
+  }
+  // this warp's heads: rounds of at_once
+  const int rounds = (heads + at_once - 1) / at_once, each = (rounds + parts - 1) / parts;
+  const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * kWarps;
+  for (int64_t w = warp; w < p.T * parts; w += warps) {
+    const int64_t t = parts == 1 ? w : w / parts;
+    const int first = parts == 1 ? 0 : (int)(w - t * parts) * each, end = min(first + each, rounds);
+    const int slot = p.slot_map[t];
+    if (slot < 0 || slot >= p.num_blocks << p.shift) {
+      if (slot != -1 && lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
       continue;
     }
-    // whole turns of the frequency itself do not matter
-    double turns = p.inv_freq[j] * 0.15915494309189535;
-    turns -= floor(turns);
-    const uint64_t F = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
-    const uint64_t x = (uint64_t)(int64_t)p.positions[(int64_t)a * p.T + t] * F;
-    const float half_turns = (float)(int32_t)(x >> 32) * 0x1p-31f;
-    sincospif(half_turns, &sn[tok][j], &cs[tok][j]);
-  }
-  __syncthreads();
+    const Tin* q = static_cast<const Tin*>(p.q) + t * p.q_stride;
+    const Tin* k = static_cast<const Tin*>(p.k) + t * p.k_stride - (int64_t)p.H * p.d;
+    const Tin* v = static_cast<const Tin*>(p.v) + t * p.v_stride - (int64_t)(p.H + p.Hkv) * p.d;
+    Piece<Tin> got[kAhead];
+    auto fetch = [&](int round, Piece<Tin>& x) {
+      const int head = round * at_once + head0;
+      if (round >= end || head >= heads) return;
+      const Tin* src = (head < p.H ? q : head < p.H + p.Hkv ? k : v) + (int64_t)head * p.d;
+      x.load(src + lo, src + hi);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(first + i, got[i]);
 
-  for (int base = first + tid; base < last; base += kAhead * kThreads) {
+    float c[2], s[2];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int at = base + i * kThreads;
-      if (at >= last) break;
-      const int tok = at / units, r = at - tok * units, head = r / per_head, u = r - head * per_head;
-      const int slot = slots[tok];
-      if (slot < 0) continue;
-      const bool rotated = head < p.H + p.Hkv;
-      const Unit w = unit_of<ADJ>(u, p.rot, rotated);
-      float* x = v[i].x;
-      if (w.pair >= 0) {
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t x = (uint64_t)(int64_t)p.positions[(int64_t)axis[i] * p.T + t] * F[i];
+      sincospif((float)(int32_t)(x >> 32) * 0x1p-31f, &s[i], &c[i]);
+    }
+    float cs[8], sn[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float c = cs[tok][w.pair + j], s = sn[tok][w.pair + j];
-          float &a = x[ADJ ? 2 * j : j], &b = x[ADJ ? 2 * j + 1 : 8 + j];
-          const float y = fmaf(a, c, -b * s);
-          b = fmaf(b, c, a * s);
-          a = y;
-        }
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, c[i & 1], from + i / 2);
+      sn[i] = __shfl_sync(0xffffffffu, s[i & 1], from + i / 2);
+      if (!turned) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
       }
-      const int64_t place = (int64_t)(slot >> p.shift) * p.block_stride + (int64_t)(slot & ((1 << p.shift) - 1)) * p.token_stride;
-      __nv_bfloat16* dst = head < p.H ? static_cast<__nv_bfloat16*>(p.q_out) + ((t0 + tok) * p.H + head) * p.d
-                           : rotated ? static_cast<__nv_bfloat16*>(p.k_cache) + place + (head - p.H) * p.head_stride
-                                     : static_cast<__nv_bfloat16*>(p.v_cache) + place + (head - p.H - p.Hkv) * p.head_stride;
-      store8(dst + w.lo, x);
-      store8(dst + w.hi, x + 8);
     }
-    if (base + kAhead * kThreads < last) {
+    __nv_bfloat16* q_out = static_cast<__nv_bfloat16*>(p.q_out) + t * p.H * p.d;
+    const int64_t place = (int64_t)(slot >> p.shift) * p.block_stride + (int64_t)(slot & ((1 << p.shift) - 1)) * p.token_stride;
+    __nv_bfloat16* k_to = static_cast<__nv_bfloat16*>(p.k_cache) + place;
+    __nv_bfloat16* v_to = static_cast<__nv_bfloat16*>(p.v_cache) + place;
+    for (int round = first; round < end; round += kAhead) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(base + (kAhead + i) * kThreads, v[i]);
+      for (int i = 0; i < kAhead; ++i) {
+        const int head = (round + i) * at_once + head0;
+        if (round + i >= end || head >= heads) break;
+        float x[16];
+        got[i].wide(x);
+        fetch(round + i + kAhead, got[i]);
+        const bool rotated = head < p.H + p.Hkv;
+        if (rotated && turned) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float &a = x[ADJ ? 2 * j : j], &b = x[ADJ ? 2 * j + 1 : 8 + j];
+            const float y = fmaf(a, cs[j], -b * sn[j]);
+            b = fmaf(b, cs[j], a * sn[j]);
+            a = y;
+          }
+        }
+        __nv_bfloat16* dst = head < p.H ? q_out + head * p.d
+                             : rotated ? k_to + (head - p.H) * p.head_stride
+                                       : v_to + (head - p.H - p.Hkv) * p.head_stride;
+        store8(dst + lo, x);
+        store8(dst + hi, x + 8);
+      }
     }
   }
 }
 
-template <typename Tin, int TOK, bool ADJ>
-cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
-  const int units = a.d / 16 * (a.H + 2 * a.Hkv);
-  const int64_t blocks = (a.T + TOK - 1) / TOK;
-  const unsigned parts = TOK == 1 ? (unsigned)((units + kThreads - 1) / kThreads) : 1;
-  rope_append_kernel<Tin, TOK, ADJ><<<dim3((unsigned)blocks, parts), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-// One token a block while that leaves SMs idle.
-constexpr int kFewTokens = 1024;
+// Few tokens: the heads of one over several warps.  Many: kBlocks blocks an SM walk over them.
+constexpr int kBlocks = 4, kFewTokens = 512;
 template <typename Tin, bool ADJ>
 cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
-  return a.T <= kFewTokens ? launch<Tin, 1, ADJ>(a, st) : launch<Tin, 4, ADJ>(a, st);
+  const int sms = device_sms();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int parts = a.T <= kFewTokens ? 4 : 1;
+  const int64_t blocks = (a.T * parts + kWarps - 1) / kWarps, most = (int64_t)sms * kBlocks;
+  rope_append_kernel<Tin, ADJ><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, st>>>(a, parts);
+  return cudaGetLastError();
 }
 
 }  // namespace
