@@ -40,7 +40,7 @@ struct Layout {
   static constexpr uint32_t kSums = kIn + kRows * D * 4;   // [kWarps][16] references and sums of weights of the warps,
   static constexpr uint32_t kAll = kSums + kWarps * kRows * 8;  // [kMaxSplit][16] of the CTAs
   static constexpr uint32_t kBar = kAll + kMaxSplit * kRows * 8;
-  static constexpr uint32_t kSmem = kBar + kWarps * kStages * 8 + 16 + 1024;
+  static constexpr uint32_t kSmem = kBar + kWarps * kStages * 8 + 8 + 1024;
   static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums take its ring's place");
 };
 

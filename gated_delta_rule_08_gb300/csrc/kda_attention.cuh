@@ -49,6 +49,7 @@ struct Params {
   unsigned int* err;
   int waits;                 // enum Waits
   int split;                 // CTAs (a cluster) that may share a tile's keys: those past parts_of() leave at once
+  int ordered;               // take the requests by falling length
   int least;                 // boxes (tc: tiles) for each of them at least
 };
 
@@ -127,23 +128,39 @@ struct Tile {
 struct Walk {
   int base = 0;     // request of lane 0
   int tiles = 0;    // tiles of the requests before it
+  const uint8_t* order = nullptr;  // requests in the order to take them in, or null
 };
+// The requests by falling length, for tiles that start in order and take as long as their requests (all threads of the CTA,
+// at most kMostOrdered requests; a barrier before the order is read).
+constexpr int kMostOrdered = 64;
+__device__ __forceinline__ void order_by_length(const int32_t* __restrict__ lengths, int N, uint8_t* order) {
+  const int i = threadIdx.x;
+  if (i >= N) return;
+  const int n = lengths[i];
+  int rank = 0;
+  for (int j = 0; j < N; ++j) {
+    const int m = lengths[j];
+    rank += m > n || (m == n && j < i);
+  }
+  order[rank] = (uint8_t)i;
+}
 __device__ __forceinline__ bool locate(const Params& p, int per, Divisor by_per, int item, Walk& w, Tile& t) {
   const int lane = threadIdx.x & 31;
   const int tile = p.by_Hkv.div(item);
   t.head = item - tile * p.Hkv;
   int k;
   if (p.cu == nullptr) {
-    t.n = p.by_each.div(tile);
-    if (t.n >= p.N) return false;
+    const int i = p.by_each.div(tile);
+    if (i >= p.N) return false;
+    t.n = w.order ? w.order[i] : i;
     t.t0 = t.n;
     t.tokens = 1;
-    k = tile - t.n * (int)p.by_each.d;
+    k = tile - i * (int)p.by_each.d;
   } else {
     while (true) {
       if (w.base >= p.N) return false;
-      const int n = w.base + lane;
-      const int a = n < p.N ? p.cu[n] : 0, b = n < p.N ? p.cu[n + 1] : 0;
+      const int i = w.base + lane, n = i < p.N && w.order ? w.order[i] : i;
+      const int a = i < p.N ? p.cu[n] : 0, b = i < p.N ? p.cu[n + 1] : 0;
       int sum = by_per.div((b - a) * p.G + per - 1);  // (T H and a tile's rows are below 2^31 together)
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -154,7 +171,7 @@ __device__ __forceinline__ bool locate(const Params& p, int per, Divisor by_per,
       if (tile < w.tiles + all) {
         const unsigned over = __ballot_sync(0xffffffffu, w.tiles + sum > tile);
         const int src = __ffs(over) - 1;
-        t.n = w.base + src;
+        t.n = __shfl_sync(0xffffffffu, n, src);
         t.t0 = __shfl_sync(0xffffffffu, a, src);
         t.tokens = __shfl_sync(0xffffffffu, b - a, src);
         // a request's last tile first: it sees the most keys
@@ -209,7 +226,7 @@ __device__ __forceinline__ Row row_keys(const Params& p, const Tile& t, int toke
   r.hi = p.cu == nullptr ? t.len - 1 : pos;
   if (p.mask) {
     r.mask = p.mask + (int64_t)(t.t0 + token) * p.mask_words;
-    pos = t.before + mask_count(p, t, token) - 1;
+    if (p.window > 0) pos = t.before + mask_count(p, t, token) - 1;
     r.hi = t.before - 1;
   }
   const int64_t lo = p.window > 0 ? (int64_t)pos + 1 - p.window : 0;
@@ -230,13 +247,15 @@ __device__ __forceinline__ Span span_of(const Params& p, const Tile& t, int a, i
   int64_t lo, all_lo;
   if (p.mask) {
     int least = 1 << 30, most = 0;
-    for (int i = a + (threadIdx.x & 31); i < b; i += 32) {
-      const int m = mask_count(p, t, i);
-      least = min(least, m);
-      most = max(most, m);
+    if (p.window > 0) {
+      for (int i = a + (threadIdx.x & 31); i < b; i += 32) {
+        const int m = mask_count(p, t, i);
+        least = min(least, m);
+        most = max(most, m);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
     }
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
     s.hi = t.len - 1;
     s.all_hi = t.before - 1;
     lo = p.window > 0 ? (int64_t)t.before + least - p.window : 0;

@@ -29,7 +29,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 11;  // (MMAs: two warps)
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr int kHalf = 128, kKeys = 128;
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
@@ -42,13 +42,13 @@ struct Layout {
   static constexpr int kParts = D / 64;
   static constexpr uint32_t kPart = kKeys * 128;             // 64 values of 128 rows
   static constexpr uint32_t kTile = kParts * kPart;
-  static constexpr int kStages = (SPLIT ? 5 : 4) * (2 / kParts);
+  static constexpr int kStages = 5 * (2 / kParts);
   static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
   static constexpr uint32_t kBar = kRing + kStages * kTile;
   static constexpr uint32_t kOut = kBar + 512;               // 4 KB a softmax warp: 64 values of its 32 rows (not SPLIT)
-  static constexpr uint32_t kSmem = kOut + (SPLIT ? 0 : 8 * 4096) + 1024;
+  static constexpr uint32_t kSmem = kOut + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
-  static_assert((2 * kStages + 20) * 8 <= 512, "barriers");
+  static_assert((2 * kStages + 20) * 8 + kMostOrdered <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
 };
 
@@ -66,6 +66,17 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
       : "memory");
+}
+// 32 bytes of a row, at once where the output begins on 32 bytes (a sector of L2; its rows are multiples of that).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
 }
 __device__ __forceinline__ void tma_prefetch_rows(const CUtensorMap* map, int x, int head, int token) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(head), "r"(token)
@@ -196,6 +207,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   uint64_t* bar_fin = q_full + 12;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* order = reinterpret_cast<uint8_t*>(tmem_slot + 2);  // [kMostOrdered]
   // reference and sum of weights of 256 rows, in Q's place once the item's products are done (SPLIT)
   float2* sums = reinterpret_cast<float2*>(sm);
 
@@ -209,6 +221,11 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   }
   // Items of this CTA: every role walks them by itself, one ahead.
   Walk walk;
+  if (SPLIT && p.ordered) {
+    order_by_length(p.lengths, p.N, order);
+    __syncthreads();
+    walk.order = order;
+  }
   int at = SPLIT ? blockIdx.x / p.split : blockIdx.x;
   const int step = SPLIT ? 0x40000000 : gridDim.x;
   auto next = [&](Item& it) {
@@ -366,7 +383,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       if (!ok) break;
       ++items;
       tc_fence_after();
-      if (SPLIT) {
+      if (SPLIT && split > 1) {
         // sums into the ring (all its tiles have been read), pieces of 16 bytes permuted by the row
         const int rr = h * kHalf + row;
         uint8_t* dst = sm + L::kRing + (uint32_t)rr * (D * 4);
@@ -388,41 +405,32 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         break;  // one item
       }
       if (rows > 0) {
-        // by way of shared memory, so that whole lines are written: 64 values of the warp's rows at a time
         const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
-        uint8_t* stage = sm + L::kOut + warp * 4096;
-        // rows 4 k + lane / 8 of the warp, and where they go
-        const int row8 = (warp & 3) * 32 + lane / 8;
-        __nv_bfloat16* dst[8];
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        const int tok = p.by_G.div(r);
+        __nv_bfloat16* dst = p.out + ((int64_t)(it.t.t0 + tok) * p.H + (it.t.head * G + r - tok * G)) * D;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int q = it.t.first + h * half_rows + row8 + 4 * k, tok = p.by_G.div(q);
-          dst[k] = p.out + ((int64_t)(it.t.t0 + tok) * p.H + (it.t.head * G + q - tok * G)) * D + lane % 8 * 8;
-        }
-#pragma unroll
-        for (int i = 0; i < L::kParts; ++i) {
+        for (int i = 0; i < D; i += 64) {
           float o[2][32];
           if (any) {
-            tmem_ld32(to + 64 * i, o[0]);
-            tmem_ld32(to + 64 * i + 32, o[1]);
+            tmem_ld32(to + i, o[0]);
+            tmem_ld32(to + i + 32, o[1]);
             tmem_landed(o[0]);
             tmem_landed(o[1]);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[0][e] = o[1][e] = 0.f;
           }
+          if (live) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* x = &o[k / 4][k % 4 * 8];
-            *reinterpret_cast<uint4*>(stage + row_chunk(lane, k)) =
-                make_uint4(pack_bf2(x[0] * inv, x[1] * inv), pack_bf2(x[2] * inv, x[3] * inv), pack_bf2(x[4] * inv, x[5] * inv),
-                           pack_bf2(x[6] * inv, x[7] * inv));
+            for (int k = 0; k < 4; ++k) {
+              const float* x = &o[k / 2][k % 2 * 16];
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = pack_bf2(x[2 * e] * inv, x[2 * e + 1] * inv);
+              store32(dst + i + 16 * k, u, wide);
+            }
           }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (row8 + 4 * k < rows)
-              *reinterpret_cast<uint4*>(dst[k] + 64 * i) = *reinterpret_cast<const uint4*>(stage + row_chunk(4 * k + lane / 8, lane & 7));
           __syncwarp();
         }
         tc_fence_before();  // O is read before the next item's weights are told
@@ -680,11 +688,11 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   }
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
-  if (!SPLIT) return;
+  if (!SPLIT || split == 1) return;
 
   // the cluster's CTAs join: each a part of the rows
   if (*abort_flag && tid < 256) sums[tid] = make_float2(kLowest, kGone);
-  walk = Walk{};
+  walk.base = walk.tiles = 0;
   at = blockIdx.x / p.split;
   next(coming);
   cluster_sync();
@@ -701,8 +709,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       const uint8_t* src = sm + L::kRing + (uint32_t)rr * (D * 4);
       const uint32_t pa = (uint32_t)(x / 4 ^ (rr & (D / 4 - 1))) << 4, pb = (uint32_t)((x / 4 + 1) ^ (rr & (D / 4 - 1))) << 4;
       bool lost = false;
-#pragma unroll 1
-      for (int k = 0; k < split; k += 2) {  // two CTAs' parts under way at a time
+#pragma unroll 2
+      for (int k = 0; k < split; k += 2) {  // (the loads of several parts under way at a time)
         const float2 s0 = ld_peer2(peer(sums + rr, k)), s1 = ld_peer2(peer(sums + rr, min(k + 1, split - 1)));
         const float4 a0 = ld_peer4(peer(src + pa, k)), b0 = ld_peer4(peer(src + pb, k));
         const float4 a1 = ld_peer4(peer(src + pa, min(k + 1, split - 1))), b1 = ld_peer4(peer(src + pb, min(k + 1, split - 1)));
@@ -779,6 +787,7 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   const int64_t items = most_tiles(a, 2 * p.half_rows) * a.Hkv;
   if (a.tree_mask == nullptr && items > sms / 2) return launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)(items < sms ? items : sms), st);
   split_of(items, most_keys(a, 2 * tokens), sms, &p.split, &p.least);
+  p.ordered = a.N > 1 && a.N <= kMostOrdered && items * p.split > sms;
   return launch_one<D, true>(maps, qmap, p, box_shift, (unsigned)(items * p.split), st);
 }
 
