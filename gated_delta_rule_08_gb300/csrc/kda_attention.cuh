@@ -115,6 +115,7 @@ __device__ __forceinline__ bool offsets_within(const int32_t* __restrict__ cu, i
   return !__syncthreads_or(bad);
 }
 
+constexpr int kMaxLength = 1 << 30;  // tokens of a request: 32-bit places of keys run some tiles past it
 // A tile of rows of one request and key head.
 struct Tile {
   int n, head;         // request, key head
@@ -186,7 +187,7 @@ __device__ __forceinline__ bool locate(const Params& p, int per, Divisor by_per,
   t.before = t.len - t.tokens;
   t.first = k * per;
   t.rows = min(t.tokens * p.G - t.first, per);
-  bool bad = t.len < 0 || (int64_t)t.len > ((int64_t)p.max_blocks << p.shift);
+  bool bad = t.len < 0 || t.len > kMaxLength || (int64_t)t.len > ((int64_t)p.max_blocks << p.shift);
   if (p.cu == nullptr) {
     if (t.len == 0) t.before = 0;  // no key: a row of zeros
   } else {

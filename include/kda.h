@@ -376,7 +376,7 @@ kda_status kda_rope_append(const void* q, const void* k, const void* v, const do
  *   lengths      : [N] int32, tokens of request n in the cache, its new ones included
  *   cu_seqlens   : [N + 1] int32, where each request's new tokens begin in q; they are its last ones.  Offsets that do not
  *                  rise from 0 to at most T set KDA_DEVERR_BAD_SEQLENS, and nothing is written; a request of more new
- *                  tokens than its length, or longer than max_blocks * block_size, sets it and is skipped.  Rows of
+ *                  tokens than its length, or longer than max_blocks * block_size or 2^30, sets it and is skipped.  Rows of
  *                  out behind the last request are left as they were
  *   window       : tokens a token sees, itself included; 0 means all.  sinks >= 0: first tokens that stay visible
  *   max_length   : no request is longer (a hint for how the work is split; 0: as long as the tables allow)
