@@ -2,7 +2,8 @@
 
 Every function here checks shapes/dtypes/devices of torch tensors, passes their
 device pointers and the current CUDA stream to the C-ABI entry point of the same
-name (include/kda.h), and raises on a non-OK status.  No arithmetic of the method
+name (include/kda.h), and raises on a non-OK status (the attention layer's operators
+do so in csrc/kda_marshal.cpp).  No arithmetic of the method
 happens in Python.  There is no fallback: without a built libkda.so or a CUDA
 device the calls raise.
 """
@@ -712,15 +713,24 @@ def kda_linear_decode_step(q, k, v, g, state_pool, slot_idx, out=None, *, scale:
 
 
 # ------------------------------------------------------------- an attention layer over a paged cache
-_CacheStrides = ctypes.c_int64 * 3
+# Marshalled by a module of C++ (csrc/kda_marshal.cpp): a step of such a layer for a few tokens takes some five
+# microseconds on the device, and checks and allocations in Python would take twice that.
+_marshal = None
 
 
-def _data_or_new(t, name: str, dtype, shape, like: torch.Tensor, index: int):
-    """`t`, checked, or a new tensor on `like`'s device."""
-    if t is None:
-        return torch.empty(shape, device=like.device, dtype=dtype)
-    _data(t, name, dtype, shape, index)
-    return t
+def _load_marshal():
+    """The marshalling module, with the entry points of the loaded library (raises if it has not been built)."""
+    global _marshal
+    lib = load_library()
+    try:
+        from . import _kda_marshal as module
+    except ImportError as e:
+        raise RuntimeError("the marshalling module is not built; run __graft_entry__.build()") from e
+    names = ("kda_block_tables", "kda_rope_append", "kda_window_attention_fwd", "kda_window_attention_decode_step",
+             "kda_tree_attention")
+    module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, KdaError)
+    _marshal = module
+    return module
 
 
 def kda_block_tables(counts, lengths, block_tables, free_ring, free_state, *, block_size: int, max_tokens: int,
@@ -730,50 +740,8 @@ def kda_block_tables(counts, lengths, block_tables, free_ring, free_state, *, bl
     in place; free_state: [2], the ring's head and number of free blocks.  new_lengths may be lengths and
     new_free_state free_state (in place); by default they are new tensors.  At most max_tokens tokens are gained.
     Returns (slot_map [max_tokens], positions [max_tokens], cu_seqlens [N + 1], new_lengths, new_free_state)."""
-    lib = _lib or load_library()
-    dev = _device_index(block_tables, "block_tables")
-    i32 = torch.int32
-    N, width = block_tables.shape
-    pc = _data(counts, "counts", i32, (N,), dev)
-    pl = _data(lengths, "lengths", i32, (N,), dev)
-    pt = _data(block_tables, "block_tables", i32, (N, width), dev)
-    blocks = free_ring.shape[0]
-    pr = _data(free_ring, "free_ring", i32, (blocks,), dev)
-    pf = _data(free_state, "free_state", i32, (2,), dev)
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
-    new_lengths = _data_or_new(new_lengths, "new_lengths", i32, (N,), block_tables, dev)
-    new_free_state = _data_or_new(new_free_state, "new_free_state", i32, (2,), block_tables, dev)
-    slot_map = _data_or_new(slot_map, "slot_map", i32, (max_tokens,), block_tables, dev)
-    positions = _data_or_new(positions, "positions", i32, (max_tokens,), block_tables, dev)
-    cu_seqlens = _data_or_new(cu_seqlens, "cu_seqlens", i32, (N + 1,), block_tables, dev)
-    st = lib.kda_block_tables(pc, pl, pt, pr, pf, new_lengths.data_ptr(), new_free_state.data_ptr(), slot_map.data_ptr(),
-                              positions.data_ptr(), cu_seqlens.data_ptr(), N, width, blocks, block_size, max_tokens,
-                              _raw_stream(dev))
-    if st != 0:
-        raise KdaError("kda_block_tables", st)
-    return slot_map, positions, cu_seqlens, new_lengths, new_free_state
-
-
-def _caches(k_cache, v_cache, index: int):
-    """Shape and strides of the two caches [num_blocks, block_size, Hkv, d], which have to be alike."""
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, Hkv, d]")
-    bf16 = torch.bfloat16
-    if not (k_cache.dtype is bf16 and v_cache.dtype is bf16 and k_cache.get_device() == index == v_cache.get_device()):
-        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            if t.dtype is not bf16:
-                raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-            if t.get_device() != index:
-                raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    strides = k_cache.stride()
-    if strides[3] != 1 or v_cache.stride() != strides:
-        raise ValueError("k_cache and v_cache must have the same strides, and dense heads")
-    blocks, size, heads, d = shape
-    # (the stride of a dimension of one says nothing)
-    return shape, _CacheStrides(strides[0] if blocks != 1 else d, strides[1] if size != 1 else d,
-                                strides[2] if heads != 1 else d)
+    return (_marshal or _load_marshal()).block_tables(counts, lengths, block_tables, free_ring, free_state, block_size, max_tokens,
+                                                      new_lengths, new_free_state, slot_map, positions, cu_seqlens)
 
 
 def kda_rope_append(q, k, v, inv_freq, positions, slot_map, k_cache, v_cache, *, axis=None, interleaved: bool = False,
@@ -783,44 +751,8 @@ def kda_rope_append(q, k, v, inv_freq, positions, slot_map, k_cache, v_cache, *,
     positions: int32 [T] or [axes, T]; slot_map: int32 [T] (a token with -1 is skipped); k_cache, v_cache:
     [num_blocks, block_size, Hkv, d] bf16, updated in place.  Pairs are values i and i + rot / 2, or 2 i and 2 i + 1 if
     interleaved.  Returns the rotated q [T, H, d] bf16."""
-    lib = _lib or load_library()
-    code = _code(q)
-    dev = _device_index(q, "q")
-    T, H, d = q.shape
-    shape, strides = _caches(k_cache, v_cache, dev)
-    Hkv, dt = shape[2], q.dtype
-    if shape[3] != d:
-        raise ValueError(f"the cache's heads have {shape[3]} values, q's {d}")
-    qs = _token_rows(q, "q", dt, (T, H, d), dev)
-    ks = _token_rows(k, "k", dt, (T, Hkv, d), dev)
-    vs = _token_rows(v, "v", dt, (T, Hkv, d), dev)
-    pairs = inv_freq.numel()
-    pi = _data(inv_freq, "inv_freq", torch.float64, (pairs,), dev)
-    pa = _data(axis, "axis", torch.int32, (pairs,), dev)
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    pp = _data(positions, "positions", torch.int32, (axes, T) if positions.dim() == 2 else (T,), dev)
-    ps = _data(slot_map, "slot_map", torch.int32, (T,), dev)
-    q_out = _data_or_new(q_out, "q_out", torch.bfloat16, (T, H, d), q, dev)
-    st = lib.kda_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), pi, pa, pp, ps, q_out.data_ptr(), k_cache.data_ptr(),
-                             v_cache.data_ptr(), T, H, Hkv, d, 2 * pairs, axes, interleaved, qs, ks, vs, shape[0], shape[1],
-                             strides, code, _raw_stream(dev))
-    if st != 0:
-        raise KdaError("kda_rope_append", st)
-    return q_out
-
-
-def _attention_args(q, k_cache, v_cache, block_tables, lengths, out):
-    dev = _device_index(q, "q")
-    T, H, d = q.shape
-    shape, strides = _caches(k_cache, v_cache, dev)
-    if shape[3] != d:
-        raise ValueError(f"the cache's heads have {shape[3]} values, q's {d}")
-    N, width = block_tables.shape
-    qs = _token_rows(q, "q", torch.bfloat16, (T, H, d), dev)
-    pt = _data(block_tables, "block_tables", torch.int32, (N, width), dev)
-    pl = _data(lengths, "lengths", torch.int32, (N,), dev)
-    out = _data_or_new(out, "out", torch.bfloat16, (T, H, d), q, dev)
-    return dev, out, pt, pl, N, T, H, shape[2], d, qs, shape[0], shape[1], width, strides
+    return (_marshal or _load_marshal()).rope_append(q, k, v, inv_freq, positions, slot_map, k_cache, v_cache, axis, interleaved,
+                                                     q_out)
 
 
 def kda_window_attention_fwd(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out=None, *, window: int = 0,
@@ -830,33 +762,15 @@ def kda_window_attention_fwd(q, k_cache, v_cache, block_tables, lengths, cu_seql
     v_cache: [num_blocks, block_size, Hkv, d] bf16; block_tables: int32 [N, max_blocks]; lengths: int32 [N], the new
     tokens included; cu_seqlens: int32 [N + 1] (rows behind its last are left); scale: d ** -0.5 unless given;
     max_length: no request is longer (a hint).  Returns out [T, H, d] bf16."""
-    lib = _lib or load_library()
-    dev, out, pt, pl, N, T, H, Hkv, d, qs, blocks, size, width, strides = _attention_args(q, k_cache, v_cache, block_tables,
-                                                                                         lengths, out)
-    pcu = _data(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    st = lib.kda_window_attention_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pt, pl, pcu, out.data_ptr(), N, T,
-                                      H, Hkv, d, qs, blocks, size, width, strides, window, sinks, max_length,
-                                      d ** -0.5 if scale is None else scale, _raw_stream(dev))
-    if st != 0:
-        raise KdaError("kda_window_attention_fwd", st)
-    return out
+    return (_marshal or _load_marshal()).window_fwd(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out, window, sinks, scale,
+                                                    max_length)
 
 
 def kda_window_attention_decode_step(q, k_cache, v_cache, block_tables, lengths, out=None, *, window: int = 0,
                                      sinks: int = 0, scale: Optional[float] = None, max_length: int = 0):
     """kda_window_attention_fwd for one new token of each request: q [N, H, d], at position lengths[n] - 1.  A request of
     length 0 gets zeros.  Returns out [N, H, d] bf16."""
-    lib = _lib or load_library()
-    dev, out, pt, pl, N, T, H, Hkv, d, qs, blocks, size, width, strides = _attention_args(q, k_cache, v_cache, block_tables,
-                                                                                         lengths, out)
-    if T != N:
-        raise ValueError(f"q has {T} tokens for {N} requests")
-    st = lib.kda_window_attention_decode_step(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pt, pl, out.data_ptr(), N,
-                                              H, Hkv, d, qs, blocks, size, width, strides, window, sinks, max_length,
-                                              d ** -0.5 if scale is None else scale, _raw_stream(dev))
-    if st != 0:
-        raise KdaError("kda_window_attention_decode_step", st)
-    return out
+    return (_marshal or _load_marshal()).window_step(q, k_cache, v_cache, block_tables, lengths, out, window, sinks, scale, max_length)
 
 
 def kda_tree_attention(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, tree_mask, out=None, *, window: int = 0,
@@ -865,15 +779,5 @@ def kda_tree_attention(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, t
     [T, words], bit j % 64 of word j / 64 saying that a token sees drafted token j of its request (its ancestors
     and itself); of the tokens before the drafted ones it sees what kda_window_attention_fwd shows at its depth.
     Returns out [T, H, d] bf16."""
-    lib = _lib or load_library()
-    dev, out, pt, pl, N, T, H, Hkv, d, qs, blocks, size, width, strides = _attention_args(q, k_cache, v_cache, block_tables,
-                                                                                         lengths, out)
-    pcu = _data(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    words = tree_mask.shape[1]
-    pm = _data(tree_mask, "tree_mask", torch.int64, (T, words), dev)
-    st = lib.kda_tree_attention(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pt, pl, pcu, pm, words, out.data_ptr(), N,
-                                T, H, Hkv, d, qs, blocks, size, width, strides, window, sinks, max_length,
-                                d ** -0.5 if scale is None else scale, _raw_stream(dev))
-    if st != 0:
-        raise KdaError("kda_tree_attention", st)
-    return out
+    return (_marshal or _load_marshal()).tree(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, tree_mask, out, window, sinks,
+                                              scale, max_length)

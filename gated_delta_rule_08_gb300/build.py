@@ -1,7 +1,8 @@
 """Builds libkda.so in-tree with nvcc for sm_103a (no CMake, no torch extension).
 
 Each .cu file under csrc/ is compiled in parallel to an object, then linked into
-gated_delta_rule_08_gb300/libkda.so (CUDA runtime linked statically).
+gated_delta_rule_08_gb300/libkda.so (CUDA runtime linked statically).  Beside it, g++ builds
+the Python module that marshals the attention layer's operators, against the installed torch.
 """
 from __future__ import annotations
 
@@ -11,10 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda.so")
+MARSHAL = os.path.join(PKG, "_kda_marshal.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -35,6 +38,18 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _marshal_command(target: str) -> list:
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [*cpp_extension.include_paths(), sysconfig.get_path("include"), os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in includes),
+            os.path.join(CSRC, "kda_marshal.cpp"), *("-L" + p for p in cpp_extension.library_paths()),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", target]
+
+
 def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -52,6 +67,12 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = Fa
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    marshal = f"{MARSHAL}.tmp{os.getpid()}"
+    remake = force or _stale(MARSHAL, [os.path.join(CSRC, "kda_marshal.cpp"), headers[-1]])
+    compiled = list(jobs)
+    if remake:
+        jobs.append(_marshal_command(marshal))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -61,8 +82,10 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = Fa
             if verbose or r.returncode != 0 or ptxas_v:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}")
-    if force or jobs or _stale(LIB, objs):
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-1]}")
+    if remake:
+        os.replace(marshal, MARSHAL)
+    if force or compiled or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
         r = subprocess.run(cmd, capture_output=True, text=True)
