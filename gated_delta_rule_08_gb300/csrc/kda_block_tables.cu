@@ -18,7 +18,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024, kFewThreads = 256;  // (a CTA of fewer warps starts sooner)
 constexpr int kCluster = 8;
 constexpr int kPerCta = 8192;  // tokens that one CTA handles before the others are worth their start
 
@@ -51,7 +51,7 @@ __device__ __forceinline__ void cluster_sync() {
 __global__ void __launch_bounds__(kThreads)
 block_tables_kernel(const BlockTablesArgs p) {
   extern __shared__ int32_t sm[];
-  __shared__ Sums warp_sums[kThreads / 32];
+  __shared__ Sums warp_sums[32];
   const int N = p.N, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* first = sm;              // first new token of each request
   int32_t* taken = first + N + 1;   // blocks taken by the requests before
@@ -63,7 +63,7 @@ block_tables_kernel(const BlockTablesArgs p) {
 
   Sums sum{0, 0, 0};  // of the requests before this round's
   bool bad = head < 0 || head >= p.num_blocks || free < 0 || free > p.num_blocks;
-  for (int base = 0; base < N; base += kThreads) {
+  for (int base = 0; base < N; base += (int)blockDim.x) {
     const int n = base + tid;
     Sums own{0, 0, 0};
     if (n < N) {
@@ -84,12 +84,19 @@ block_tables_kernel(const BlockTablesArgs p) {
     }
     if (lane == 31) warp_sums[warp] = scan;
     __syncthreads();
-    Sums before = sum;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before = before + warp_sums[w];
-      sum = sum + warp_sums[w];
+    if (warp == 0) {  // the warps' sums likewise
+      Sums s = lane < (int)blockDim.x / 32 ? warp_sums[lane] : Sums{0, 0, 0};
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const Sums up = shfl_up(s, o);
+        if (lane >= o) s = s + up;
+      }
+      warp_sums[lane] = s;
     }
     __syncthreads();
+    const Sums before = warp == 0 ? sum : sum + warp_sums[warp - 1];
+    sum = sum + warp_sums[31];
+    if (base + (int)blockDim.x < N) __syncthreads();
     if (n < N) {  // tokens past 2^31 - 1 have no use: the step does nothing then
       first[n] = (int)(before.tokens + scan.tokens - own.tokens);
       taken[n] = (int)(before.taken + scan.taken - own.taken);
@@ -99,31 +106,32 @@ block_tables_kernel(const BlockTablesArgs p) {
   bad = __syncthreads_or(bad) || sum.tokens > p.T || (int64_t)free + sum.given > p.num_blocks;
   const bool few = !bad && sum.taken > (uint32_t)free;
   const int total = bad || few ? 0 : (int)sum.tokens;
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int cta = blockIdx.x, ctas = gridDim.x, threads = blockDim.x;
   bool bad_block = false;
 
   // slots and positions, four tokens a thread
-  for (int64_t t0 = ((int64_t)cta * kThreads + tid) * 4; t0 < p.T; t0 += (int64_t)ctas * kThreads * 4) {
-    int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0};
+  for (int64_t t0 = ((int64_t)cta * threads + tid) * 4; t0 < p.T; t0 += (int64_t)ctas * threads * 4) {
+    int slot[4] = {-1, -1, -1, -1}, pos[4] = {0, 0, 0, 0}, block[4];
+    int32_t* entry[4] = {};  // where a new block goes
     int n = t0 < total ? find(first, N, (int)t0) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {  // (all loads before a store, which they could not pass)
       const int t = (int)t0 + i;
       if (t >= total) break;
       while (n + 1 < N && first[n + 1] <= t) ++n;
       const int x = length[n] + (t - first[n]), b = x >> p.shift, held = (length[n] + round) >> p.shift;
-      int32_t* entry = p.block_tables + (int64_t)n * p.max_blocks + b;
-      int block;
-      if (b >= held) {
-        int at = head + taken[n] + (b - held);
-        at = at >= p.num_blocks ? at - p.num_blocks : at;
-        block = p.free_ring[at];
-        if ((x & round) == 0) *entry = block;
-      } else {
-        block = *entry;
-      }
+      int32_t* mine = p.block_tables + (int64_t)n * p.max_blocks + b;
+      int at = head + taken[n] + (b - held);
+      at = at >= p.num_blocks ? at - p.num_blocks : at;
+      block[i] = *(b >= held ? p.free_ring + at : mine);
+      if (b >= held && (x & round) == 0) entry[i] = mine;
       pos[i] = x;
-      if ((unsigned)block < (unsigned)p.num_blocks) slot[i] = (block << p.shift) + (x & round);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((int)t0 + i >= total) break;
+      if (entry[i]) *entry[i] = block[i];
+      if ((unsigned)block[i] < (unsigned)p.num_blocks) slot[i] = (block[i] << p.shift) + (pos[i] & round);
       else bad_block = true;
     }
     if (t0 + 3 < p.T) {
@@ -138,7 +146,7 @@ block_tables_kernel(const BlockTablesArgs p) {
   }
   // blocks given back, behind those that are free
   if (!bad && !few) {
-    for (int r = cta * kThreads + tid; r < (int)sum.given; r += ctas * kThreads) {
+    for (int r = cta * threads + tid; r < (int)sum.given; r += ctas * threads) {
       const int n = find(given, N, r);
       // (the length after the step: the row keeps its first blocks)
       const int after = (int)(((int64_t)length[n] + p.counts[n] + round) >> p.shift);
@@ -152,7 +160,7 @@ block_tables_kernel(const BlockTablesArgs p) {
   if (bad_block) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
 
   if (ctas > 1) cluster_sync(); else __syncthreads();
-  for (int n = cta * kThreads + tid; n <= N; n += ctas * kThreads) {
+  for (int n = cta * threads + tid; n <= N; n += ctas * threads) {
     p.cu_seqlens[n] = total == 0 ? 0 : n < N ? first[n] : total;
     if (n < N) p.new_lengths[n] = bad || few ? length[n] : length[n] + p.counts[n];
   }
@@ -183,7 +191,7 @@ cudaError_t block_tables_launch(const BlockTablesArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   const unsigned ctas = a.T <= kPerCta ? 1 : kCluster;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(a.N <= kFewThreads && a.T <= 8 * kFewThreads ? kFewThreads : kThreads);
   cfg.dynamicSmemBytes = smem_bytes(a.N);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -4,8 +4,8 @@
 //
 // A position times a frequency has more whole turns than fp32 can hold fractions of, so the angle is taken in
 // fixed point: F = f / (2 pi) 2^64 modulo 2^64 once for each pair, and pos F modulo 2^64, which wraps at whole turns by
-// itself.  Its top 32 bits, as a signed fraction of a turn, go to sincospi.  That is exact to 2^-32 of a turn for every
-// 32-bit position (F's own rounding, 2^-53 of it, adds at most |pos f| 2^-53).
+// itself.  Its top 32 bits, as a signed fraction of a turn, go to sincospi.  That is exact to 2^-31 of a turn for every
+// 32-bit position.
 //
 // A warp has a token (for few tokens a part of its heads), each lane a unit of 16 values of a head (two pieces of 16
 // bytes in bf16): eight pairs, or 16 values to copy, the same ones in every head.  A lane makes the cosines and sines of
@@ -21,7 +21,6 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kAhead = 4;  // heads a lane has under way
 
 // 16 values of a lane, as they come
 template <typename T>
@@ -68,16 +67,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
-// f / (2 pi) in 64-bit fixed point, without its whole turns
+// f / (2 pi) in 64-bit fixed point, without its whole turns: f = m 2^(e - 1075) with a 53-bit m, and m times
+// floor(2^64 / (2 pi)), shifted.  In integers, because FP64 arithmetic is slow here (2 us of a token's 8).
 __device__ __forceinline__ uint64_t turns_of(double f) {
-  double turns = f * 0.15915494309189535;
-  turns -= floor(turns);
-  return turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
+  constexpr uint64_t kPerRadian = 0x28be60db9391054aull;
+  const uint64_t w = (uint64_t)__double_as_longlong(f), m = (w & 0xfffffffffffffull) | 0x10000000000000ull;
+  const int shift = 1075 - (int)(w >> 52 & 2047);
+  const uint64_t hi = __umul64hi(m, kPerRadian), lo = m * kPerRadian;
+  uint64_t turns;
+  if (shift >= 128) turns = 0;
+  else if (shift >= 64) turns = hi >> (shift - 64);
+  else if (shift > 0) turns = hi << (64 - shift) | lo >> shift;
+  else turns = shift > -64 ? lo << -shift : 0;
+  return (int64_t)w < 0 ? 0 - turns : turns;
 }
 
 template <typename Tin, bool ADJ>
 __global__ void __launch_bounds__(kThreads)
 rope_append_kernel(const RopeArgs p, const int parts) {
+  constexpr int kAhead = sizeof(Tin) == 2 ? 4 : 2;  // heads a lane has under way: 128 bytes
   const int lane = threadIdx.x & 31;
   const int per_head = p.d / 16, at_once = 32 / per_head;  // lanes of a head, heads of a warp
   const int u = lane % per_head, head0 = lane / per_head;
@@ -87,21 +95,17 @@ rope_append_kernel(const RopeArgs p, const int parts) {
   const int lo = turned && !ADJ ? 8 * u : 16 * u, hi = turned && !ADJ ? pairs + 8 * u : 16 * u + 8;
   const int from = turned ? 4 * u : 0;  // the lane with the first two of its pairs, 8 u and 8 u + 1
 
-  uint64_t F[2] = {0, 0};
+  double freq[2] = {0.0, 0.0};
   int axis[2] = {0, 0};
-  bool bad = false;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int j = 2 * lane + i;
     if (j >= pairs) continue;
-    F[i] = turns_of(p.inv_freq[j]);
-    axis[i] = p.axis ? p.axis[j] : 0;
-    bad |= (unsigned)axis[i] >= (unsigned)p.axes;
+    freq[i] = p.inv_freq[j];
+    if (p.axis) axis[i] = p.axis[j];
   }
-  if (__any_sync(0xffffffffu, bad)) {
-    if (lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-    return;
-  }
+  uint64_t F[2];
+  bool begun = false;
   // this warp's heads: rounds of at_once
   const int rounds = (heads + at_once - 1) / at_once, each = (rounds + parts - 1) / parts;
   const int64_t warp = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * kWarps;
@@ -109,10 +113,6 @@ rope_append_kernel(const RopeArgs p, const int parts) {
     const int64_t t = parts == 1 ? w : w / parts;
     const int first = parts == 1 ? 0 : (int)(w - t * parts) * each, end = min(first + each, rounds);
     const int slot = p.slot_map[t];
-    if (slot < 0 || slot >= p.num_blocks << p.shift) {
-      if (slot != -1 && lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-      continue;
-    }
     const Tin* q = static_cast<const Tin*>(p.q) + t * p.q_stride;
     const Tin* k = static_cast<const Tin*>(p.k) + t * p.k_stride - (int64_t)p.H * p.d;
     const Tin* v = static_cast<const Tin*>(p.v) + t * p.v_stride - (int64_t)(p.H + p.Hkv) * p.d;
@@ -126,11 +126,24 @@ rope_append_kernel(const RopeArgs p, const int parts) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(first + i, got[i]);
 
+    if (!begun) {  // (here, so that the first loads are all under way at once)
+      begun = true;
+      if (__any_sync(0xffffffffu, (unsigned)axis[0] >= (unsigned)p.axes || (unsigned)axis[1] >= (unsigned)p.axes)) {
+        if (lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+        return;
+      }
+      F[0] = turns_of(freq[0]);
+      F[1] = turns_of(freq[1]);
+    }
     float c[2], s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint64_t x = (uint64_t)(int64_t)p.positions[(int64_t)axis[i] * p.T + t] * F[i];
       sincospif((float)(int32_t)(x >> 32) * 0x1p-31f, &s[i], &c[i]);
+    }
+    if (slot < 0 || slot >= p.num_blocks << p.shift) {
+      if (slot != -1 && lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+      continue;
     }
     float cs[8], sn[8];
 #pragma unroll
