@@ -8,7 +8,6 @@ the same entry-point names, and the seeded synthetic-input generators.
 """
 from .binding import (  # noqa: F401
     KdaError,
-    kda_attention_workspace_size,
     kda_block_tables,
     kda_chunk_bwd,
     kda_chunk_fwd,

@@ -38,7 +38,7 @@ EXPORTS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_decode_step", "
            "kda_noalloc_scratch_bytes", "kda_chunk_fwd_segment_map", "kda_state_compose", "kda_rmsnorm_quant",
            "kda_matmul_fp8", "kda_linear_chunk_fwd_workspace_size", "kda_linear_chunk_fwd",
            "kda_linear_decode_step", "kda_block_tables", "kda_rope_append", "kda_window_attention_fwd",
-           "kda_window_attention_decode_step", "kda_tree_attention", "kda_attention_workspace_size")
+           "kda_window_attention_decode_step", "kda_tree_attention")
 
 
 class KdaError(RuntimeError):
@@ -104,14 +104,12 @@ def load_library(path: Optional[str] = None):
         lib.kda_block_tables.restype = I
         lib.kda_rope_append.argtypes = [P, P, P, P, P, P, P, P, P, P, I64, I, I, I, I, I, I, I64, I64, I64, I, I, P, I, P]
         lib.kda_rope_append.restype = I
-        lib.kda_window_attention_fwd.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, I, I64, I, I, I, P, I, I, I64, F, P, SZ, P]
+        lib.kda_window_attention_fwd.argtypes = [P, P, P, P, P, P, P, I, I64, I, I, I, I64, I, I, I, P, I, I, I64, F, P]
         lib.kda_window_attention_fwd.restype = I
-        lib.kda_window_attention_decode_step.argtypes = [P, P, P, P, P, P, I, I, I, I, I64, I, I, I, P, I, I, I64, F, P, SZ, P]
+        lib.kda_window_attention_decode_step.argtypes = [P, P, P, P, P, P, I, I, I, I, I64, I, I, I, P, I, I, I64, F, P]
         lib.kda_window_attention_decode_step.restype = I
-        lib.kda_tree_attention.argtypes = [P, P, P, P, P, P, P, I, P, I, I64, I, I, I, I64, I, I, I, P, I, I, I64, F, P, SZ, P]
+        lib.kda_tree_attention.argtypes = [P, P, P, P, P, P, P, I, P, I, I64, I, I, I, I64, I, I, I, P, I, I, I64, F, P]
         lib.kda_tree_attention.restype = I
-        lib.kda_attention_workspace_size.argtypes = [I, I64, I, I, I]
-        lib.kda_attention_workspace_size.restype = SZ
         lib.kda_noalloc_scratch_bytes.argtypes = []
         lib.kda_noalloc_scratch_bytes.restype = SZ
         lib.kda_trace_enable.argtypes = [I]
@@ -729,7 +727,7 @@ def _load_marshal():
     except ImportError as e:
         raise RuntimeError("the marshalling module is not built; run __graft_entry__.build()") from e
     names = ("kda_block_tables", "kda_rope_append", "kda_window_attention_fwd", "kda_window_attention_decode_step",
-             "kda_tree_attention", "kda_attention_workspace_size")
+             "kda_tree_attention")
     module.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, KdaError)
     _marshal = module
     return module
@@ -757,36 +755,29 @@ def kda_rope_append(q, k, v, inv_freq, positions, slot_map, k_cache, v_cache, *,
                                                      q_out)
 
 
-def kda_attention_workspace_size(N: int, T: int, H: int, Hkv: int, d: int) -> int:
-    """Bytes of scratch that the attentions use for N requests with T new tokens in all (0: none)."""
-    return int(load_library().kda_attention_workspace_size(N, T, H, Hkv, d))
-
-
 def kda_window_attention_fwd(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out=None, *, window: int = 0,
-                             sinks: int = 0, scale: Optional[float] = None, max_length: int = 0, workspace=None):
+                             sinks: int = 0, scale: Optional[float] = None, max_length: int = 0):
     """Attention of new tokens over a paged cache that holds them already: the token at position p sees the keys
     j <= p with j > p - window (all if window is 0) or j < sinks.  q: [T, H, d] bf16 (tokens may be strided); k_cache,
     v_cache: [num_blocks, block_size, Hkv, d] bf16; block_tables: int32 [N, max_blocks]; lengths: int32 [N], the new
     tokens included; cu_seqlens: int32 [N + 1] (rows behind its last are left); scale: d ** -0.5 unless given;
-    max_length: no request is longer (a hint); workspace: uint8 of kda_attention_workspace_size(...) bytes at least, or
-    None (allocated).  Returns out [T, H, d] bf16."""
+    max_length: no request is longer (a hint).  Returns out [T, H, d] bf16."""
     return (_marshal or _load_marshal()).window_fwd(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out, window, sinks, scale,
-                                                    max_length, workspace)
+                                                    max_length)
 
 
 def kda_window_attention_decode_step(q, k_cache, v_cache, block_tables, lengths, out=None, *, window: int = 0,
-                                     sinks: int = 0, scale: Optional[float] = None, max_length: int = 0, workspace=None):
+                                     sinks: int = 0, scale: Optional[float] = None, max_length: int = 0):
     """kda_window_attention_fwd for one new token of each request: q [N, H, d], at position lengths[n] - 1.  A request of
     length 0 gets zeros.  Returns out [N, H, d] bf16."""
-    return (_marshal or _load_marshal()).window_step(q, k_cache, v_cache, block_tables, lengths, out, window, sinks, scale, max_length,
-                                                     workspace)
+    return (_marshal or _load_marshal()).window_step(q, k_cache, v_cache, block_tables, lengths, out, window, sinks, scale, max_length)
 
 
 def kda_tree_attention(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, tree_mask, out=None, *, window: int = 0,
-                       sinks: int = 0, scale: Optional[float] = None, max_length: int = 0, workspace=None):
+                       sinks: int = 0, scale: Optional[float] = None, max_length: int = 0):
     """Attention of drafted tokens that form a tree, over the cache that holds them as its last tokens.  tree_mask: int64
     [T, words], bit j % 64 of word j / 64 saying that a token sees drafted token j of its request (its ancestors
     and itself); of the tokens before the drafted ones it sees what kda_window_attention_fwd shows at its depth.
     Returns out [T, H, d] bf16."""
     return (_marshal or _load_marshal()).tree(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, tree_mask, out, window, sinks,
-                                              scale, max_length, workspace)
+                                              scale, max_length)

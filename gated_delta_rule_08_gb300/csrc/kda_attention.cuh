@@ -45,7 +45,6 @@ struct Params {
   int half_rows;             // rows of half an item, and of an item (kda_attention_tc.cu)
   Divisor by_item;
   int shift, max_blocks, num_blocks, window, sinks;
-  float4* parts;             // items cut at the CTAs' shares (kda_attention_tc.cu), or null
   float c;                   // scale log2(e): scores are kept in log2
   unsigned int* err;
   int waits;                 // enum Waits
@@ -125,29 +124,6 @@ struct Tile {
   int first, rows;     // first row and number of rows of the tile (0: nothing to do)
 };
 
-// The k-th tile of `per` rows of t.n, whose first new token and number of new tokens are known; no rows if the request
-// cannot be served, which is reported.
-__device__ __forceinline__ void fill_tile(const Params& p, int per, int k, Tile& t, bool report) {
-  t.len = p.lengths[t.n];
-  t.before = t.len - t.tokens;
-  t.first = k * per;
-  t.rows = min(t.tokens * p.G - t.first, per);
-  bool bad = t.len < 0 || t.len > kMaxLength || (int64_t)t.len > ((int64_t)p.max_blocks << p.shift);
-  if (p.cu == nullptr) {
-    if (t.len == 0) t.before = 0;  // no key: a row of zeros
-  } else {
-    bad |= t.tokens > t.len;
-  }
-  if (bad) {
-    if (report) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
-    t.rows = 0;
-  }
-  if (p.mask && t.tokens > 64 * p.mask_words) {
-    if (report) atomicOr(p.err, KDA_DEVERR_BAD_COUNT);
-    t.rows = 0;
-  }
-}
-
 // Walks the tiles of all requests in order, `per` rows a tile: item = (tile, key head).  A warp calls it
 // with rising items; `base` and `tiles` keep its place.
 struct Walk {
@@ -207,7 +183,24 @@ __device__ __forceinline__ bool locate(const Params& p, int per, Divisor by_per,
       w.base += 32;
     }
   }
-  fill_tile(p, per, k, t, lane == 0);
+  t.len = p.lengths[t.n];
+  t.before = t.len - t.tokens;
+  t.first = k * per;
+  t.rows = min(t.tokens * p.G - t.first, per);
+  bool bad = t.len < 0 || t.len > kMaxLength || (int64_t)t.len > ((int64_t)p.max_blocks << p.shift);
+  if (p.cu == nullptr) {
+    if (t.len == 0) t.before = 0;  // no key: a row of zeros
+  } else {
+    bad |= t.tokens > t.len;
+  }
+  if (bad) {
+    if (lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
+    t.rows = 0;
+  }
+  if (p.mask && t.tokens > 64 * p.mask_words) {
+    if (lane == 0) atomicOr(p.err, KDA_DEVERR_BAD_COUNT);
+    t.rows = 0;
+  }
   return true;
 }
 
@@ -249,11 +242,21 @@ struct Span {
   int all_lo, all_hi;  // every row sees these
   int sink_boxes, first_box, boxes;
 };
-// Tokens [a, b) of the tile's request; least, most: drafted tokens that one of them sees (where masks and a window meet).
-__device__ __forceinline__ Span span_from(const Params& p, const Tile& t, int a, int b, int least, int most, int box_shift) {
+// (one warp together; tokens [a, b) of the tile's request)
+__device__ __forceinline__ Span span_of(const Params& p, const Tile& t, int a, int b, int box_shift) {
   Span s;
   int64_t lo, all_lo;
   if (p.mask) {
+    int least = 1 << 30, most = 0;
+    if (p.window > 0) {
+      for (int i = a + (threadIdx.x & 31); i < b; i += 32) {
+        const int m = mask_count(p, t, i);
+        least = min(least, m);
+        most = max(most, m);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+    }
     s.hi = t.len - 1;
     s.all_hi = t.before - 1;
     lo = p.window > 0 ? (int64_t)t.before + least - p.window : 0;
@@ -274,20 +277,6 @@ __device__ __forceinline__ Span span_from(const Params& p, const Tile& t, int a,
   const int last = s.hi < 0 ? -1 : s.hi >> box_shift;
   s.boxes = s.sink_boxes + (last >= s.first_box ? last - s.first_box + 1 : 0);
   return s;
-}
-// (one warp together)
-__device__ __forceinline__ Span span_of(const Params& p, const Tile& t, int a, int b, int box_shift) {
-  int least = 1 << 30, most = 0;
-  if (p.mask && p.window > 0) {
-    for (int i = a + (threadIdx.x & 31); i < b; i += 32) {
-      const int m = mask_count(p, t, i);
-      least = min(least, m);
-      most = max(most, m);
-    }
-    least = __reduce_min_sync(0xffffffffu, least);
-    most = __reduce_max_sync(0xffffffffu, most);
-  }
-  return span_from(p, t, a, b, least, most, box_shift);
 }
 // the first key of the span's box i
 __device__ __forceinline__ int box_key(const Span& s, int i, int box_shift) {

@@ -46,7 +46,7 @@ bool many_rows(const AttentionArgs& a) {
   return rows > (int64_t)(a.N * a.Hkv <= 32 ? 64 : 16) * a.N;
 }
 
-kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, size_t workspace_bytes, void* stream) {
+kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, void* stream) {
   if (a.N < 0 || a.T < 0 || a.H <= 0 || a.Hkv <= 0 || a.num_blocks < 0 || a.max_blocks < 0 || a.window < 0 || a.sinks < 0 ||
       a.max_length < 0 || !(a.scale > 0.f) || isinf(a.scale))
     return KDA_ERR_INVALID_ARG;
@@ -71,9 +71,6 @@ kda_status attention(AttentionArgs a, int block_size, const int64_t* strides, si
   if (a.max_length == 0 || a.max_length > longest) a.max_length = longest;
   a.block_stride = strides[0]; a.token_stride = strides[1]; a.head_stride = strides[2];
   a.waits = test_wait_timeout();
-  const size_t need = many_rows(a) ? attention_tc_workspace(a.N, a.d) : 0;
-  if (need == 0) a.workspace = nullptr;
-  if (a.workspace && (workspace_bytes < need || !aligned(a.workspace, 256))) return KDA_ERR_WORKSPACE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return done(many_rows(a) ? attention_tc_launch(a, s) : attention_rows_launch(a, s));
 }
@@ -147,58 +144,48 @@ namespace {
 
 AttentionArgs args_of(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                       const int32_t* lengths, const int32_t* cu_seqlens, void* out, int N, int64_t T, int H, int Hkv, int d,
-                      int64_t q_stride, int num_blocks, int max_blocks, int window, int sinks, int64_t max_length, float scale, void* workspace) {
+                      int64_t q_stride, int num_blocks, int max_blocks, int window, int sinks, int64_t max_length, float scale) {
   AttentionArgs a{};
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.block_tables = block_tables; a.lengths = lengths;
   a.cu_seqlens = cu_seqlens; a.out = out; a.N = N; a.T = T; a.H = H; a.Hkv = Hkv; a.d = d; a.num_blocks = num_blocks;
-  a.max_blocks = max_blocks; a.window = window; a.sinks = sinks; a.max_length = max_length; a.scale = scale; a.workspace = workspace;
+  a.max_blocks = max_blocks; a.window = window; a.sinks = sinks; a.max_length = max_length; a.scale = scale;
   return a;
 }
 
 }  // namespace
 
-KDA_API size_t kda_attention_workspace_size(int N, int64_t T, int H, int Hkv, int d) {
-  if (N <= 0 || T <= 0 || H <= 0 || Hkv <= 0 || !heads_ok(H, Hkv) || (d != 64 && d != 128)) return 0;
-  AttentionArgs a{};
-  a.N = N; a.T = T; a.H = H; a.Hkv = Hkv; a.d = d;
-  return many_rows(a) ? attention_tc_workspace(N, d) : 0;
-}
-
 KDA_API kda_status kda_window_attention_fwd(const void* q, const void* k_cache, const void* v_cache,
                                             const int32_t* block_tables, const int32_t* lengths, const int32_t* cu_seqlens,
                                             void* out, int N, int64_t T, int H, int Hkv, int d, int64_t q_stride,
                                             int num_blocks, int block_size, int max_blocks, const int64_t* cache_strides,
-                                            int window, int sinks, int64_t max_length, float scale, void* workspace,
-                                            size_t workspace_bytes, void* stream) {
+                                            int window, int sinks, int64_t max_length, float scale, void* stream) {
   if (N > 0 && T > 0 && !cu_seqlens) return KDA_ERR_INVALID_ARG;
   return attention(args_of(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out, N, T, H, Hkv, d, q_stride, num_blocks,
-                           max_blocks, window, sinks, max_length, scale, workspace),
-                   block_size, cache_strides, workspace_bytes, stream);
+                           max_blocks, window, sinks, max_length, scale),
+                   block_size, cache_strides, stream);
 }
 
 KDA_API kda_status kda_window_attention_decode_step(const void* q, const void* k_cache, const void* v_cache,
                                                     const int32_t* block_tables, const int32_t* lengths, void* out, int N,
                                                     int H, int Hkv, int d, int64_t q_stride, int num_blocks, int block_size,
                                                     int max_blocks, const int64_t* cache_strides, int window, int sinks,
-                                                    int64_t max_length, float scale, void* workspace,
-                                            size_t workspace_bytes, void* stream) {
+                                                    int64_t max_length, float scale, void* stream) {
   return attention(args_of(q, k_cache, v_cache, block_tables, lengths, nullptr, out, N, N, H, Hkv, d, q_stride, num_blocks,
-                           max_blocks, window, sinks, max_length, scale, workspace),
-                   block_size, cache_strides, workspace_bytes, stream);
+                           max_blocks, window, sinks, max_length, scale),
+                   block_size, cache_strides, stream);
 }
 
 KDA_API kda_status kda_tree_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                       const int32_t* lengths, const int32_t* cu_seqlens, const uint64_t* tree_mask,
                                       int mask_words, void* out, int N, int64_t T, int H, int Hkv, int d, int64_t q_stride,
                                       int num_blocks, int block_size, int max_blocks, const int64_t* cache_strides,
-                                      int window, int sinks, int64_t max_length, float scale, void* workspace,
-                                            size_t workspace_bytes, void* stream) {
+                                      int window, int sinks, int64_t max_length, float scale, void* stream) {
   if (mask_words < 1) return KDA_ERR_INVALID_ARG;
   if (mask_words > 16) return KDA_ERR_UNSUPPORTED;
   if (N > 0 && T > 0 && (!cu_seqlens || !tree_mask)) return KDA_ERR_INVALID_ARG;
   AttentionArgs a = args_of(q, k_cache, v_cache, block_tables, lengths, cu_seqlens, out, N, T, H, Hkv, d, q_stride, num_blocks,
-                            max_blocks, window, sinks, max_length, scale, workspace);
+                            max_blocks, window, sinks, max_length, scale);
   a.tree_mask = tree_mask;
   a.mask_words = mask_words;
-  return attention(a, block_size, cache_strides, workspace_bytes, stream);
+  return attention(a, block_size, cache_strides, stream);
 }

@@ -128,7 +128,6 @@ struct QMap {
 // An item as every role sees it.
 struct Item {
   Tile t;
-  bool whole;      // this CTA has all of its tiles
   Span span;       // of both halves: the boxes
   int tile0, tile1;  // this CTA's tiles
 };
@@ -188,123 +187,7 @@ __device__ __forceinline__ Plain plain_tiles(const Span& boxes, const Span& rows
 // a value that is the same in all lanes, as one that the compiler knows to be
 __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// ------------------------------------------------------------------ equal shares
-// Where items are few for the SMs, or differ in length, the CTAs' shares are cut at equal numbers of tiles instead: items
-// lie in a row, tile after tile, and CTA b of B takes the tiles from b / B to (b + 1) / B of them.  An item that
-// a cut goes through leaves its sums for each CTA in the workspace, and a second kernel joins them.
-constexpr int kMostShared = 2048;  // requests, and tiles of rows, that a CTA looks through to find its share
-struct Share {
-  int at, offset, budget;  // first item and tile in it, number of tiles
-};
-// Sum of the threads' values before this one's, and of all (kThreads threads; 16 ints of shared memory).
-__device__ __forceinline__ int scan_block(int v, int* scratch, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int sum = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += up;
-  }
-  __syncthreads();
-  if (lane == 31) scratch[warp] = sum;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    before += i < warp ? scratch[i] : 0;
-    total += scratch[i];
-  }
-  return before + sum - v;
-}
-// What an item counts for: its tiles; one that sees no key has its rows of zeros to write.
-__device__ __forceinline__ int cost_of(const Tile& t, const Span& s, int box_shift) {
-  return t.rows > 0 ? max(((s.boxes << box_shift) + kKeys - 1) / kKeys, 1) : 0;
-}
-// (all threads; scratch: N + 33 ints)
-__device__ Share share_of(const Params& p, int per, int box_shift, int* scratch, int cta, int ctas) {
-  const int tid = threadIdx.x;
-  int *found = scratch + 16, *first = scratch + 32;  // [N + 1] tiles of rows before each request
-  int tiles = p.N * (int)p.by_each.d;
-  if (p.cu != nullptr) {
-    const int each = (p.N + kThreads - 1) / kThreads, n0 = min(tid * each, p.N), n1 = min(n0 + each, p.N);
-    int mine = 0;
-    for (int n = n0; n < n1; ++n) mine += p.by_item.div((p.cu[n + 1] - p.cu[n]) * p.G + per - 1);
-    int at = scan_block(mine, scratch, tiles);
-    for (int n = n0; n < n1; ++n) {
-      first[n] = at;
-      at += p.by_item.div((p.cu[n + 1] - p.cu[n]) * p.G + per - 1);
-    }
-    if (tid == 0) first[p.N] = tiles;
-    __syncthreads();
-  }
-  auto cost = [&](int i) {
-    Tile t;
-    int k;
-    if (p.cu == nullptr) {
-      t.n = p.by_each.div(i);
-      t.t0 = t.n;
-      t.tokens = 1;
-      k = i - t.n * (int)p.by_each.d;
-    } else {
-      int lo = 0, hi = p.N - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= i) lo = mid; else hi = mid - 1;
-      }
-      t.n = lo;
-      t.t0 = p.cu[lo];
-      t.tokens = p.cu[lo + 1] - t.t0;
-      k = first[lo + 1] - 1 - i;
-    }
-    fill_tile(p, per, k, t, false);
-    if (t.rows == 0) return 0;
-    const int a = p.by_G.div(t.first), b = a + p.by_G.div(t.rows);
-    int least = 1 << 30, most = 0;
-    if (p.mask && p.window > 0)
-      for (int j = a; j < b; ++j) {
-        const int m = mask_count(p, t, j);
-        least = min(least, m);
-        most = max(most, m);
-      }
-    return cost_of(t, span_from(p, t, a, b, least, most, box_shift), box_shift);
-  };
-  const int each = (tiles + kThreads - 1) / kThreads, i0 = min(tid * each, tiles), i1 = min(i0 + each, tiles);
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) mine += cost(i) * p.Hkv;
-  int all;
-  int at = scan_block(mine, scratch, all);
-  const int shares = min(ctas, all);
-  if (cta >= shares) return {-1, 0, 0};
-  const int x0 = (int)((int64_t)all * cta / shares), x1 = (int)((int64_t)all * (cta + 1) / shares);
-  if (at <= x0 && x0 < at + mine) {
-    for (int i = i0;; ++i) {
-      const int c = cost(i), here = c * p.Hkv;
-      if (x0 < at + here) {
-        found[0] = i * p.Hkv + (x0 - at) / c;
-        found[1] = (x0 - at) % c;
-        break;
-      }
-      at += here;
-    }
-  }
-  __syncthreads();
-  return {found[0], found[1], x1 - x0};
-}
-// The workspace: [2 B][D / 4][256] sums of four values of a row, [2 B][256] references and sums of weights, [B] where a
-// share begins.  CTA b's slots: 2 b for an item that it comes to in the middle, 2 b + 1 for one that it leaves there.
-template <int D>
-struct Parts {
-  float4* values;
-  float2* sums;
-  int2* begins;
-  __host__ __device__ Parts(float4* base, int ctas)
-      : values(base), sums(reinterpret_cast<float2*>(base + (size_t)2 * ctas * (D / 4) * 256)),
-        begins(reinterpret_cast<int2*>(sums + (size_t)2 * ctas * 256)) {}
-  static size_t bytes(int ctas) { return (size_t)2 * ctas * 256 * (D * 4 + 8) + (size_t)ctas * 8; }
-};
-
-// SPLIT: an item a cluster, whose p.split CTAs share its keys; else a CTA walks over items, or over its share of them.
+// SPLIT: an item a cluster, whose p.split CTAs share its keys; else a CTA walks over items.
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
@@ -343,20 +226,11 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     __syncthreads();
     walk.order = order;
   }
-  int at = SPLIT ? blockIdx.x / p.split : blockIdx.x, offset = 0, budget = 0x7fffffff;
-  int step = SPLIT ? 0x40000000 : gridDim.x;
-  const Parts<D> parts(p.parts, gridDim.x);
-  if (!SPLIT && p.parts != nullptr) {
-    const Share s = share_of(p, 2 * half_rows, box_shift, reinterpret_cast<int*>(sm + L::kRing), blockIdx.x, gridDim.x);
-    at = s.at; offset = s.offset; budget = s.budget;
-    step = 1;
-    if (tid == 0) parts.begins[blockIdx.x] = make_int2(at, offset);
-    fence_proxy_async_smem();  // (the copies' ring was looked through)
-    __syncthreads();
-  }
+  int at = SPLIT ? blockIdx.x / p.split : blockIdx.x;
+  const int step = SPLIT ? 0x40000000 : gridDim.x;
   auto next = [&](Item& it) {
     while (true) {
-      if (at < 0 || budget == 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
+      if (at < 0 || !locate(p, 2 * half_rows, p.by_item, at, walk, it.t)) return false;
       at += step;  // (a second one of a split item's passes 2^31 or the last item)
       if (it.t.rows > 0) break;
     }
@@ -364,17 +238,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     it.span = span_of(p, it.t, a, a + p.by_G.div(it.t.rows), box_shift);
     const int tiles = ((it.span.boxes << box_shift) + kKeys - 1) / kKeys;
     if (SPLIT) split = parts_of(p, tiles);
-    if (SPLIT) {
-      it.tile0 = (int)((int64_t)tiles * rank / split);
-      it.tile1 = (int)((int64_t)tiles * (rank + 1) / split);
-    } else {
-      const int cost = max(tiles, 1), taken = min(cost - offset, budget);
-      it.whole = taken == cost;
-      it.tile0 = offset;
-      it.tile1 = min(offset + taken, tiles);
-      budget -= taken;
-      offset = 0;
-    }
+    it.tile0 = SPLIT ? (int)((int64_t)tiles * rank / split) : 0;
+    it.tile1 = SPLIT ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
     return true;
   };
   Item coming;
@@ -538,28 +403,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
         sums[rr] = make_float2(m, l);
         break;  // one item
-      }
-      if (!SPLIT && !it.whole) {
-        const int slot = 2 * blockIdx.x + (it.tile0 > 0 ? 0 : 1), rr = h * kHalf + row;
-        if (rows > 0) {
-          float4* dst = parts.values + (size_t)slot * (D / 4) * 256 + rr;
-#pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            if (any) {
-              tmem_ld32(to + i, o);
-              tmem_landed(o);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) dst[(i + e) / 4 * 256] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          }
-          parts.sums[(size_t)slot * 256 + rr] = make_float2(m, l);
-        }
-        tc_fence_before();
-        continue;
       }
       if (rows > 0) {
         const float inv = l != 0.f ? 1.f / l : 0.f;  // a row that sees nothing is zero (a NaN stays one)
@@ -844,8 +687,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     __syncthreads();
   }
   tc_fence_after();
-  if (!SPLIT && p.parts != nullptr && *abort_flag && tid < 256)
-    for (int i = 0; i < 2; ++i) parts.sums[((size_t)2 * blockIdx.x + i) * 256 + tid] = make_float2(kLowest, kGone);
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
   if (!SPLIT || split == 1) return;
 
@@ -889,58 +730,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     }
   }
   cluster_sync();  // no CTA leaves while another reads its memory
-}
-
-// Joins the items that cuts between shares go through: 32 rows a CTA, of the item at cut blockIdx.x / 8, if that is the
-// first cut through it.  A warp has a row a lane and eight of its values at a time.
-constexpr int kJoinThreads = 128;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
-attention_join_kernel(const Params p, const int ctas) {
-  griddep_wait();
-  const Parts<D> parts(p.parts, ctas);
-  const int b = blockIdx.x / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) return;
-  const int2 begin = parts.begins[b + 1], before = parts.begins[b];
-  if (begin.y == 0 || (before.y > 0 && before.x == begin.x)) return;
-  Walk walk;
-  Tile t;
-  if (!locate(p, 2 * p.half_rows, p.by_item, begin.x, walk, t)) return;
-  const int rr = blockIdx.x % 8 * 32 + lane, row = rr % kHalf, q = rr / kHalf * p.half_rows + row;
-  if (row >= p.half_rows || q >= t.rows) return;
-  float m = kLowest, l = 0.f;
-  int end = b + 1;
-  bool lost = false;
-  for (int j = b; j < ctas; ++j) {
-    if (j > b) {
-      const int2 at = parts.begins[j];
-      if (at.x != begin.x || at.y == 0) break;
-      end = j + 1;
-    }
-    const float2 s = parts.sums[(size_t)(j == b ? 2 * b + 1 : 2 * j) * 256 + rr];
-    lost |= s.y == kGone;
-    const float n = fmaxf(m, s.x);
-    l = fmaf(ex2(m - n), l, ex2(s.x - n) * s.y);
-    m = n;
-  }
-  if (lost) return;
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const int r = t.first + q, tok = p.by_G.div(r);
-  __nv_bfloat16* dst = p.out + ((int64_t)(t.t0 + tok) * p.H + (t.head * p.G + r - tok * p.G)) * D;
-#pragma unroll 1
-  for (int c = 2 * warp; c < D / 4; c += 2 * (kJoinThreads / 32)) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-#pragma unroll 4
-    for (int j = b; j < end; ++j) {
-      const size_t slot = j == b ? 2 * b + 1 : 2 * j;
-      const float f = ex2(parts.sums[slot * 256 + rr].x - m);
-      const float4* src = parts.values + (slot * (D / 4) + c) * 256 + rr;
-      x = f4_fma(f, src[0], x);
-      y = f4_fma(f, src[256], y);
-    }
-    *reinterpret_cast<uint4*>(dst + 4 * c) = make_uint4(pack_bf2(x.x * inv, x.y * inv), pack_bf2(x.z * inv, x.w * inv),
-                                                        pack_bf2(y.x * inv, y.y * inv), pack_bf2(y.z * inv, y.w * inv));
-  }
 }
 
 // CTAs that may share an item's keys, and the tiles for each at least: where items leave SMs idle, as many as there are SMs
@@ -995,36 +784,14 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
       !tensor_map_cache(&maps.v, a.v_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, 1u << box_shift) ||
       !tensor_map_rows(&qmap.q, a.q, a.T, a.H, D, a.q_stride, (uint32_t)tokens, (uint32_t)p.G))
     return cudaErrorInvalidValue;
-  const int64_t tiles = most_tiles(a, 2 * p.half_rows), items = tiles * a.Hkv;
-  const bool shared = a.workspace != nullptr && a.N <= kMostShared && tiles <= kMostShared;
-  if (items * 2 <= sms && !shared) {
-    split_of(items, most_keys(a, 2 * tokens), sms, &p.split, &p.least);
-    return launch_one<D, true>(maps, qmap, p, box_shift, (unsigned)(items * p.split), st);
-  }
-  if (!shared) return launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)(items < sms ? items : sms), st);
-  p.parts = static_cast<float4*>(a.workspace);
-  cudaError_t e = launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)sms, st);
-  if (e != cudaSuccess) return e;
-  TraceScope ts("kda_attention_join", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(sms - 1) * 8);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<D>, p, sms);
+  const int64_t items = most_tiles(a, 2 * p.half_rows) * a.Hkv;
+  if (a.tree_mask == nullptr && items > sms / 2) return launch_one<D, false>(maps, qmap, p, box_shift, (unsigned)(items < sms ? items : sms), st);
+  split_of(items, most_keys(a, 2 * tokens), sms, &p.split, &p.least);
+  p.ordered = a.N > 1 && a.N <= kMostOrdered && items * p.split > sms;
+  return launch_one<D, true>(maps, qmap, p, box_shift, (unsigned)(items * p.split), st);
 }
 
 }  // namespace
-
-size_t attention_tc_workspace(int64_t N, int d) {
-  const int sms = device_sms();
-  if (sms <= 0 || N > kMostShared) return 0;
-  return align_up(d == 64 ? Parts<64>::bytes(sms) : Parts<128>::bytes(sms), 256);
-}
 
 cudaError_t attention_tc_launch(const AttentionArgs& a, cudaStream_t st) {
   return a.d == 64 ? launch<64>(a, params_of(a), st) : launch<128>(a, params_of(a), st);

@@ -323,11 +323,9 @@ struct AttentionArgs {
   int H, Hkv, d, num_blocks, shift, max_blocks, window, sinks;
   int64_t max_length;          // > 0
   float scale;
-  void* workspace;             // may be null
   unsigned int* err;
   int waits;  // test_wait_timeout()
 };
-size_t attention_tc_workspace(int64_t N, int d);
 cudaError_t attention_rows_launch(const AttentionArgs& a, cudaStream_t stream);  // few rows (kda_attention.cu)
 cudaError_t attention_tc_launch(const AttentionArgs& a, cudaStream_t stream);    // many rows (kda_attention_tc.cu)
 

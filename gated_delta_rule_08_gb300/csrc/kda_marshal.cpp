@@ -27,7 +27,6 @@ struct {
   decltype(&kda_window_attention_fwd) fwd = nullptr;
   decltype(&kda_window_attention_decode_step) step = nullptr;
   decltype(&kda_tree_attention) tree = nullptr;
-  decltype(&kda_attention_workspace_size) workspace_size = nullptr;
   PyObject* error = nullptr;  // KdaError
 } g;
 
@@ -183,7 +182,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.fwd = reinterpret_cast<decltype(g.fwd)>(address("kda_window_attention_fwd"));
     g.step = reinterpret_cast<decltype(g.step)>(address("kda_window_attention_decode_step"));
     g.tree = reinterpret_cast<decltype(g.tree)>(address("kda_tree_attention"));
-    g.workspace_size = reinterpret_cast<decltype(g.workspace_size)>(address("kda_attention_workspace_size"));
     Py_INCREF(a[1]);
     Py_XDECREF(g.error);
     g.error = a[1];
@@ -259,17 +257,14 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// What the three attentions have in common: q, k_cache, v_cache, block_tables, lengths, .. out, window, sinks, scale, max_length,
-// workspace
+// What the three attentions have in common: q, k_cache, v_cache, block_tables, lengths, .. out, window, sinks, scale, max_length
 struct Attention {
   const at::Tensor &q, &kc, &vc, &table, &lengths;
   int dev;
   int64_t T, H, N, width, q_stride;
   Caches c;
   const int32_t *tables, *len;
-  at::Tensor out, workspace;
-  void* scratch = nullptr;
-  size_t bytes = 0;
+  at::Tensor out;
   int window, sinks;
   int64_t most;
   float scale;
@@ -289,50 +284,42 @@ struct Attention {
     scale = rest[3] == Py_None ? (float)(1.0 / std::sqrt((double)c.d)) : (float)number(rest[3]);
     most = integer(rest[4]);
     narrow(N, "block_tables"); narrow(width, "block_tables"); narrow(H, "q");
-    if (const at::Tensor* given = tensor(rest[5], "workspace", true)) {
-      rank(*given, "workspace", 1);
-      scratch = data<void>(given, "workspace", at::kByte, {given->size(0)}, dev);
-      bytes = (size_t)given->size(0);
-    } else if ((bytes = g.workspace_size((int)N, T, (int)H, c.heads, c.d)) > 0) {
-      workspace = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
-      scratch = workspace.data_ptr();
-    }
   }
 };
 
-// .., cu_seqlens, out, window, sinks, scale, max_length, workspace
+// .., cu_seqlens, out, window, sinks, scale, max_length
 PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n, 12);
+    want(n, 11);
     const Attention t(a, a + 6);
     const int32_t* cu = data<int32_t>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {t.N + 1}, t.dev);
     done("kda_window_attention_fwd",
          g.fwd(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, t.out.data_ptr(), (int)t.N, t.T, (int)t.H,
                t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides, t.window, t.sinks, t.most, t.scale,
-               t.scratch, t.bytes, stream_of(t.dev)));
+               stream_of(t.dev)));
     return THPVariable_Wrap(t.out);
   });
 }
 
-// .., out, window, sinks, scale, max_length, workspace
+// .., out, window, sinks, scale, max_length
 PyObject* window_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n, 11);
+    want(n, 10);
     const Attention t(a, a + 5);
     if (t.T != t.N)
       refuse(PyExc_ValueError, "q has " + std::to_string(t.T) + " tokens for " + std::to_string(t.N) + " requests");
     done("kda_window_attention_decode_step",
          g.step(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, t.out.data_ptr(), (int)t.N, (int)t.H, t.c.heads,
                 t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides, t.window, t.sinks, t.most, t.scale,
-                t.scratch, t.bytes, stream_of(t.dev)));
+                stream_of(t.dev)));
     return THPVariable_Wrap(t.out);
   });
 }
 
-// .., cu_seqlens, tree_mask, out, window, sinks, scale, max_length, workspace
+// .., cu_seqlens, tree_mask, out, window, sinks, scale, max_length
 PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n, 13);
+    want(n, 12);
     const Attention t(a, a + 7);
     const int32_t* cu = data<int32_t>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {t.N + 1}, t.dev);
     const at::Tensor& mask = *tensor(a[6], "tree_mask");
@@ -342,8 +329,7 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done("kda_tree_attention",
          g.tree(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, pm, narrow(words, "tree_mask"),
                 t.out.data_ptr(), (int)t.N, t.T, (int)t.H, t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width,
-                t.c.strides, t.window, t.sinks, t.most, t.scale, t.scratch, t.bytes,
-                stream_of(t.dev)));
+                t.c.strides, t.window, t.sinks, t.most, t.scale, stream_of(t.dev)));
     return THPVariable_Wrap(t.out);
   });
 }

@@ -380,21 +380,16 @@ kda_status kda_rope_append(const void* q, const void* k, const void* v, const do
  *                  out behind the last request are left as they were
  *   window       : tokens a token sees, itself included; 0 means all.  sinks >= 0: first tokens that stay visible
  *   max_length   : no request is longer (a hint for how the work is split; 0: as long as the tables allow)
- *   workspace    : device scratch of at least kda_attention_workspace_size(...) bytes, 256-byte aligned, whose contents
- *                  on entry are ignored and on exit undefined; or NULL, with which long work is cut less evenly and
- *                  takes longer.  Calls whose GPU work may overlap need one each.  The size is 0 where none is used
  *   out          : [T, H, d] bf16, dense; must not overlap an input
  * Keys and values of tokens that a row sees have to be finite.  What lies in the cache elsewhere may be anything, and
  * table entries of blocks that no new token sees are not read.  A block that is, outside [0, num_blocks),
  * sets KDA_DEVERR_BAD_SLOT; the rows of its request are then undefined (nothing outside the cache is read).
  * Scores, softmax and sums are fp32; the weights are rounded to bf16 for their product with the values. */
-size_t kda_attention_workspace_size(int N, int64_t T, int H, int Hkv, int d);  /* (one token of each request: T = N) */
 kda_status kda_window_attention_fwd(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                     const int32_t* lengths, const int32_t* cu_seqlens, void* out, int N, int64_t T,
                                     int H, int Hkv, int d, int64_t q_stride, int num_blocks, int block_size,
                                     int max_blocks, const int64_t* cache_strides, int window, int sinks,
-                                    int64_t max_length, float scale, void* workspace, size_t workspace_bytes,
-                                    void* stream);
+                                    int64_t max_length, float scale, void* stream);
 
 /* The same for one new token of each request: q, out [N, H, d], request n's token being its last (position
  * lengths[n] - 1).  A request of length 0 gets zeros; one below 0 or longer than its table sets KDA_DEVERR_BAD_SEQLENS and
@@ -403,8 +398,7 @@ kda_status kda_window_attention_decode_step(const void* q, const void* k_cache, 
                                             const int32_t* block_tables, const int32_t* lengths, void* out, int N, int H,
                                             int Hkv, int d, int64_t q_stride, int num_blocks, int block_size,
                                             int max_blocks, const int64_t* cache_strides, int window, int sinks,
-                                            int64_t max_length, float scale, void* workspace, size_t workspace_bytes,
-                                            void* stream);
+                                            int64_t max_length, float scale, void* stream);
 
 /* Attention of drafted tokens that form a tree, over the cache: the verify step that goes with kda_decode_multi's.
  * A request's drafted tokens lie in the cache as its last cu_seqlens[n + 1] - cu_seqlens[n] ones, behind `before` others.
@@ -418,8 +412,7 @@ kda_status kda_tree_attention(const void* q, const void* k_cache, const void* v_
                               const int32_t* lengths, const int32_t* cu_seqlens, const uint64_t* tree_mask, int mask_words,
                               void* out, int N, int64_t T, int H, int Hkv, int d, int64_t q_stride, int num_blocks,
                               int block_size, int max_blocks, const int64_t* cache_strides, int window, int sinks,
-                              int64_t max_length, float scale, void* workspace, size_t workspace_bytes,
-                              void* stream);
+                              int64_t max_length, float scale, void* stream);
 
 /* Synchronises `stream`, then reads and clears the current device's error word into
  * *flags (KDA_DEVERR_* bits).  Returns KDA_OK, or KDA_ERR_CUDA if the sync failed. */

@@ -68,21 +68,21 @@ def test_rope_append_refuses(lib):
 
 
 def fwd(lib, q=at(1), kc=at(2), vc=at(3), table=at(4), lengths=at(5), cu=at(6), out=at(7), N=2, T=8, H=4, Hkv=2, d=128, qs=512, blocks=8,
-        size=16, width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0, ws=None, nbytes=0):
+        size=16, width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0):
     return lib.kda_window_attention_fwd(q, kc, vc, table, lengths, cu, out, N, T, H, Hkv, d, qs, blocks, size, width, strides, window, sinks,
-                                        most, scale, ws, nbytes, None)
+                                        most, scale, None)
 
 
 def step(lib, q=at(1), kc=at(2), vc=at(3), table=at(4), lengths=at(5), out=at(7), N=2, H=4, Hkv=2, d=128, qs=512, blocks=8, size=16,
-         width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0, ws=None, nbytes=0):
+         width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0):
     return lib.kda_window_attention_decode_step(q, kc, vc, table, lengths, out, N, H, Hkv, d, qs, blocks, size, width, strides, window,
-                                                sinks, most, scale, ws, nbytes, None)
+                                                sinks, most, scale, None)
 
 
 def tree(lib, mask=at(8), words=1, cu=at(6), q=at(1), kc=at(2), vc=at(3), table=at(4), lengths=at(5), out=at(7), N=2, T=8, H=4, Hkv=2, d=128,
-         qs=512, blocks=8, size=16, width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0, ws=None, nbytes=0):
+         qs=512, blocks=8, size=16, width=4, strides=STR, window=0, sinks=0, most=0, scale=1.0):
     return lib.kda_tree_attention(q, kc, vc, table, lengths, cu, mask, words, out, N, T, H, Hkv, d, qs, blocks, size, width, strides, window,
-                                  sinks, most, scale, ws, nbytes, None)
+                                  sinks, most, scale, None)
 
 
 @pytest.mark.parametrize("call", [fwd, step, tree], ids=["fwd", "step", "tree"])
@@ -102,12 +102,6 @@ def test_attention_refuses(lib, call):
     for name in ("q", "kc", "vc", "out"):
         assert call(lib, **{name: P(0x20008)}) == INVALID, name
     assert call(lib, out=at(1)) == INVALID and call(lib, out=at(3)) == INVALID and call(lib, lengths=P(0x20002)) == INVALID
-
-
-def test_workspace_size(lib):
-    f = lib.kda_attention_workspace_size
-    assert f(4, 4, 8, 2, 128) == 0                                # single tokens of four rows a key head
-    assert f(0, 8, 8, 2, 128) == 0 and f(4, -1, 8, 2, 128) == 0 and f(4, 4000, 7, 2, 128) == 0 and f(4, 4000, 8, 2, 96) == 0
 
 
 def test_packed_attention_refuses(lib):
