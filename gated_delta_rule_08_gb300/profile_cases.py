@@ -2,7 +2,7 @@
 see one kernel family on a small device footprint.
 
     python -m gated_delta_rule_08_gb300.profile_cases prefill|prefill_epi|varlen|decode|verify|backward|prefill_d64|
-        prefill_d64_epi|norm|matmul|matmul_few|linear|linear_token
+        prefill_d64_epi|norm|matmul|matmul_few|linear|linear_token|rope|window|window_token|tree
         [--calls N]
 
 prefill      B=1, H=32, T=8192, dk=dv=128, bf16 (q, k, v, g, beta: 337 MB; records 310 MB)
@@ -18,6 +18,10 @@ matmul       8192 x 4096 by 4096 x 4096 e4m3 with block scales
 matmul_few   64 x 4096 by 12288 x 4096
 linear       linear attention, one decay per head: B=1, H=32, T=8192, dk=dv=128, bf16
 linear_token the same for one token of each of N=256 requests on a pool of 512 states
+rope         rotary positions and cache write: 16384 tokens, 32 heads of 8, d=128, bf16
+window       one prompt of 8192 tokens, 32 heads of 8, d=128, a window of 1024 and 4 sinks
+window_token one token of each of N=256 requests over 2000 tokens each, same heads and window
+tree         64 drafted tokens of each of N=16 requests over 4000 tokens each, same heads, all keys
 
 Every call goes through the C-ABI binding; the first call is a warm-up.  Nothing is timed here.
 """
@@ -72,10 +76,45 @@ def _layer_operator(case, calls, dev):
                 binding.kda_linear_decode_step(q, k, v, g, pool, slots, scale=128 ** -0.5)
 
 
+def _attention_operator(case, calls, dev):
+    gen = torch.Generator(device=dev).manual_seed(13)
+    H, Hkv, d, block = 32, 8, 128, 64
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, device=dev).to(torch.bfloat16)
+
+    def ints(values):
+        return torch.tensor(values, dtype=torch.int32, device=dev)
+
+    if case == "rope":
+        T = 16384
+        row = randn(T, H + 2 * Hkv, d)
+        cache = [torch.empty(T // block, block, Hkv, d, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        freq = 10000.0 ** (-torch.arange(d // 2, device=dev, dtype=torch.float64) / (d // 2))
+        pos = torch.arange(T, dtype=torch.int32, device=dev)
+        for _ in range(calls + 1):
+            binding.kda_rope_append(row[:, :H], row[:, H:H + Hkv], row[:, H + Hkv:], freq, pos, pos, *cache)
+        return
+    N, length, new = {"window": (1, 8192, 8192), "window_token": (256, 2000, 1), "tree": (16, 4000, 64)}[case]
+    each = -(-length // block)
+    cache = [randn(N * each, block, Hkv, d) for _ in range(2)]
+    tables = torch.arange(N * each, dtype=torch.int32, device=dev).view(N, each)
+    lengths, cu, q = ints([length] * N), ints([new * i for i in range(N + 1)]), randn(N * new, H, d)
+    mask = torch.tensor([1 << i | 1 for i in range(63)] + [1 - (1 << 63)], dtype=torch.int64, device=dev)
+    for _ in range(calls + 1):
+        if case == "window":
+            binding.kda_window_attention_fwd(q, *cache, tables, lengths, cu, window=1024, sinks=4)
+        elif case == "window_token":
+            binding.kda_window_attention_decode_step(q, *cache, tables, lengths, window=1024, sinks=4)
+        else:
+            binding.kda_tree_attention(q, *cache, tables, lengths, cu, mask.repeat(N)[:, None].contiguous())
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["prefill", "prefill_epi", "varlen", "decode", "verify", "backward", "prefill_d64",
-                                     "prefill_d64_epi", "norm", "matmul", "matmul_few", "linear", "linear_token"])
+                                     "prefill_d64_epi", "norm", "matmul", "matmul_few", "linear", "linear_token", "rope",
+                                     "window", "window_token", "tree"])
     ap.add_argument("--calls", type=int, default=2)
     args = ap.parse_args(argv)
     dev = torch.device("cuda", 0)
@@ -99,6 +138,8 @@ def main(argv=None) -> int:
                                          commit=False, gate=D["gate"], norm_weight=D["norm_weight"])
     elif args.case in ("norm", "matmul", "matmul_few", "linear", "linear_token"):
         _layer_operator(args.case, args.calls, dev)
+    elif args.case in ("rope", "window", "window_token", "tree"):
+        _attention_operator(args.case, args.calls, dev)
     else:
         P = inputs.prefill_inputs(inputs.PREFILL, device=dev)
         gen = torch.Generator(device=dev).manual_seed(11)
