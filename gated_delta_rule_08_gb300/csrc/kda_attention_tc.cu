@@ -57,9 +57,10 @@ struct Layout {
   static constexpr int kStages = 5 * (2 / kParts);           // (four: long prompts 2 to 4 % slower)
   static constexpr uint32_t kRing = 2 * kTile;               // behind Q of the halves
   static constexpr uint32_t kBar = kRing + kStages * kTile;
-  static constexpr uint32_t kSmem = kBar + 512 + 1024;
+  static constexpr uint32_t kItems = kBar + 512;
+  static constexpr uint32_t kSmem = kItems + 1024 + 1024;
   static_assert(kSmem <= 232448, "shared memory of a CTA");
-  static_assert((2 * kStages + 20) * 8 + kMostOrdered <= 512, "barriers");
+  static_assert((2 * kStages + 19 + 8) * 8 + kMostOrdered <= 512, "barriers");
   static_assert(256 * D * 4 <= kStages * kTile, "a split item's sums take the ring's place");
 };
 
@@ -136,13 +137,6 @@ struct QMap {
   CUtensorMap q;
 };
 
-// An item as every role sees it.
-struct Item {
-  Tile t;
-  Span span;       // of both halves: the boxes
-  int tile0, tile1;  // this CTA's tiles
-};
-
 // The first key of 16-key group g of tile j, or -1 past the last box.
 __device__ __forceinline__ int group_key(const Span& s, int j, int g, int box_shift) {
   const int key = j * kKeys + g * 16, box = key >> box_shift;
@@ -195,6 +189,16 @@ __device__ __forceinline__ Plain plain_tiles(const Span& boxes, const Span& rows
   const int first = max((boxes.sink_boxes << box_shift) + kKeys - 1, rows.all_lo - shift + kKeys - 1) / kKeys;
   return {first, max(first, (rows.all_hi + 1 - shift) / kKeys)};
 }
+// An item as every role sees it: the copy warp looks them up, one ahead, and hands them over in shared memory.
+struct Item {
+  int have;              // 0: there are no more
+  Tile t;
+  int tile0, tile1;      // this CTA's tiles
+  Span span, half[2];    // of both halves (the boxes), and of each
+  Plain plain, half_plain[2];
+};
+constexpr int kItems = 4;  // in shared memory, so that the copies need not wait for the other roles
+static_assert(kItems * sizeof(Item) <= 1024, "items in shared memory");
 // a value that is the same in all lanes, as one that the compiler knows to be
 __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
@@ -216,9 +220,12 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   uint64_t* unclear = q_full + 9;  // ... have landed
   uint64_t* turn = q_full + 10;    // [2] the half's turn at the tensor cores
   uint64_t* bar_fin = q_full + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 18);
+  uint64_t* item_full = q_full + 18;   // [kItems] an item handed over
+  uint64_t* item_empty = item_full + kItems;  // ... and done with, by the warps of the other roles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kItems);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* order = reinterpret_cast<uint8_t*>(tmem_slot + 2);  // [kMostOrdered]
+  Item* items = reinterpret_cast<Item*>(sm + L::kItems);
   // reference and sum of weights of 256 rows, in Q's place once the item's products are done (SPLIT)
   float2* sums = reinterpret_cast<float2*>(sm);
 
@@ -230,7 +237,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
   }
-  // Items of this CTA: every role walks them by itself, one ahead.
+  // Items of this CTA: all warps look up the first, the copy warp the others.
   Walk walk;
   if (SPLIT && p.ordered) {
     order_by_length(p.lengths, p.N, order);
@@ -251,11 +258,19 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     if (SPLIT) split = parts_of(p, tiles);
     it.tile0 = SPLIT ? (int)((int64_t)tiles * rank / split) : 0;
     it.tile1 = SPLIT ? (int)((int64_t)tiles * (rank + 1) / split) : tiles;
+    it.plain = plain_tiles(it.span, it.span, box_shift);
+    for (int h = 0; h < 2; ++h) {
+      const int first = a + h * span_tokens, last = min(first + span_tokens, a + p.by_G.div(it.t.rows));
+      it.half[h] = first < last ? span_of(p, it.t, first, last, box_shift) : it.span;
+      it.half_plain[h] = plain_tiles(it.span, it.half[h], box_shift);
+    }
     return true;
   };
   Item coming;
   bool have = next(coming);
   if (SPLIT && (!have || rank >= split)) return;
+  coming.have = have;
+  if (warp == kCopyWarp && lane == 0) items[0] = coming;
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -276,6 +291,10 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
     }
     mbar_init(cleared, 1);
     mbar_init(unclear, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kThreads / 32 - 1);
+    }
     mbar_init(bar_fin, 2);
     *abort_flag = 0;
     mbar_fence_init();
@@ -285,34 +304,38 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  auto half_span = [&](const Item& it, int h) {
-    const int first = p.by_G.div(it.t.first), a = first + h * span_tokens, b = min(a + span_tokens, first + p.by_G.div(it.t.rows));
-    return span_of(p, it.t, a, b, box_shift);
-  };
   const Waiter w{abort_flag, p.waits == kWaitsGiveUp};
   bool ok = true;
   int64_t issued = 0, q_issued = 0;  // copies started (copy warp)
-  Item it;
+  // For the other roles: item n; done with it, on to the next.
+  auto wait_item = [&](int n) { ok = w.hold(&item_full[n % kItems], (uint32_t)(n / kItems & 1)); };
+  auto advance = [&](int& n) {
+    warp_arrive(&item_empty[n % kItems]);
+    wait_item(++n);
+  };
 
   if (warp < 8) {
     // ======================== softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int h = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t ts = tmem_lane(tmem, warp) + kTmS + 128 * h, to = tmem_lane(tmem, warp) + kTmO + 128 * h;
-    uint32_t seen = 0, items = 0;  // scores and items so far: the barriers' phases
-    while (ok && have) {
-      it = coming;
+    uint32_t seen = 0;  // scores so far: the barriers' phase
+    int n = 0;
+    wait_item(n);
+    while (ok && items[n % kItems].have) {
+      const Item& it = items[n % kItems];
       const int rows = min(half_rows, it.t.rows - h * half_rows);
       const bool live = row < rows;
       const int r = it.t.first + h * half_rows + (live ? row : 0);  // in the request
       float m = kLowest, l = 0.f;
       bool any = false;
       if (rows > 0) {
-        const Span span = half_span(it, h);
+        const Span& span = it.half[h];
         const Row keys = row_keys(p, it.t, p.by_G.div(r));
-        const Plain plain = plain_tiles(it.span, span, box_shift);
+        const Plain plain = it.half_plain[h];
+        const int tile1 = it.tile1;
 #pragma unroll 1
-        for (int j = it.tile0; j < it.tile1; ++j) {
+        for (int j = it.tile0; j < tile1; ++j) {
           const bool whole = j >= plain.first && j < plain.end;
           if (!whole && !tile_seen(p, it.span, span, j, box_shift)) continue;
           ok = w.hold(&s_full[h], seen & 1);
@@ -389,10 +412,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
       }
       if (!ok) break;
-      have = next(coming);  // before the wait for the item's last products
-      ok = w.hold(&o_done[h], items & 1);
+      ok = w.hold(&o_done[h], (uint32_t)(n & 1));
       if (!ok) break;
-      ++items;
       tc_fence_after();
       if (SPLIT && split > 1) {
         // sums into the ring (all its tiles have been read), pieces of 16 bytes permuted by the row
@@ -446,13 +467,17 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         }
         tc_fence_before();  // O is read before the next item's weights are told
       }
+      if (SPLIT) break;
+      advance(n);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kCopyWarp) {
       // ======================== copies
+      int n = 0;
+      warp_arrive(&item_full[0]);
       while (ok && have) {
-        it = coming;
+        const Item it = coming;
         auto copy_q = [&]() {
           if (q_issued > 0) ok = w.hold(q_empty, (uint32_t)((q_issued - 1) & 1));
           if (!ok) return;
@@ -469,6 +494,12 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         };
         auto look_ahead = [&]() {
           have = next(coming);
+          ++n;
+          if (n >= kItems) ok = w.hold(&item_empty[n % kItems], (uint32_t)((n / kItems - 1) & 1));
+          if (!ok) return;
+          coming.have = have;
+          if (lane == 0) items[n % kItems] = coming;
+          warp_arrive(&item_full[n % kItems]);
           if (!have) return;
           // Towards L2, as all CTAs come to their next items at about the same time: its queries, and its last keys and
           // values (of a prompt: those that no item before it has read).
@@ -554,14 +585,14 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       const bool works = !(p.waits == kFirstCtaStalls && blockIdx.x == 0);
       int stage = 0;  // of the next tile in the ring, and its phase
       uint32_t phase = 0, weights = 0, clears = 0, q_used = 0, turns = h ^ 1;  // (half 0 has the first turn)
-      have = __any_sync(0xffffffffu, have);
-      while (works && ok && have) {
-        it = coming;
+      int n = 0;
+      wait_item(n);
+      while (works && ok && same(items[n % kItems].have)) {
+        const Item& it = items[n % kItems];
         const int tile0 = same(it.tile0), tile1 = same(it.tile1);
         const bool rows = same(it.t.rows) > h * half_rows;
-        const Plain plain = plain_tiles(it.span, it.span, box_shift);
-        const int plain0 = same(plain.first), plain1 = same(plain.end);
-        const Span span = rows ? half_span(it, h) : it.span;
+        const int plain0 = same(it.plain.first), plain1 = same(it.plain.end);
+        const Span& span = it.half[h];
         ok = w.poll(q_full, q_used & 1);
         q_used ^= 1;
         bool pending = false, begun = false, clean = true, left = false;  // weights to come, O begun, V as it came, Q given up
@@ -580,8 +611,6 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
             }
             ok = w.poll(&full[stage], phase);
             if (!ok) break;
-          } else {
-            have = __any_sync(0xffffffffu, next(coming));
           }
           if (j > tile0) {
             ok = clean ? w.poll(&full[v_stage], v_phase) : w.poll(cleared, clears);
@@ -649,13 +678,16 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           mma_commit_by(leader, &o_done[h ^ 1]);
           break;
         }
+        advance(n);
       }
     } else if (warp == kClearWarp) {
       // ======================== values that no row sees
       // (told of a tile's arrival by the MMA warp, which follows the ring; a wait that skips phases would mistake them)
       uint32_t used = 0, tiles = 0;
-      for (; ok && have; have = next(coming)) {
-        it = coming;
+      int n = 0;
+      wait_item(n);
+      while (ok && items[n % kItems].have) {
+        const Item& it = items[n % kItems];
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1 && ok; ++j, used += 2) {
           if (!unclean(it.span, j, box_shift)) continue;
@@ -678,6 +710,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           warp_arrive(cleared);
         }
         if (SPLIT) break;
+        advance(n);
       }
     }
   }
@@ -703,12 +736,9 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
 
   // the cluster's CTAs join: each a part of the rows
   if (*abort_flag && tid < 256) sums[tid] = make_float2(kLowest, kGone);
-  walk.base = walk.tiles = 0;
-  at = blockIdx.x / p.split;
-  next(coming);
   cluster_sync();
   {
-    const Tile& t = coming.t;
+    const Tile& t = items[0].t;
     constexpr int kPieces = D / 8;  // a thread's eight values
     const int each = 256 / split;
     for (int i = tid; i < each * kPieces; i += kThreads) {
