@@ -41,7 +41,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 11;  // (MMAs: two warps)
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;  // (184 and 136: 10 % slower)
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // (184 and 136: 10 % slower)
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr int kHalf = 128, kKeys = 128;
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key
