@@ -76,6 +76,13 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = p.split > 1 ? (int)(blockIdx.x % p.split) : 0;
 
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full[i], 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  griddep_wait();
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
@@ -88,11 +95,6 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int split = parts_of(p, span.boxes);
   if (rank >= split) return;
   if (split > 1) cluster_arrive();  // this CTA has begun: others may write to its memory
-  if (tid == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&full[i], 1);
-    *abort_flag = 0;
-    mbar_fence_init();
-  }
   __syncthreads();
   const int box0 = split > 1 ? (int)((int64_t)span.boxes * rank / split) : 0;
   const int box1 = split > 1 ? (int)((int64_t)span.boxes * (rank + 1) / split) : span.boxes;
@@ -377,18 +379,7 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   p.by_each = divisor((p.G + kRows - 1) / kRows);
   split_of(tiles, most_keys(a, kRows), sms, &p.split, &p.least);
   TraceScope ts("kda_attention_rows", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_rows_kernel<D>, maps, p);
+  return launch_overlapped(attention_rows_kernel<D>, (unsigned)(tiles * p.split), kThreads, Layout<D>::kSmem, (unsigned)p.split, st, maps, p);
 }
 
 }  // namespace

@@ -233,6 +233,8 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   const int rank = SPLIT ? (int)(blockIdx.x % p.split) : 0;
   int split = 1;
   const int G = p.G, half_rows = p.half_rows, span_tokens = p.by_G.div(half_rows);  // of a half
+  griddep_launch_dependents();
+  griddep_wait();
   if (p.cu != nullptr && !offsets_within(p.cu, p.N, p.T)) {
     if (tid == 0) atomicOr(p.err, KDA_DEVERR_BAD_SEQLENS);
     return;
@@ -798,18 +800,7 @@ cudaError_t launch_one(const Maps& maps, const QMap& qmap, const Params& p, int 
   });
   if (e != cudaSuccess) return e;
   TraceScope ts("kda_attention_tc", st);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Layout<D>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_tc_kernel<D, SPLIT>, maps, qmap, p, box_shift);
+  return launch_overlapped(attention_tc_kernel<D, SPLIT>, grid, kThreads, Layout<D>::kSmem, (unsigned)p.split, st, maps, qmap, p, box_shift);
 }
 
 template <int D>

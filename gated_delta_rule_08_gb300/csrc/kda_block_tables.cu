@@ -15,6 +15,7 @@
 // 256 requests of one token 6.4 us, 1000 requests with 39494 tokens in all 12.5 us.
 #include "kda_device.cuh"
 #include "kda_internal.h"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -53,6 +54,8 @@ __global__ void __launch_bounds__(kThreads)
 block_tables_kernel(const BlockTablesArgs p) {
   extern __shared__ int32_t sm[];
   __shared__ Sums warp_sums[32];
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
   const int N = p.N, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* first = sm;              // first new token of each request
   int32_t* taken = first + N + 1;   // blocks taken by the requests before
@@ -189,19 +192,9 @@ cudaError_t block_tables_launch(const BlockTablesArgs& a, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   TraceScope ts("kda_block_tables", st);
-  cudaLaunchConfig_t cfg{};
   const unsigned ctas = a.T <= kPerCta ? 1 : kCluster;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(a.N <= kFewThreads && a.T <= 8 * kFewThreads ? kFewThreads : kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(a.N);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_tables_kernel, a);
+  const unsigned threads = a.N <= kFewThreads && a.T <= 8 * kFewThreads ? kFewThreads : kThreads;
+  return launch_overlapped(block_tables_kernel, ctas, threads, smem_bytes(a.N), ctas, st, a);
 }
 
 }  // namespace kda

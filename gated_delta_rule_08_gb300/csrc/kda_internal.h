@@ -265,6 +265,28 @@ struct MatmulArgs {
 };
 cudaError_t matmul_fp8_launch(const MatmulArgs& a, cudaStream_t stream);
 
+// A launch that may start while the kernel before it in the stream drains, in clusters of `cluster` CTAs.  The kernel calls
+// griddep_wait() in all its threads before it touches memory or returns, so that it sees what the one before wrote
+// and does not complete before it.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- an attention layer over a paged cache (kda_attention_api.cu dispatches to them).  block_size is 1 << shift.
 
 constexpr int kMaxTableRequests = 8192;  // their sums lie in shared memory

@@ -18,6 +18,7 @@
 // shared memory: 102 us); one token 4.5 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 6.2 us (latency).
 #include "kda_device.cuh"
 #include "kda_internal.h"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -87,6 +88,8 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
 template <typename Tin, bool ADJ>
 __global__ void __launch_bounds__(kThreads)
 rope_append_kernel(const RopeArgs p, const int parts) {
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
   constexpr int kAhead = sizeof(Tin) == 2 ? 4 : 2;  // heads a lane has under way: 128 bytes
   const int lane = threadIdx.x & 31;
   const int per_head = p.d / 16, at_once = 32 / per_head;  // lanes of a head, heads of a warp
@@ -198,8 +201,7 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t st) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int parts = a.T <= kFewTokens ? 4 : 1;
   const int64_t blocks = (a.T * parts + kWarps - 1) / kWarps, most = (int64_t)sms * kBlocks;
-  rope_append_kernel<Tin, ADJ><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, st>>>(a, parts);
-  return cudaGetLastError();
+  return launch_overlapped(rope_append_kernel<Tin, ADJ>, (unsigned)(blocks < most ? blocks : most), kThreads, 0, 1, st, a, parts);
 }
 
 }  // namespace
