@@ -20,17 +20,17 @@
 // Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 and 10 the halves' MMAs, 11 clears.  The two MMA warps take turns
 // at the tensor cores (without turns both halves fall into step, and softmax and products no longer overlap: 2.2 ms
 // instead of 1.5 for the first case below), and each passes its turn on before its QK, because that takes
-// some 500 clocks.  A CTA an SM walks over items (a request's last tiles first, which have the most keys), each role
-// one item ahead; few items, and trees: a cluster of CTAs shares the keys of one and joins through distributed
+// some 500 clocks.  A CTA an SM walks over items (a request's last tiles first, which have the most keys), which the
+// copy warp looks up ahead and hands to the others; few items, and trees: a cluster of CTAs shares the keys of one and joins through distributed
 // shared memory, cut by the request's own length, the longest first.
 //
-// Measured on GB300 (bf16, 32 heads of 8 key heads, d = 128): 16384 tokens, all keys: 1.55 ms in a graph of its own (1.40
-// PFLOP/s of the pairs a token sees; 1.65 ms once the power limit takes hold); 8192 tokens, a window of 1024 and 4 sinks:
-// 152 us (0.84 PFLOP/s); 32 trees of 64 drafted tokens over 500 to 16000: 194 us (3.3 TB/s).  Five parts of prompts, up to
-// 2000 tokens over 9000, 20 heads of 4, d = 64, a window of 4096: 108 us.
+// Measured on GB300 (bf16, 32 heads of 8 key heads, d = 128): 16384 tokens, all keys: 1.54 ms by itself (1.41
+// PFLOP/s of the pairs a token sees; 1.62 ms once the power limit takes hold); 8192 tokens, a window of 1024 and 4 sinks:
+// 144 us (0.89 PFLOP/s); 32 trees of 64 drafted tokens over 500 to 16000: 185 us (3.5 TB/s).  Five parts of prompts, up to
+// 2000 tokens over 9000, 20 heads of 4, d = 64, a window of 4096: 105 us.
 // Bound in long prompts by a half's chain from scores to scores: softmax 1250 clocks (of them 700 exponentials, rounding and
 // stores), PV 500 to 600, QK 650 to 700, two hand-overs of 150; the tensor cores are busy for 2300 of the 2800 clocks that
-// the halves need for a tile.  A window's items have ten tiles and some 12 thousand clocks between them (sums
+// the halves need for a tile.  A window's items have ten tiles and 6 to 8 thousand clocks between them (sums
 // read and stored, the next queries).  Trees: a CTA starts and joins in 15 us, in which it reads nothing.
 #include "kda_attention.cuh"
 
@@ -41,7 +41,7 @@ using namespace attn;
 
 constexpr int kThreads = 384;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kClearWarp = 11;  // (MMAs: two warps)
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // (184 and 136: 10 % slower)
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // (208 and 88: 2 to 6 % slower)
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
 constexpr int kHalf = 128, kKeys = 128;
 constexpr float kLowest = -3.402823466e38f;  // below every score: a weight relative to it is 0 for a masked key

@@ -14,8 +14,8 @@
 // into fixed point once, as a warp walks over tokens.
 //
 // Bound by HBM for many tokens: every value read once and written once.  Measured on GB300: 16384 tokens of 32 + 2 x 8
-// heads of 128 in bf16, three axes: 67.5 us, 6.0 TB/s (88 % of the measured copy; by blocks of four tokens with the cosines in
-// shared memory: 102 us); one token 4.5 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 6.2 us (latency).
+// heads of 128 in bf16, three axes: 65 us, 6.2 TB/s (91 % of the measured copy; by blocks of four tokens with the cosines in
+// shared memory: 102 us); one token 4.6 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 5.7 us (latency).
 #include "kda_device.cuh"
 #include "kda_internal.h"
 #include "tc_ptx.cuh"

@@ -317,7 +317,7 @@ kda_status kda_linear_decode_step(const void* q, const void* k, const void* v, c
 /* ---- An attention layer over a paged cache (serving), as models mix it with recurrent layers.  The cache is a pool
  * of blocks of block_size tokens (16, 32, 64, 128 or 256), for keys and for values:
  *   k_cache, v_cache : [num_blocks, block_size, Hkv, d] bf16.  The d values of a head are dense; blocks, tokens and
- *                      heads lie cache_strides[0], [1] and [2] elements apart (both caches alike; multiples of 8),
+ *                      heads lie cache_strides[0], [1] and [2] elements apart (both caches alike; at least d, multiples of 8),
  *                      so a layout [num_blocks, Hkv, block_size, d] is one of strides
  *   block_tables     : [N, max_blocks] int32 device; token p of request n lies in block block_tables[n][p / block_size]
  *   d in {64, 128};  H a multiple of Hkv, H / Hkv at most 128 (KDA_ERR_UNSUPPORTED otherwise).
