@@ -12,7 +12,7 @@
 // read and written are different ones.
 //
 // Bound by latency (launch, the loads of counts and lengths, the running sums, then ring and table).  Measured on GB300:
-// 256 requests of one token 6.4 us, 1000 requests with 39494 tokens in all 12.5 us.
+// 256 requests of one token 6.4 us, 1000 requests with 39494 tokens in all 10.4 us (a cluster of 8: 12.5).
 #include "kda_device.cuh"
 #include "kda_internal.h"
 #include "tc_ptx.cuh"
@@ -21,8 +21,8 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 1024, kFewThreads = 256;  // (a CTA of fewer warps starts sooner)
-constexpr int kCluster = 8;
-constexpr int kPerCta = 8192;  // tokens that one CTA handles before the others are worth their start
+constexpr int kCluster = 16;
+constexpr int kPerCta = 4096;  // tokens that one CTA handles before the others are worth their start
 
 struct Sums {
   int64_t tokens;
@@ -187,8 +187,9 @@ cudaError_t block_tables_launch(const BlockTablesArgs& a, cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   cudaError_t e = once.run(dev, [] {
-    return cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)smem_bytes(kMaxTableRequests));
+    const cudaError_t f = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem_bytes(kMaxTableRequests));
+    return f == cudaSuccess ? cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : f;
   });
   if (e != cudaSuccess) return e;
   TraceScope ts("kda_block_tables", st);
