@@ -115,7 +115,8 @@ __device__ __forceinline__ bool offsets_within(const int32_t* __restrict__ cu, i
   return !__syncthreads_or(bad);
 }
 
-constexpr int kMaxLength = 1 << 30;  // tokens of a request: 32-bit places of keys run some tiles past it
+// Tokens of a request: its tiles take some 0.2 s of a CTA, and a role may wait for another one that long, out of half a second.
+constexpr int kMaxLength = 1 << 24;
 // A tile of rows of one request and key head.
 struct Tile {
   int n, head;         // request, key head

@@ -45,10 +45,10 @@
  *     looks for such slots too.  The check reads every
  *     g and beta once (decode: O(N^2) slot comparisons); it is off by default.
  *   - Testing: with the environment variable KDA_TEST_WAIT_TIMEOUT set (any value but "" or "0";
- *     read at every call) the prefill, kda_matmul_fp8 and kda_linear_chunk_fwd launch kernel variants
+ *     read at every call) the prefill, kda_matmul_fp8, kda_linear_chunk_fwd and the attentions launch kernel variants
  *     whose bounded waits on work of their own CTA give up at once, so that a test can make them run
  *     out and see KDA_DEVERR_WAIT_TIMEOUT reported with the device left usable.  With the value
- *     "stall" kda_matmul_fp8 and kda_linear_chunk_fwd launch variants whose first CTA starts no work,
+ *     "stall" kda_matmul_fp8, kda_linear_chunk_fwd and the attentions launch variants whose first CTA starts no work,
  *     so that its waits run out at their limit, about a second.  Not for production use.
  */
 #ifndef KDA_H_
@@ -376,7 +376,7 @@ kda_status kda_rope_append(const void* q, const void* k, const void* v, const do
  *   lengths      : [N] int32, tokens of request n in the cache, its new ones included
  *   cu_seqlens   : [N + 1] int32, where each request's new tokens begin in q; they are its last ones.  Offsets that do not
  *                  rise from 0 to at most T set KDA_DEVERR_BAD_SEQLENS, and nothing is written; a request of more new
- *                  tokens than its length, or longer than max_blocks * block_size or 2^30, sets it and is skipped.  Rows of
+ *                  tokens than its length, or longer than max_blocks * block_size or 2^24, sets it and is skipped.  Rows of
  *                  out behind the last request are left as they were
  *   window       : tokens a token sees, itself included; 0 means all.  sinks >= 0: first tokens that stay visible
  *   max_length   : no request is longer (a hint for how the work is split; 0: as long as the tables allow)
@@ -384,6 +384,7 @@ kda_status kda_rope_append(const void* q, const void* k, const void* v, const do
  * Keys and values of tokens that a row sees have to be finite.  What lies in the cache elsewhere may be anything, and
  * table entries of blocks that no new token sees are not read.  A block that is, outside [0, num_blocks),
  * sets KDA_DEVERR_BAD_SLOT; the rows of its request are then undefined (nothing outside the cache is read).
+ * The mean number of new tokens decides how the work is done, so prompts and single tokens are faster in calls of their own.
  * Scores, softmax and sums are fp32; the weights are rounded to bf16 for their product with the values. */
 kda_status kda_window_attention_fwd(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                     const int32_t* lengths, const int32_t* cu_seqlens, void* out, int N, int64_t T,
@@ -392,7 +393,7 @@ kda_status kda_window_attention_fwd(const void* q, const void* k_cache, const vo
                                     int64_t max_length, float scale, void* stream);
 
 /* The same for one new token of each request: q, out [N, H, d], request n's token being its last (position
- * lengths[n] - 1).  A request of length 0 gets zeros; one below 0 or longer than its table sets KDA_DEVERR_BAD_SEQLENS and
+ * lengths[n] - 1).  A request of length 0 gets zeros; one below 0 or longer than its table or 2^24 sets KDA_DEVERR_BAD_SEQLENS and
  * is skipped. */
 kda_status kda_window_attention_decode_step(const void* q, const void* k_cache, const void* v_cache,
                                             const int32_t* block_tables, const int32_t* lengths, void* out, int N, int H,
