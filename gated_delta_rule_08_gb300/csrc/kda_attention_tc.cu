@@ -217,7 +217,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
   uint64_t* p_ready = q_full + 14;  // [2][2] weights of half the keys written
   uint64_t* o_done = q_full + 6;   // [2] the item's products complete (split: both halves')
   uint64_t* cleared = q_full + 8;  // a tile's values cleared
-  uint64_t* unclear = q_full + 9;  // ... have landed
+  uint64_t* unclear = q_full + 9;  // ... have landed, and both MMA warps know of the tile cleared before
   uint64_t* turn = q_full + 10;    // [2] the half's turn at the tensor cores
   uint64_t* bar_fin = q_full + 12;
   uint64_t* item_full = q_full + 18;   // [kItems] an item handed over
@@ -292,7 +292,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       mbar_init(&o_done[h], SPLIT ? 2 : 1);
     }
     mbar_init(cleared, 1);
-    mbar_init(unclear, 1);
+    mbar_init(unclear, 2);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kThreads / 32 - 1);
@@ -667,9 +667,13 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
               stage = 0;
               phase ^= 1;
             }
-            if (!clean && h == 0) {
-              ok = w.poll(&full[v_stage], v_phase);
-              if (!ok) break;
+            if (!clean) {
+              // Both warps tell of the tile, each past its wait for the tile cleared before: `cleared` is then never two
+              // phases ahead of a warp, which would take it for the one that it waits for not to have come.
+              if (h == 0) {
+                ok = w.poll(&full[v_stage], v_phase);
+                if (!ok) break;
+              }
               warp_arrive(unclear);
             }
           }
@@ -684,7 +688,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       }
     } else if (warp == kClearWarp) {
       // ======================== values that no row sees
-      // (told of a tile's arrival by the MMA warp, which follows the ring; a wait that skips phases would mistake them)
+      // (told of a tile's arrival by the MMA warps, which follow the ring; a wait that skips phases would mistake them)
       uint32_t used = 0, tiles = 0;
       int n = 0;
       wait_item(n);
