@@ -679,6 +679,12 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           }
         }
         if (!ok) break;
+        if (!SPLIT && n > 0) {
+          // All roles are done with the item before: its o_done has been seen, and does not move on by two phases.  (They
+          // mostly have been for long; an item without keys, or without rows for this half, asks nothing of them.)
+          ok = w.poll(&item_empty[(n - 1) % kItems], (uint32_t)((n - 1) / kItems & 1));
+          if (!ok) break;
+        }
         mma_commit_by(leader, &o_done[h]);
         if (SPLIT) {
           mma_commit_by(leader, &o_done[h ^ 1]);

@@ -24,3 +24,28 @@ def test_items_whose_tiles_are_all_cleared(d, H, Hkv, window, sinks):
     want = b.run()
     b.check(want)
     repeats(b.run, want)
+
+
+@pytest.mark.parametrize("Hkv,N", [(1, 700), (8, 90)])
+def test_requests_without_keys_in_a_walk(Hkv, N):
+    """One token of each of more requests than there are SMs, 32 heads a key head: requests of length zero by themselves and
+    several in a row, between short and long ones, get zeros, and the others their rows."""
+    lengths = [(0, 1, 700, 0, 0, 0, 130, 3, 0, 0, 0, 0, 0, 0, 257, 40)[i * 7 % 16 if i % 100 < 60 else i % 16] for i in range(N)]
+    lengths[0], lengths[-1] = 0, 500
+    b = Batch([max(0, n - 1) for n in lengths], [1] * N, H=32 * Hkv, Hkv=Hkv, d=64, seed=Hkv)
+    b.lengths = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    for n, length in enumerate(lengths):
+        if length == 0:
+            b.see[n][:] = False
+    want = b.step()
+    b.check(want)
+    assert not want[b.lengths == 0].any()
+    repeats(b.step, want)
+
+
+def test_items_without_rows_in_their_second_half():
+    """One token of each request, 32 heads a key head: 32 rows of 256, so that the second half only takes its turns."""
+    b = Batch([(i * 37) % 200 for i in range(400)], [1] * 400, H=32, Hkv=1, d=128, window=90, sinks=3, seed=1)
+    want = b.step()
+    b.check(want)
+    repeats(b.step, want)
