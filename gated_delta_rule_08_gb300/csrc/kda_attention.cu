@@ -63,7 +63,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, bool TREES>
 __global__ void __launch_bounds__(kThreads)
 attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   using L = Layout<D>;
@@ -110,16 +110,26 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint64_t* bars = full + warp * kStages;
   const int count = box1 > box0 + warp ? (box1 - box0 - warp + kWarps - 1) / kWarps : 0;  // boxes of this warp
   const int32_t* table = p.tables + (int64_t)t.n * p.max_blocks;
+  // trees: which drafted tokens the CTA's rows see, from the first box on that holds some
+  uint64_t named = 0;
+  bool drafted = false;
   // the blocks of boxes [32 i, 32 i + 32) of this warp, one a lane
   auto block_ids = [&](int i) {
     const int at = 32 * i + lane;
-    int id = 0;
+    int id = 0, key = 0;
     if (at < count) {
-      id = table[box_key(span, box0 + warp + at * kWarps, kBoxShift) >> p.shift];
-      if ((unsigned)id >= (unsigned)p.num_blocks) {
-        atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-        id = p.num_blocks;  // reads as zeros
-      }
+      key = box_key(span, box0 + warp + at * kWarps, kBoxShift);
+      id = table[key >> p.shift];
+    }
+    bool used = true;  // by some row
+    if (TREES && __any_sync(0xffffffffu, at < count && key + kBox > t.before)) {
+      if (!drafted) named = named_by(p, t, token0, token1);
+      drafted = true;
+      used = used16<TREES>(p, t, span, named, key) != 0;
+    }
+    if (at < count && (!used || (unsigned)id >= (unsigned)p.num_blocks)) {
+      if (used) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+      id = p.num_blocks;  // reads as zeros
     }
     return id;
   };
@@ -187,7 +197,7 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
     const bool whole = all_seen(p, span, base, kBox);
     if (!whole) {
       // values that no row sees may be anything, and meet weights of 0 in the product: cleared
-      const uint32_t used = used16(p, span, base);
+      const uint32_t used = used16<TREES>(p, t, span, named, base);
       if (used != 0xffffu) {
         for (int i = lane; i < kBox * 8 * L::kParts; i += 32) {
           const int r = i & 15, j = i >> 4;
@@ -358,7 +368,7 @@ void split_of(int64_t tiles, int64_t keys, int sms, int* split, int* least) {
   while (*split < kMaxSplit && tiles * *split * 2 <= kMostCtas && keys > kMostKeys * *split) *split *= 2;
 }
 
-template <int D>
+template <int D, bool TREES>
 cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   Maps maps;
   if (!tensor_map_cache(&maps.k, a.k_cache, a.num_blocks, 1u << a.shift, a.Hkv, D, a.block_stride, a.token_stride, a.head_stride, kBox) ||
@@ -370,8 +380,8 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   const int sms = device_sms();
   if (sms <= 0) return cudaErrorInvalidDevice;
   cudaError_t e = once.run(dev, [] {
-    cudaError_t f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
-    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t f = cudaFuncSetAttribute(attention_rows_kernel<D, TREES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::kSmem);
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(attention_rows_kernel<D, TREES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return f;
   });
   if (e != cudaSuccess) return e;
@@ -379,13 +389,14 @@ cudaError_t launch(const AttentionArgs& a, Params p, cudaStream_t st) {
   p.by_each = divisor((p.G + kRows - 1) / kRows);
   split_of(tiles, most_keys(a, kRows), sms, &p.split, &p.least);
   TraceScope ts("kda_attention_rows", st);
-  return launch_overlapped(attention_rows_kernel<D>, (unsigned)(tiles * p.split), kThreads, Layout<D>::kSmem, (unsigned)p.split, st, maps, p);
+  return launch_overlapped(attention_rows_kernel<D, TREES>, (unsigned)(tiles * p.split), kThreads, Layout<D>::kSmem, (unsigned)p.split, st, maps, p);
 }
 
 }  // namespace
 
 cudaError_t attention_rows_launch(const AttentionArgs& a, cudaStream_t st) {
-  return a.d == 64 ? launch<64>(a, params_of(a), st) : launch<128>(a, params_of(a), st);
+  if (a.tree_mask) return a.d == 64 ? launch<64, true>(a, params_of(a), st) : launch<128, true>(a, params_of(a), st);
+  return a.d == 64 ? launch<64, false>(a, params_of(a), st) : launch<128, false>(a, params_of(a), st);
 }
 
 }  // namespace kda

@@ -309,9 +309,39 @@ __device__ __forceinline__ uint32_t seen16(const Params& p, const Tile& t, const
   }
   return m;
 }
-// Which of them some row of the span sees.
-__device__ __forceinline__ uint32_t used16(const Params& p, const Span& s, int base) {
-  return bits_between(base, s.lo, s.hi) | (p.sinks > 0 ? bits_between(base, 0, min(p.sinks - 1, s.hi)) : 0u);
+// Trees: 64 drafted tokens from 64 w on, those of them that some row of tokens [a, b) of the request sees (one warp together).
+__device__ __forceinline__ uint64_t named_word(const Params& p, const Tile& t, int a, int b, int w) {
+  uint32_t lo = 0, hi = 0;
+  for (int i = a + (int)(threadIdx.x & 31); i < b; i += 32) {
+    const uint64_t m = p.mask[(int64_t)(t.t0 + i) * p.mask_words + w];
+    lo |= (uint32_t)m;
+    hi |= (uint32_t)(m >> 32);
+  }
+  return (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 | __reduce_or_sync(0xffffffffu, lo);
+}
+// All of them, word w in lane w.
+__device__ __forceinline__ uint64_t named_by(const Params& p, const Tile& t, int a, int b) {
+  uint64_t mine = 0;
+#pragma unroll 1
+  for (int w = 0; w * 64 < t.tokens; ++w) {
+    const uint64_t word = named_word(p, t, a, b, w);
+    if ((int)(threadIdx.x & 31) == w) mine = word;
+  }
+  return mine;
+}
+// Which of the 16 keys from `base` on some row of the span sees.  Trees: `named` as above for the span's tokens, one warp
+// together (each lane may have a base of its own).  TREES says that there may be masks.
+template <bool TREES>
+__device__ __forceinline__ uint32_t used16(const Params& p, const Tile& t, const Span& s, uint64_t named, int base) {
+  const int hi = TREES && p.mask ? t.before - 1 : s.hi;
+  uint32_t m = bits_between(base, s.lo, hi) | (p.sinks > 0 ? bits_between(base, 0, min(p.sinks - 1, hi)) : 0u);
+  if (TREES && p.mask) {
+    const int off = base - t.before, i = off > 0 ? off >> 6 : 0, sh = off & 63;
+    const uint64_t w = __shfl_sync(0xffffffffu, named, i & 31), next = __shfl_sync(0xffffffffu, named, (i + 1) & 31);
+    const uint64_t drafted = off <= -16 ? 0 : off < 0 ? w << -off : sh > 48 ? w >> sh | next << (64 - sh) : w >> sh;
+    m |= (uint32_t)drafted & bits_between(base, t.before, t.len - 1);
+  }
+  return m;
 }
 // Whether every row of the span sees all keys of [base, base + n).
 __device__ __forceinline__ bool all_seen(const Params& p, const Span& s, int base, int n) {

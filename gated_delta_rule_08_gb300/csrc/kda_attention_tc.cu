@@ -150,15 +150,29 @@ __device__ __forceinline__ bool tile_seen(const Params& p, const Span& boxes, co
   const int shift = place_shift(boxes, box_shift), first = j * kKeys;
   return (first < rows.hi + 1 - shift && first + kKeys > rows.lo - shift) || first < min(p.sinks, rows.hi + 1);
 }
-// Whether tile j may hold keys that no row of the item sees.
-__device__ __forceinline__ bool unclean(const Span& s, int j, int box_shift) {
+// Whether tile j may hold keys that no row of the item sees (of drafted tokens, those that no mask names).
+template <bool TREES>
+__device__ __forceinline__ bool unclean(const Params& p, const Tile& t, const Span& s, int j, int box_shift) {
   const int shift = place_shift(s, box_shift), first = j * kKeys;
-  return first < s.lo - shift || first + kKeys > s.hi + 1 - shift;
+  return first < s.lo - shift || first + kKeys > (TREES && p.mask ? t.before : s.hi + 1) - shift;
 }
 // Bits [a, b) of 32.
 __device__ __forceinline__ uint32_t bits(int a, int b) {
   const uint32_t below_a = a <= 0 ? 0u : a >= 32 ? ~0u : (1u << a) - 1u, below_b = b <= 0 ? 0u : b >= 32 ? ~0u : (1u << b) - 1u;
   return below_b & ~below_a;
+}
+// Trees: whether some row of the tile sees one of the keys [key, key + n), a box of its span (one warp together, each lane a
+// box of its own).
+__device__ __forceinline__ bool box_used(const Params& p, const Tile& t, const Span& s, int key, int n) {
+  const int a = p.by_G.div(t.first), b = a + p.by_G.div(t.rows);
+  bool used = key < t.before && (s.lo < t.before || key < p.sinks);
+#pragma unroll 1
+  for (int w = 0; w * 64 < t.tokens; ++w) {
+    const uint64_t named = named_word(p, t, a, b, w);
+    const int x = key - t.before - 64 * w, y = min(x + n, t.tokens - 64 * w);
+    used |= ((uint32_t)named & bits(x, y)) != 0 || ((uint32_t)(named >> 32) & bits(x - 32, y - 32)) != 0;
+  }
+  return used;
 }
 // Which keys of tile j a row sees, a bit each.
 __device__ __forceinline__ uint4 row_mask(const Params& p, const Tile& t, const Span& s, const Row& r, int j, int box_shift) {
@@ -202,7 +216,7 @@ static_assert(kItems * sizeof(Item) <= 1024, "items in shared memory");
 // a value that is the same in all lanes, as one that the compiler knows to be
 __device__ __forceinline__ int same(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// SPLIT: an item a cluster, whose p.split CTAs share its keys; else a CTA walks over items.
+// SPLIT: an item a cluster, whose p.split CTAs share its keys; else a CTA walks over items, which are not trees'.
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ QMap qmap, const Params p, const int box_shift) {
@@ -527,14 +541,15 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
         const int per = kKeys >> box_shift;  // boxes of a tile, at most 8
         // a lane has a box of four tiles at a time
         auto block_ids = [&](int j) {
-          const int box = j * per + lane;
-          int id = 0;
-          if (lane < 4 * per && box < it.span.boxes && box < it.tile1 * per) {
-            id = table[box_key(it.span, box, box_shift) >> p.shift];
-            if ((unsigned)id >= (unsigned)p.num_blocks) {
-              atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-              id = p.num_blocks;  // reads as zeros
-            }
+          const int box = j * per + lane, key = box_key(it.span, box, box_shift);
+          const bool mine = lane < 4 * per && box < it.span.boxes && box < it.tile1 * per;
+          int id = mine ? table[key >> p.shift] : 0;
+          // by some row: of a tree's boxes, those that end before the drafted tokens are
+          const bool used = !SPLIT || !p.mask || !__any_sync(0xffffffffu, mine && key + (1 << box_shift) > it.t.before) ||
+                            box_used(p, it.t, it.span, key, 1 << box_shift);
+          if (mine && (!used || (unsigned)id >= (unsigned)p.num_blocks)) {
+            if (used) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+            id = p.num_blocks;  // reads as zeros
           }
           return id;
         };
@@ -609,7 +624,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
             active = rows;
             if (j < plain0 || j >= plain1) {
               active = rows && __any_sync(0xffffffffu, tile_seen(p, it.span, span, j, box_shift));
-              next_clean = !__any_sync(0xffffffffu, unclean(it.span, j, box_shift));
+              next_clean = !__any_sync(0xffffffffu, unclean<SPLIT>(p, it.t, it.span, j, box_shift));
             }
             ok = w.poll(&full[stage], phase);
             if (!ok) break;
@@ -700,9 +715,12 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
       wait_item(n);
       while (ok && items[n % kItems].have) {
         const Item& it = items[n % kItems];
+        const bool drafted = SPLIT && p.mask && it.tile1 * kKeys > it.t.before - place_shift(it.span, box_shift);  // in its tiles
+        const int a = p.by_G.div(it.t.first);
+        const uint64_t named = drafted ? named_by(p, it.t, a, a + p.by_G.div(it.t.rows)) : 0;
 #pragma unroll 1
         for (int j = it.tile0; j < it.tile1 && ok; ++j, used += 2) {
-          if (!unclean(it.span, j, box_shift)) continue;
+          if (!unclean<SPLIT>(p, it.t, it.span, j, box_shift)) continue;
           const int s = (int)((used + 1) % L::kStages);
           ok = w.hold(unclear, tiles & 1);
           if (!ok) break;
@@ -710,7 +728,7 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           uint8_t* st = sm + L::kRing + s * L::kTile;
           for (int g = 0; g < 8; ++g) {
             const int base = group_key(it.span, j, g, box_shift);
-            const uint32_t keep = base < 0 ? 0u : used16(p, it.span, base);
+            const uint32_t keep = base < 0 ? 0u : used16<SPLIT>(p, it.t, it.span, named, base);
             if (keep == 0xffffu) continue;
             for (int i = lane; i < 16 * 8 * L::kParts; i += 32) {
               const int r = i & 15, c = i >> 4;
