@@ -10,9 +10,11 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/SmallVector.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cmath>
 #include <sstream>
 #include <string>
@@ -88,6 +90,14 @@ int device_of(const at::Tensor& t, const char* name) {
                                  std::to_string(current));
   return index;
 }
+// Lets other Python threads run while it lives: allocations and launches may wait for the device, and what the device waits
+// for may need the interpreter.  (The caller's frame keeps the arguments' tensors.)
+struct Released {
+  PyThreadState* const state = PyEval_SaveThread();
+  Released() = default;
+  Released(const Released&) = delete;
+  ~Released() { PyEval_RestoreThread(state); }
+};
 // The address of a dense tensor of that type, shape and device.
 template <class T>
 T* data(const at::Tensor* t, const char* name, at::ScalarType dtype, at::IntArrayRef shape, int index) {
@@ -98,13 +108,27 @@ T* data(const at::Tensor* t, const char* name, at::ScalarType dtype, at::IntArra
   shaped(*t, name, shape);
   return static_cast<T*>(t->data_ptr());
 }
-// ... of one that is given, or a new one
-at::Tensor output(PyObject* o, const char* name, at::ScalarType dtype, at::IntArrayRef shape, int index) {
-  if (const at::Tensor* t = tensor(o, name, true)) {
-    data<void>(t, name, dtype, shape, index);
-    return *t;
+// Outputs: dense tensors of that type, shape and device that are given, or new ones.
+struct Wanted {
+  PyObject* given;
+  const char* name;
+  c10::SmallVector<int64_t, 3> shape;
+};
+template <size_t N>
+std::array<at::Tensor, N> outputs(const Wanted (&wanted)[N], at::ScalarType dtype, int index) {
+  std::array<at::Tensor, N> r;
+  bool all = true;
+  for (size_t i = 0; i < N; ++i) {
+    const at::Tensor* t = tensor(wanted[i].given, wanted[i].name, true);
+    data<void>(t, wanted[i].name, dtype, wanted[i].shape, index);
+    if (t) r[i] = *t; else all = false;
   }
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)index));
+  if (all) return r;
+  const Released other_threads;
+  const auto options = at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)index);
+  for (size_t i = 0; i < N; ++i)
+    if (!r[i].defined()) r[i] = at::empty(wanted[i].shape, options);
+  return r;
 }
 // [tokens, heads, d] whose heads are dense and whose tokens may lie further apart: the distance of two tokens.
 int64_t token_rows(const at::Tensor& t, const char* name, at::ScalarType dtype, at::IntArrayRef shape, int index) {
@@ -144,7 +168,14 @@ struct Caches {
 
 void* stream_of(int index) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream(); }
 
-void done(const char* fn, int status) {
+// Calls an entry point, whose arguments have been formed, and raises what it answers.
+template <class F, class... A>
+void call(const char* fn, F entry, A... args) {
+  int status;
+  {
+    const Released other_threads;
+    status = entry(args...);
+  }
   if (status == 0) return;
   if (PyObject* e = PyObject_CallFunction(g.error, "si", fn, status)) {
     PyErr_SetObject(g.error, e);
@@ -207,13 +238,11 @@ PyObject* block_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* pt = data<int32_t>(&table, "block_tables", i32, {N, width}, dev);
     int32_t* pr = data<int32_t>(&ring, "free_ring", i32, {blocks}, dev);
     const int32_t* ps = data<int32_t>(&state, "free_state", i32, {2}, dev);
-    const at::Tensor now = output(a[7], "new_lengths", i32, {N}, dev), left = output(a[8], "new_free_state", i32, {2}, dev);
-    const at::Tensor slot = output(a[9], "slot_map", i32, {T}, dev), pos = output(a[10], "positions", i32, {T}, dev);
-    const at::Tensor cu = output(a[11], "cu_seqlens", i32, {N + 1}, dev);
-    done("kda_block_tables",
-         g.block_tables(pc, pl, pt, pr, ps, now.data_ptr<int32_t>(), left.data_ptr<int32_t>(), slot.data_ptr<int32_t>(),
-                        pos.data_ptr<int32_t>(), cu.data_ptr<int32_t>(), narrow(N, "block_tables"), narrow(width, "block_tables"),
-                        narrow(blocks, "free_ring"), small(a[5], "block_size"), T, stream_of(dev)));
+    const auto [now, left, slot, pos, cu] = outputs({{a[7], "new_lengths", {N}}, {a[8], "new_free_state", {2}}, {a[9], "slot_map", {T}},
+                                                     {a[10], "positions", {T}}, {a[11], "cu_seqlens", {N + 1}}}, i32, dev);
+    call("kda_block_tables", g.block_tables, pc, pl, pt, pr, ps, now.data_ptr<int32_t>(), left.data_ptr<int32_t>(),
+         slot.data_ptr<int32_t>(), pos.data_ptr<int32_t>(), cu.data_ptr<int32_t>(), narrow(N, "block_tables"),
+         narrow(width, "block_tables"), narrow(blocks, "free_ring"), small(a[5], "block_size"), T, stream_of(dev));
     PyObject* r = PyTuple_New(5);
     if (!r) return nullptr;
     const at::Tensor* all[5] = {&slot, &pos, &cu, &now, &left};
@@ -248,11 +277,10 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* ps = data<int32_t>(&slot, "slot_map", at::kInt, {T}, dev);
     const int turned = PyObject_IsTrue(a[9]);
     if (turned < 0) throw PyError();
-    const at::Tensor out = output(a[10], "q_out", at::kBFloat16, {T, H, d}, dev);
-    done("kda_rope_append",
-         g.rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), pf, pa, pp, ps, out.data_ptr(), kc.data_ptr(), vc.data_ptr(), T,
-                       narrow(H, "q"), c.heads, c.d, narrow(2 * pairs, "inv_freq"), narrow(axes, "positions"), turned, qs, ks, vs,
-                       c.blocks, c.size, c.strides, dt == at::kBFloat16 ? KDA_DTYPE_BF16 : KDA_DTYPE_FP32, stream_of(dev)));
+    const auto [out] = outputs({{a[10], "q_out", {T, H, d}}}, at::kBFloat16, dev);
+    call("kda_rope_append", g.rope_append, q.data_ptr(), k.data_ptr(), v.data_ptr(), pf, pa, pp, ps, out.data_ptr(), kc.data_ptr(),
+         vc.data_ptr(), T, narrow(H, "q"), c.heads, c.d, narrow(2 * pairs, "inv_freq"), narrow(axes, "positions"), turned, qs, ks,
+         vs, c.blocks, c.size, c.strides, dt == at::kBFloat16 ? KDA_DTYPE_BF16 : KDA_DTYPE_FP32, stream_of(dev));
     return THPVariable_Wrap(out);
   });
 }
@@ -279,7 +307,7 @@ struct Attention {
     q_stride = token_rows(q, "q", at::kBFloat16, {T, H, c.d}, dev);
     tables = data<int32_t>(&table, "block_tables", at::kInt, {N, width}, dev);
     len = data<int32_t>(&lengths, "lengths", at::kInt, {N}, dev);
-    out = output(rest[0], "out", at::kBFloat16, {T, H, c.d}, dev);
+    out = outputs({{rest[0], "out", {T, H, c.d}}}, at::kBFloat16, dev)[0];
     window = small(rest[1], "window"); sinks = small(rest[2], "sinks");
     scale = rest[3] == Py_None ? (float)(1.0 / std::sqrt((double)c.d)) : (float)number(rest[3]);
     most = integer(rest[4]);
@@ -293,10 +321,9 @@ PyObject* window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want(n, 11);
     const Attention t(a, a + 6);
     const int32_t* cu = data<int32_t>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {t.N + 1}, t.dev);
-    done("kda_window_attention_fwd",
-         g.fwd(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, t.out.data_ptr(), (int)t.N, t.T, (int)t.H,
-               t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides, t.window, t.sinks, t.most, t.scale,
-               stream_of(t.dev)));
+    call("kda_window_attention_fwd", g.fwd, t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, t.out.data_ptr(),
+         (int)t.N, t.T, (int)t.H, t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides, t.window, t.sinks,
+         t.most, t.scale, stream_of(t.dev));
     return THPVariable_Wrap(t.out);
   });
 }
@@ -308,10 +335,9 @@ PyObject* window_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Attention t(a, a + 5);
     if (t.T != t.N)
       refuse(PyExc_ValueError, "q has " + std::to_string(t.T) + " tokens for " + std::to_string(t.N) + " requests");
-    done("kda_window_attention_decode_step",
-         g.step(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, t.out.data_ptr(), (int)t.N, (int)t.H, t.c.heads,
-                t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides, t.window, t.sinks, t.most, t.scale,
-                stream_of(t.dev)));
+    call("kda_window_attention_decode_step", g.step, t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len,
+         t.out.data_ptr(), (int)t.N, (int)t.H, t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width, t.c.strides,
+         t.window, t.sinks, t.most, t.scale, stream_of(t.dev));
     return THPVariable_Wrap(t.out);
   });
 }
@@ -326,10 +352,9 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rank(mask, "tree_mask", 2);
     const int64_t words = mask.size(1);
     const uint64_t* pm = data<uint64_t>(&mask, "tree_mask", at::kLong, {t.T, words}, t.dev);
-    done("kda_tree_attention",
-         g.tree(t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, pm, narrow(words, "tree_mask"),
-                t.out.data_ptr(), (int)t.N, t.T, (int)t.H, t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size, (int)t.width,
-                t.c.strides, t.window, t.sinks, t.most, t.scale, stream_of(t.dev)));
+    call("kda_tree_attention", g.tree, t.q.data_ptr(), t.kc.data_ptr(), t.vc.data_ptr(), t.tables, t.len, cu, pm,
+         narrow(words, "tree_mask"), t.out.data_ptr(), (int)t.N, t.T, (int)t.H, t.c.heads, t.c.d, t.q_stride, t.c.blocks, t.c.size,
+         (int)t.width, t.c.strides, t.window, t.sinks, t.most, t.scale, stream_of(t.dev));
     return THPVariable_Wrap(t.out);
   });
 }
