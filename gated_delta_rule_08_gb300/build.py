@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda.so")
 MARSHAL = os.path.join(PKG, "_kda_marshal.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+MARSHAL_FOR = os.path.join(BUILD_DIR, "marshal_for")  # what the module has been built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr"]
@@ -50,6 +52,18 @@ def _marshal_command(target: str) -> list:
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", target]
 
 
+def _marshal_stale(deps) -> bool:
+    """Whether the marshalling module has to be built: it is bound to torch's C++ interface and to this interpreter's, so it
+    is rebuilt when either has been exchanged, whatever the files' times say."""
+    return _stale(MARSHAL, deps) or not os.path.exists(MARSHAL_FOR) or open(MARSHAL_FOR).read() != _marshal_for()
+
+
+def _marshal_for() -> str:
+    import torch
+
+    return f"torch {torch.__version__} {os.path.dirname(torch.__file__)}, Python {sys.version}, {platform.machine()}\n"
+
+
 def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -68,7 +82,7 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = Fa
             jobs.append(cmd)
 
     marshal = f"{MARSHAL}.tmp{os.getpid()}"
-    remake = force or _stale(MARSHAL, [os.path.join(CSRC, "kda_marshal.cpp"), headers[-1]])
+    remake = force or _marshal_stale([os.path.join(CSRC, "kda_marshal.cpp"), headers[-1]])
     compiled = list(jobs)
     if remake:
         jobs.append(_marshal_command(marshal))
@@ -85,6 +99,8 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_v: bool = Fa
                 raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-1]}")
     if remake:
         os.replace(marshal, MARSHAL)
+        with open(MARSHAL_FOR, "w") as f:
+            f.write(_marshal_for())
     if force or compiled or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
