@@ -115,7 +115,9 @@ __device__ __forceinline__ bool offsets_within(const int32_t* __restrict__ cu, i
   return !__syncthreads_or(bad);
 }
 
-// Tokens of a request: its tiles take some 0.2 s of a CTA, and a role may wait for another one that long, out of half a second.
+// Tokens of a request: its tiles take some 0.2 s of a CTA of the kernel for many rows, and a role may wait for another one that
+// long, out of half a second.  (The kernel for few rows has no such wait, but sizes decide between the two, and a request
+// is not to be refused by one and answered by the other.)
 constexpr int kMaxLength = 1 << 24;
 // A tile of rows of one request and key head.
 struct Tile {

@@ -99,8 +99,8 @@ __device__ __forceinline__ void tma_prefetch_box(const CUtensorMap* map, int x, 
                "r"(block)
                : "memory");
 }
-// Waits of a whole warp (branches are on votes, so that it stays together), with a limit of about a second, or none at
-// all in the variant that gives up.  hold() leaves the waiting to the hardware; poll() is for the MMA warp, which all
+// Waits of a whole warp (branches are on votes, so that it stays together), with a limit of half a second to a second, or
+// none at all in the variant that gives up.  hold() leaves the waiting to the hardware; poll() is for the MMA warp, which all
 // others wait for (a suspended warp comes back some hundreds of clocks late).  Both are kept small: they are inlined many
 // times, and the warps' loops share an instruction cache.
 struct Waiter {

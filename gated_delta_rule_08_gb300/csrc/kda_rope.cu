@@ -4,8 +4,9 @@
 //
 // A position times a frequency has more whole turns than fp32 can hold fractions of, so the angle is taken in
 // fixed point: F = f / (2 pi) 2^64 modulo 2^64 once for each pair, and pos F modulo 2^64, which wraps at whole turns by
-// itself.  Its top 32 bits, as a signed fraction of a turn, go to sincospi.  That is exact to 2^-31 of a turn for every
-// 32-bit position.
+// itself.  Its top 32 bits, as a signed fraction of a turn, are rounded to fp32 and go to sincospi.  The angle is then off by
+// 2^-26 of a turn for that rounding, 2^-32 for the bits below and (|f| + 1) |pos| 2^-64 for F's: less than 2^-25 in all
+// for frequencies up to 64 and every 32-bit position.
 //
 // A warp has a token (for few tokens a part of its heads), each lane a unit of 16 values of a head (two pieces of 16
 // bytes in bf16): eight pairs, or 16 values to copy, the same ones in every head.  A lane makes the cosines and sines of

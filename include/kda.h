@@ -49,7 +49,7 @@
  *     whose bounded waits on work of their own CTA give up at once, so that a test can make them run
  *     out and see KDA_DEVERR_WAIT_TIMEOUT reported with the device left usable.  With the value
  *     "stall" kda_matmul_fp8, kda_linear_chunk_fwd and the attentions launch variants whose first CTA starts no work,
- *     so that its waits run out at their limit, about a second.  Not for production use.
+ *     so that its waits run out at their limit, half a second to a second.  Not for production use.
  */
 #ifndef KDA_H_
 #define KDA_H_
@@ -351,11 +351,12 @@ kda_status kda_block_tables(const int32_t* counts, const int32_t* lengths, int32
 
 /* Rotary positions with one or several axes, and the cache's write.  For pair i of a head's first rot values
  *   angle = positions[axis[i]][t] * inv_freq[i],  (a, b) -> (a cos - b sin, b cos + a sin)
- * the pair being values i and i + rot / 2, or 2 i and 2 i + 1 if interleaved; values from rot on are left.  The
- * angle is reduced exactly (in 64-bit fixed point), so positions may be as far as int32 goes, and negative.
+ * the pair being values i and i + rot / 2, or 2 i and 2 i + 1 if interleaved; values from rot on are left.  Whole
+ * turns are taken off in 64-bit fixed point, so positions may be as far as int32 goes, and negative: the angle is off by
+ * less than 2^-25 of a turn for |inv_freq| up to 64, beyond that by |inv_freq * position| 2^-64 turns more.
  *   q, k, v   : [T, H, d], [T, Hkv, d], [T, Hkv, d] (dtype), a token's heads dense, tokens q_stride / k_stride /
  *               v_stride elements apart (as in kda_linear_chunk_fwd)
- *   inv_freq  : [rot / 2] fp64, radians for each position;  axis: [rot / 2] int32 in [0, axes), or NULL (all 0)
+ *   inv_freq  : [rot / 2] fp64, finite, radians for each position;  axis: [rot / 2] int32 in [0, axes), or NULL (all 0)
  *   positions : [axes, T] int32
  *   slot_map  : [T] int32, as from kda_block_tables: token t's keys and values go to slot slot_map[t].  A token with -1 is
  *               skipped whole (its row of q_out too); other slots outside the cache set KDA_DEVERR_BAD_SLOT and are
@@ -376,8 +377,9 @@ kda_status kda_rope_append(const void* q, const void* k, const void* v, const do
  *   lengths      : [N] int32, tokens of request n in the cache, its new ones included
  *   cu_seqlens   : [N + 1] int32, where each request's new tokens begin in q; they are its last ones.  Offsets that do not
  *                  rise from 0 to at most T set KDA_DEVERR_BAD_SEQLENS, and nothing is written; a request of more new
- *                  tokens than its length, or longer than max_blocks * block_size or 2^24, sets it and is skipped.  Rows of
- *                  out behind the last request are left as they were
+ *                  tokens than its length, or longer than max_blocks * block_size or 2^24, sets it and is skipped (in all
+ *                  three calls alike, whichever kernel their sizes lead to).  Rows of out behind the last request are
+ *                  left as they were
  *   window       : tokens a token sees, itself included; 0 means all.  sinks >= 0: first tokens that stay visible
  *   max_length   : no request is longer (a hint for how the work is split; 0: as long as the tables allow)
  *   out          : [T, H, d] bf16, dense; must not overlap an input
