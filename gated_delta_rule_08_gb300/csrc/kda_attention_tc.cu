@@ -726,9 +726,11 @@ attention_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Q
           if (!ok) break;
           ++tiles;
           uint8_t* st = sm + L::kRing + s * L::kTile;
+          // (lane g looks at group g)
+          const int base = group_key(it.span, j, lane & 7, box_shift);
+          const uint32_t seen = used16<SPLIT>(p, it.t, it.span, named, base < 0 ? 0 : base), keeps = base < 0 ? 0u : seen;
           for (int g = 0; g < 8; ++g) {
-            const int base = group_key(it.span, j, g, box_shift);
-            const uint32_t keep = base < 0 ? 0u : used16<SPLIT>(p, it.t, it.span, named, base);
+            const uint32_t keep = __shfl_sync(0xffffffffu, keeps, g);
             if (keep == 0xffffu) continue;
             for (int i = lane; i < 16 * 8 * L::kParts; i += 32) {
               const int r = i & 15, c = i >> 4;
