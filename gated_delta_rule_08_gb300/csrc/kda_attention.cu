@@ -117,19 +117,24 @@ attention_rows_kernel(const __grid_constant__ Maps maps, const Params p) {
   auto block_ids = [&](int i) {
     const int at = 32 * i + lane;
     int id = 0, key = 0;
+    auto check = [&](bool used) {  // by some row
+      if (used && (unsigned)id < (unsigned)p.num_blocks) return;
+      if (used) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
+      id = p.num_blocks;  // reads as zeros
+    };
     if (at < count) {
       key = box_key(span, box0 + warp + at * kWarps, kBoxShift);
       id = table[key >> p.shift];
+      if (!TREES) check(true);  // (here: below, with the trees', a single token over 8000 keys takes 15.6 us instead of 14.5)
     }
-    bool used = true;  // by some row
-    if (TREES && __any_sync(0xffffffffu, at < count && key + kBox > t.before)) {
-      if (!drafted) named = named_by(p, t, token0, token1);
-      drafted = true;
-      used = used16<TREES>(p, t, span, named, key) != 0;
-    }
-    if (at < count && (!used || (unsigned)id >= (unsigned)p.num_blocks)) {
-      if (used) atomicOr(p.err, KDA_DEVERR_BAD_SLOT);
-      id = p.num_blocks;  // reads as zeros
+    if (TREES) {
+      bool used = true;
+      if (__any_sync(0xffffffffu, at < count && key + kBox > t.before)) {
+        if (!drafted) named = named_by(p, t, token0, token1);
+        drafted = true;
+        used = used16<TREES>(p, t, span, named, key) != 0;
+      }
+      if (at < count) check(used);
     }
     return id;
   };
