@@ -17,6 +17,9 @@
 // that some row does not see look at masks.  Values that no row sees may be anything (unwritten memory, NaN) and meet
 // weights of 0: a warp of its own clears them before such a tile is multiplied.
 //
+// Roles wait for phases of barriers by parity, so no phase may complete before all that wait for the one before it have
+// seen that.  Rings and hand-overs that are answered see to it by themselves; `unclear` and `o_done` are told where it has to be.
+//
 // Warps: 0-3 and 4-7 softmax of the halves, 8 copies, 9 and 10 the halves' MMAs, 11 clears.  The two MMA warps take turns
 // at the tensor cores (without turns both halves fall into step, and softmax and products no longer overlap: 2.2 ms
 // instead of 1.5 for the first case below), and each passes its turn on before its QK, because that takes
@@ -24,9 +27,9 @@
 // copy warp looks up ahead and hands to the others; few items, and trees: a cluster of CTAs shares the keys of one and joins through distributed
 // shared memory, cut by the request's own length, the longest first.
 //
-// Measured on GB300 (bf16, 32 heads of 8 key heads, d = 128): 16384 tokens, all keys: 1.54 ms by itself (1.41
+// Measured on GB300 (bf16, 32 heads of 8 key heads, d = 128): 16384 tokens, all keys: 1.57 ms by itself (1.38
 // PFLOP/s of the pairs a token sees; 1.62 ms once the power limit takes hold); 8192 tokens, a window of 1024 and 4 sinks:
-// 144 us (0.89 PFLOP/s); 32 trees of 64 drafted tokens over 500 to 16000: 185 us (3.5 TB/s).  Five parts of prompts, up to
+// 145 us (0.88 PFLOP/s); 32 trees of 64 drafted tokens over 500 to 16000: 185 us (3.5 TB/s).  Five parts of prompts, up to
 // 2000 tokens over 9000, 20 heads of 4, d = 64, a window of 4096: 105 us.
 // Bound in long prompts by a half's chain from scores to scores: softmax 1250 clocks (of them 700 exponentials, rounding and
 // stores), PV 500 to 600, QK 650 to 700, two hand-overs of 150; the tensor cores are busy for 2300 of the 2800 clocks that

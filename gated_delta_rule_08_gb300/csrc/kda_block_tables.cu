@@ -12,7 +12,7 @@
 // read and written are different ones.
 //
 // Bound by latency (launch, the loads of counts and lengths, the running sums, then ring and table).  Measured on GB300:
-// 256 requests of one token 6.4 us, 1000 requests with 39494 tokens in all 10.4 us (a cluster of 8: 12.5).
+// 256 requests of one token 6.3 us, 1000 requests with 39494 tokens in all 10.3 us (a cluster of 8: 12.5).
 #include "kda_device.cuh"
 #include "kda_internal.h"
 #include "tc_ptx.cuh"

@@ -16,7 +16,7 @@
 //
 // Bound by HBM for many tokens: every value read once and written once.  Measured on GB300: 16384 tokens of 32 + 2 x 8
 // heads of 128 in bf16, three axes: 65 us, 6.2 TB/s (91 % of the measured copy; by blocks of four tokens with the cosines in
-// shared memory: 102 us); one token 4.6 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 5.7 us (latency).
+// shared memory: 102 us); one token 4.3 us, 1237 fp32 tokens of 12 + 2 x 4 heads of 64: 5.1 us (latency).
 #include "kda_device.cuh"
 #include "kda_internal.h"
 #include "tc_ptx.cuh"

@@ -409,7 +409,9 @@ kda_status kda_window_attention_decode_step(const void* q, const void* k_cache, 
  *               request (its ancestors and itself; the mask alone decides); a request drafts at most 64 * mask_words
  *               tokens (KDA_DEVERR_BAD_COUNT, and it is skipped).  Bits past a request's drafted tokens are ignored
  * A token whose mask names m drafted tokens stands at position before + m - 1 and sees, of the tokens before the drafted
- * ones, what kda_window_attention_fwd shows it there.  A token that sees nothing gets zeros.
+ * ones, what kda_window_attention_fwd shows it there.  A token that sees nothing gets zeros.  Drafted tokens that no mask
+ * names (padding) may hold anything, as what lies elsewhere in the cache may.  kda_block_tables takes back a request's last
+ * tokens: accepted tokens that are not the first drafted ones have to be taken back and run again.
  * mask_words 1 to 16; tree_mask 8-byte aligned.  All else as for kda_window_attention_fwd. */
 kda_status kda_tree_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                               const int32_t* lengths, const int32_t* cu_seqlens, const uint64_t* tree_mask, int mask_words,
